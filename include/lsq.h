@@ -319,6 +319,114 @@ lsq_status lsq_decode_run(lsq_state* st, int32_t H, const float* q, const float*
 lsq_status lsq_prefill(lsq_state* st, int32_t T, const float* k, const float* v,
                        const float* alpha, const float* beta, void* stream);
 
+/* ---- Slots: a serving program's states, addressed by sequence ----
+ *
+ * A handle's batch axis is a pool of sequences: slot b is heads [b*heads,
+ * (b+1)*heads) of the state buffers.  The four calls below work on chosen
+ * slots: a packed batch of prompts (lsq_attend), one token each
+ * (lsq_step_slots), and copies between an fp32 handle and a quantised one
+ * (lsq_state_store_slots, lsq_state_load_slots: a state cache).  Slot numbers
+ * and sequence offsets are device data, so a captured launch may be replayed
+ * with other slots; the host does not see them and the kernels check them:
+ *   - a negative slot marks a padded entry: nothing of it is read or written
+ *     (its output rows stay as they were);
+ *   - a slot >= batch, or one that an earlier entry of the same call already
+ *     names, is refused on the device: no state is touched and the entry's
+ *     output rows are filled with NaN (a copy of slots leaves the destination
+ *     as it was).  The first entry that names a slot is carried out.
+ * Token inputs use LSQ_IO_* types for q, k, v and o; alpha and beta are fp32.
+ */
+typedef enum { LSQ_IO_F32 = 0, LSQ_IO_F16 = 1, LSQ_IO_BF16 = 2 } lsq_io_type;
+
+/* A packed batch of tokens.  Token t of q and k holds qk_heads vectors of dk
+ * elements, of v and o heads vectors of dv elements, contiguous within the
+ * token; consecutive tokens are q_stride, ... elements apart (a slice of a
+ * wider projection, or 0 for an input that all tokens share).  Value head h
+ * reads q and k of head h / (heads / qk_heads).  alpha is [tokens][heads], or
+ * [tokens][heads][dk] under a diagonal decay, and beta [tokens][heads], both
+ * contiguous.  Sequence i owns tokens [cu_seqlens[i], cu_seqlens[i+1]) and
+ * slot slots[i]; tokens outside every sequence are neither read nor written.
+ * Offsets are clamped to [0, tokens] and a decreasing pair is an empty
+ * sequence.  fresh[i] != 0 starts sequence i from S = 0 instead of its slot's
+ * state (whose old contents, even NaN, do not matter).  An empty sequence
+ * leaves its slot as it was. */
+typedef struct {
+  int32_t io;                 /* lsq_io_type of q, k, v and o */
+  int32_t qk_heads;           /* heads of q and k; divides the handle's heads */
+  int32_t seqs;               /* sequences (entries) */
+  int64_t tokens;             /* rows of q, k, v, alpha, beta and o */
+  int64_t q_stride, k_stride, v_stride, o_stride;   /* elements from one token to the next */
+  const void* q;
+  const void* k;
+  const void* v;
+  const float* alpha;
+  const float* beta;
+  void* o;
+  const int32_t* cu_seqlens;  /* [seqs + 1]; not read by lsq_step_slots */
+  const int32_t* slots;       /* [seqs], or NULL: entry i is slot i */
+  const uint8_t* fresh;       /* [seqs], or NULL: none is fresh */
+} lsq_token_batch;
+
+/* Bytes of workspace lsq_attend needs for this batch (0 when it needs none).
+ * Host only; depends on the handle's configuration, io, qk_heads, seqs and
+ * tokens alone. */
+lsq_status lsq_attend_workspace(const lsq_state* st, const lsq_token_batch* batch, size_t* bytes);
+
+/* Linear attention over a packed batch of prompts, with outputs: for every
+ * sequence the recurrence of Eq. (1) of "LinQuant: Functional Invariances for
+ * Low-Precision Linear Recurrences" (Theoretical Foundation) from its slot's
+ * state (or 0), o_t = S_t q_t for every token, and the final state back to
+ * the slot.  The handle is an fp32 one (bits 32).  With a scalar decay and
+ * the linear write (delta 0) the tokens are taken in chunks on the matrix
+ * cores, as in that page's chunkwise realisation (Methodology) without its
+ * INT8 operands: states and sums are fp32, operands are split so that the
+ * state keeps fp32 accuracy.  A diagonal decay or the delta rule walks the
+ * tokens one by one with the state in registers.  alpha lies in [0, 1] (0
+ * forgets everything before the token); a negative or NaN alpha gives NaN.
+ * A long sequence is taken in segments whose states pass through the
+ * workspace; the same batch gives the same bits on every call.
+ *
+ * q, k (and a diagonal alpha): 16-byte aligned, their token strides a
+ * multiple of 16 bytes; v, o, alpha and beta element-aligned (wide accesses
+ * are used where their addresses allow).  o must not overlap an input.  The
+ * workspace is device memory, 16-byte aligned, used by this call alone until
+ * the stream has passed it (two captured graphs that may run at once need two).
+ * The step index does not move.  INVALID_ARG: null or misaligned pointers,
+ * seqs < 0, tokens < 0, qk_heads not dividing heads, an o_stride below
+ * heads * dv or a negative stride, a workspace of NULL where one is needed;
+ * BUFFER_TOO_SMALL: a smaller workspace; UNSUPPORTED: a quantised handle, or
+ * more than 2^31 - 1 workgroups. */
+lsq_status lsq_attend(lsq_state* st, const lsq_token_batch* batch, void* workspace,
+                      size_t workspace_bytes, void* stream);
+
+/* The recurrent form: one token for every entry (tokens == seqs, token i is
+ * entry i's; cu_seqlens is not read).  fp32 handle, either decay, either
+ * delta.  The arithmetic is the fp32 step's: S' = fl(alpha_c S), w = fl(beta
+ * fl(v - delta S'.k)), S = fma(w, k_c, S'), o = S.q rounded once to the io
+ * type.  The step index does not move.  Errors as lsq_attend. */
+lsq_status lsq_step_slots(lsq_state* st, const lsq_token_batch* batch, void* stream);
+
+/* Quantise slots of an fp32 handle into slots of a quantised one: entry i
+ * takes slot src_slots[i] of src to slot dst_slots[i] of dst (either array
+ * NULL: entry i is slot i), with the scales and codes of
+ * lsq_state_calibrate, in dst's group format (the yoked reference is copied
+ * too).  Only dst's slots are checked for repetition: one state may go to
+ * many pages.  dst's calibrated flag does not move: a persistent handle whose
+ * slots are all filled this way is declared with lsq_state_set_calibrated.
+ * INVALID_ARG: null handles, a negative count, handles of different heads,
+ * dk or dv; UNSUPPORTED: src not fp32, dst not quantised or with a bypass
+ * (its buffer belongs to one step index for all slots). */
+lsq_status lsq_state_store_slots(lsq_state* dst, const lsq_state* src, int32_t count,
+                                 const int32_t* dst_slots, const int32_t* src_slots,
+                                 void* stream);
+
+/* The reverse: slots of a quantised handle read back into slots of an fp32
+ * one, S = fl(C s) as lsq_state_dequantize gives it.  Checks and errors as
+ * lsq_state_store_slots with the handles' roles exchanged. */
+lsq_status lsq_state_load_slots(lsq_state* dst, const lsq_state* src, int32_t count,
+                                const int32_t* dst_slots, const int32_t* src_slots,
+                                void* stream);
+
 /* Static description of a status code. */
 const char* lsq_status_string(lsq_status s);
 

@@ -33,6 +33,14 @@ class lsq_buffers(ctypes.Structure):
                 ("lrb", ctypes.c_void_p), ("lrb_bytes", ctypes.c_size_t)]
 
 
+class lsq_token_batch(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("io", "qk_heads", "seqs")] +
+                [(n, ctypes.c_int64) for n in ("tokens", "q_stride", "k_stride", "v_stride",
+                                               "o_stride")] +
+                [(n, ctypes.c_void_p) for n in ("q", "k", "v", "alpha", "beta", "o", "cu_seqlens",
+                                                "slots", "fresh")])
+
+
 class LsqError(RuntimeError):
     def __init__(self, status: int, where: str, detail: str):
         self.status = status
@@ -53,6 +61,7 @@ def load() -> ctypes.CDLL:
     L = ctypes.CDLL(LIB_PATH)
     P, S = ctypes.c_void_p, ctypes.c_size_t
     cfgp = ctypes.POINTER(lsq_config)
+    batchp = ctypes.POINTER(lsq_token_batch)
     sig = {
         "lsq_state_sizes": [cfgp, ctypes.POINTER(S), ctypes.POINTER(S), ctypes.POINTER(S),
                             ctypes.POINTER(S), ctypes.POINTER(S)],
@@ -68,6 +77,11 @@ def load() -> ctypes.CDLL:
         "lsq_decode_step": [P, P, P, P, P, P, P, P, P],
         "lsq_decode_run": [P, ctypes.c_int32, P, P, P, P, P, P, P, P],
         "lsq_prefill": [P, ctypes.c_int32, P, P, P, P, P],
+        "lsq_attend_workspace": [P, batchp, ctypes.POINTER(S)],
+        "lsq_attend": [P, batchp, P, S, P],
+        "lsq_step_slots": [P, batchp, P],
+        "lsq_state_store_slots": [P, P, ctypes.c_int32, P, P, P],
+        "lsq_state_load_slots": [P, P, ctypes.c_int32, P, P, P],
         "lsq_status_string": [ctypes.c_int],
         "lsq_last_error": [],
         "lsq_version": [],

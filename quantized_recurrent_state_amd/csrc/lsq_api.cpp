@@ -11,6 +11,7 @@
 #include "lsq.h"
 #include "lsq_internal.h"
 #include "lsq_probe.h"
+#include "lsq_slots.h"
 
 struct lsq_state {
   lsq_config cfg;
@@ -241,6 +242,108 @@ lsq_status launch_one_step(lsq_state* st, const float* q, const float* k, const 
   lsq_status s = hip_status(e, "decode-step launch");
   if (s == LSQ_OK) ++st->step;
   return s;
+}
+
+size_t io_bytes(int32_t io) { return io == LSQ_IO_F32 ? 4 : 2; }
+
+bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+// Checks of a token batch over an fp32 handle that need no device; `one` for
+// one token per entry (no offsets to read).
+lsq_status check_batch(const lsq_state* st, const lsq_token_batch* b) {
+  if (!st) return fail(LSQ_ERR_INVALID_ARG, "state is null");
+  if (!b) return fail(LSQ_ERR_INVALID_ARG, "batch is null");
+  if (st->cfg.bits != 32)
+    return fail(LSQ_ERR_UNSUPPORTED, "token batches run on an fp32 handle (bits 32)");
+  if (b->io != LSQ_IO_F32 && b->io != LSQ_IO_F16 && b->io != LSQ_IO_BF16)
+    return fail(LSQ_ERR_INVALID_ARG, "io must be F32, F16 or BF16");
+  if (b->seqs < 0 || b->tokens < 0) return fail(LSQ_ERR_INVALID_ARG, "negative seqs or tokens");
+  if (b->qk_heads < 0 || (b->qk_heads == 0 && st->cfg.heads > 0) ||
+      (b->qk_heads > 0 && st->cfg.heads % b->qk_heads != 0))
+    return fail(LSQ_ERR_INVALID_ARG, "qk_heads %d must divide heads %d", b->qk_heads, st->cfg.heads);
+  if (b->q_stride < 0 || b->k_stride < 0 || b->v_stride < 0)
+    return fail(LSQ_ERR_INVALID_ARG, "negative token stride");
+  if (b->o_stride < (int64_t)st->cfg.heads * st->cfg.dv)
+    return fail(LSQ_ERR_INVALID_ARG, "o_stride must be at least heads * dv");
+  return ok();
+}
+
+bool empty_batch(const lsq_state* st, const lsq_token_batch* b) {
+  return n_heads(st->cfg) == 0 || b->seqs == 0 || b->tokens == 0;
+}
+
+lsq_status check_batch_ptrs(const lsq_state* st, const lsq_token_batch* b) {
+  const size_t e = io_bytes(b->io);
+  if (!b->q || !b->k || !b->v || !b->alpha || !b->beta || !b->o)
+    return fail(LSQ_ERR_INVALID_ARG, "q, k, v, alpha, beta and o must be non-null");
+  if (!aligned16(b->q) || !aligned16(b->k) || (b->q_stride * e) % 16 || (b->k_stride * e) % 16)
+    return fail(LSQ_ERR_INVALID_ARG, "q and k must be 16-byte aligned, their token strides a multiple of 16 bytes");
+  if (!aligned_to(b->v, e) || !aligned_to(b->o, e) || !aligned4(b->beta) || !aligned4(b->alpha))
+    return fail(LSQ_ERR_INVALID_ARG, "v, o, alpha and beta must be aligned to their elements");
+  if (st->cfg.decay == LSQ_DECAY_DIAG && !aligned16(b->alpha))
+    return fail(LSQ_ERR_INVALID_ARG, "a diagonal alpha must be 16-byte aligned");
+  if (!aligned4(b->slots) || !aligned4(b->cu_seqlens))
+    return fail(LSQ_ERR_INVALID_ARG, "slots and cu_seqlens must be 4-byte aligned");
+  if (!b->slots && b->seqs > st->cfg.batch)
+    return fail(LSQ_ERR_INVALID_ARG, "%d entries without slots on a handle of %d", b->seqs, st->cfg.batch);
+  return ok();
+}
+
+lsq::SlotArgs slot_args(const lsq_state* st, const lsq_token_batch* b) {
+  lsq::SlotArgs a{};
+  a.S = st->f32;
+  a.q = b->q; a.k = b->k; a.v = b->v; a.alpha = b->alpha; a.beta = b->beta; a.o = b->o;
+  a.cu = b->cu_seqlens; a.slots = b->slots; a.fresh = b->fresh;
+  a.q_stride = b->q_stride; a.k_stride = b->k_stride; a.v_stride = b->v_stride;
+  a.o_stride = b->o_stride;
+  a.tokens = b->tokens;
+  a.seqs = b->seqs; a.nslots = st->cfg.batch; a.heads = st->cfg.heads;
+  a.share = st->cfg.heads / b->qk_heads;
+  a.dv = st->cfg.dv;
+  return a;
+}
+
+lsq_status slot_status(hipError_t e, const char* what) {
+  if (e == hipErrorInvalidConfiguration)
+    return fail(LSQ_ERR_UNSUPPORTED, "%s: too many workgroups for one launch", what);
+  return hip_status(e, what);
+}
+
+// Store (fp32 -> quantised) and load (quantised -> fp32) of slots.
+lsq_status copy_slots(const lsq_state* f, const lsq_state* q, bool store, int32_t count,
+                      const int32_t* dst_slots, const int32_t* src_slots, void* stream) {
+  const char* what = store ? "store_slots" : "load_slots";
+  if (!f || !q) return fail(LSQ_ERR_INVALID_ARG, "state is null");
+  if (count < 0) return fail(LSQ_ERR_INVALID_ARG, "negative count");
+  const lsq_config &cf = f->cfg, &cq = q->cfg;
+  if (cf.bits != 32 || cq.bits == 32)
+    return fail(LSQ_ERR_UNSUPPORTED, "%s copies between an fp32 handle and a quantised one", what);
+  if (cq.lrb_rank != 0) return fail(LSQ_ERR_UNSUPPORTED, "%s does not take the bypass", what);
+  if (cf.heads != cq.heads || cf.dk != cq.dk || cf.dv != cq.dv)
+    return fail(LSQ_ERR_INVALID_ARG, "%s: the handles differ in heads, dk or dv", what);
+  const int32_t dst_n = store ? cq.batch : cf.batch, src_n = store ? cf.batch : cq.batch;
+  if (!aligned4(dst_slots) || !aligned4(src_slots))
+    return fail(LSQ_ERR_INVALID_ARG, "slots must be 4-byte aligned");
+  if ((!dst_slots && count > dst_n) || (!src_slots && count > src_n))
+    return fail(LSQ_ERR_INVALID_ARG, "%s: %d entries without slots on a smaller handle", what, count);
+  if (count == 0 || n_heads(cf) == 0 || n_heads(cq) == 0) return ok();
+  lsq::CopyArgs a{};
+  a.S = f->f32;
+  a.codes = static_cast<uint8_t*>(q->codes);
+  a.scales = q->scales;
+  a.ref = cq.policy == LSQ_POLICY_YOKED ? q->ref : nullptr;
+  a.dst_slots = dst_slots;
+  a.src_slots = src_slots;
+  a.count = count;
+  a.dst_n = dst_n;
+  a.src_n = src_n;
+  a.heads = cq.heads;
+  a.dv = cq.dv;
+  a.group = cq.group;
+  a.sfmt = cq.scale_fmt;
+  hipStream_t hs = static_cast<hipStream_t>(stream);
+  return slot_status(store ? lsq::launch_store_slots(a, cq.bits, cq.dk, hs)
+                           : lsq::launch_load_slots(a, cq.bits, cq.dk, hs), what);
 }
 
 }  // namespace
@@ -480,6 +583,53 @@ lsq_status lsq_prefill(lsq_state* st, int32_t T, const float* k, const float* v,
   if (e != hipSuccess) return hip_status(e, "prefill launch");
   st->step += T;
   return ok();
+}
+
+lsq_status lsq_attend_workspace(const lsq_state* st, const lsq_token_batch* batch, size_t* bytes) {
+  lsq_status s = check_batch(st, batch);
+  if (s != LSQ_OK) return s;
+  if (!bytes) return fail(LSQ_ERR_INVALID_ARG, "bytes is null");
+  *bytes = 0;
+  return ok();
+}
+
+lsq_status lsq_attend(lsq_state* st, const lsq_token_batch* batch, void* workspace,
+                      size_t workspace_bytes, void* stream) {
+  lsq_status s = check_batch(st, batch);
+  if (s != LSQ_OK) return s;
+  if (empty_batch(st, batch)) return ok();
+  if (!batch->cu_seqlens) return fail(LSQ_ERR_INVALID_ARG, "cu_seqlens is null");
+  s = check_batch_ptrs(st, batch);
+  if (s != LSQ_OK) return s;
+  const lsq_config& c = st->cfg;
+  return slot_status(lsq::launch_walk(slot_args(st, batch), batch->io, c.dk, c.delta,
+                                      c.decay == LSQ_DECAY_DIAG, static_cast<hipStream_t>(stream)),
+                     "attend launch");
+}
+
+lsq_status lsq_step_slots(lsq_state* st, const lsq_token_batch* batch, void* stream) {
+  lsq_status s = check_batch(st, batch);
+  if (s != LSQ_OK) return s;
+  if (batch->tokens != batch->seqs)
+    return fail(LSQ_ERR_INVALID_ARG, "step_slots takes one token per entry (tokens == seqs)");
+  if (empty_batch(st, batch)) return ok();
+  s = check_batch_ptrs(st, batch);
+  if (s != LSQ_OK) return s;
+  const lsq_config& c = st->cfg;
+  lsq::SlotArgs a = slot_args(st, batch);
+  a.cu = nullptr;
+  return slot_status(lsq::launch_walk(a, batch->io, c.dk, c.delta, c.decay == LSQ_DECAY_DIAG,
+                                      static_cast<hipStream_t>(stream)), "step_slots launch");
+}
+
+lsq_status lsq_state_store_slots(lsq_state* dst, const lsq_state* src, int32_t count,
+                                 const int32_t* dst_slots, const int32_t* src_slots, void* stream) {
+  return copy_slots(src, dst, true, count, dst_slots, src_slots, stream);
+}
+
+lsq_status lsq_state_load_slots(lsq_state* dst, const lsq_state* src, int32_t count,
+                                const int32_t* dst_slots, const int32_t* src_slots, void* stream) {
+  return copy_slots(dst, src, false, count, dst_slots, src_slots, stream);
 }
 
 lsq_status lsq_probe_stream(int32_t kind, const void* src, void* dst, size_t bytes,
