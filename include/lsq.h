@@ -346,8 +346,9 @@ typedef enum { LSQ_IO_F32 = 0, LSQ_IO_F16 = 1, LSQ_IO_BF16 = 2 } lsq_io_type;
  * [tokens][heads][dk] under a diagonal decay, and beta [tokens][heads], both
  * contiguous.  Sequence i owns tokens [cu_seqlens[i], cu_seqlens[i+1]) and
  * slot slots[i]; tokens outside every sequence are neither read nor written.
- * Offsets are clamped to [0, tokens] and a decreasing pair is an empty
- * sequence.  fresh[i] != 0 starts sequence i from S = 0 instead of its slot's
+ * Offsets must not decrease and lie in [0, tokens]; others are clamped, so
+ * that nothing outside the batch is touched, and their sequences' values are
+ * unspecified.  fresh[i] != 0 starts sequence i from S = 0 instead of its slot's
  * state (whose old contents, even NaN, do not matter).  An empty sequence
  * leaves its slot as it was. */
 typedef struct {

@@ -309,6 +309,9 @@ lsq_status slot_status(hipError_t e, const char* what) {
   return hip_status(e, what);
 }
 
+// A scalar decay and the linear write run in chunks; the rest token by token.
+bool chunked(const lsq_config& c) { return c.decay == LSQ_DECAY_SCALAR && c.delta == 0; }
+
 // Store (fp32 -> quantised) and load (quantised -> fp32) of slots.
 lsq_status copy_slots(const lsq_state* f, const lsq_state* q, bool store, int32_t count,
                       const int32_t* dst_slots, const int32_t* src_slots, void* stream) {
@@ -589,7 +592,10 @@ lsq_status lsq_attend_workspace(const lsq_state* st, const lsq_token_batch* batc
   lsq_status s = check_batch(st, batch);
   if (s != LSQ_OK) return s;
   if (!bytes) return fail(LSQ_ERR_INVALID_ARG, "bytes is null");
-  *bytes = 0;
+  const lsq_config& c = st->cfg;
+  *bytes = empty_batch(st, batch) || !chunked(c)
+               ? 0
+               : lsq::attend_plan(batch->tokens, batch->seqs, c.heads, c.dk, c.dv).workspace;
   return ok();
 }
 
@@ -602,9 +608,29 @@ lsq_status lsq_attend(lsq_state* st, const lsq_token_batch* batch, void* workspa
   s = check_batch_ptrs(st, batch);
   if (s != LSQ_OK) return s;
   const lsq_config& c = st->cfg;
-  return slot_status(lsq::launch_walk(slot_args(st, batch), batch->io, c.dk, c.delta,
-                                      c.decay == LSQ_DECAY_DIAG, static_cast<hipStream_t>(stream)),
-                     "attend launch");
+  hipStream_t hs = static_cast<hipStream_t>(stream);
+  if (!chunked(c))
+    return slot_status(lsq::launch_walk(slot_args(st, batch), batch->io, c.dk, c.delta,
+                                        c.decay == LSQ_DECAY_DIAG, hs), "attend launch");
+  const lsq::AttendPlan p = lsq::attend_plan(batch->tokens, batch->seqs, c.heads, c.dk, c.dv);
+  if (p.workspace) {
+    if (!workspace || !aligned16(workspace))
+      return fail(LSQ_ERR_INVALID_ARG, "the workspace must be non-null and 16-byte aligned");
+    if (workspace_bytes < p.workspace)
+      return fail(LSQ_ERR_BUFFER_TOO_SMALL, "the workspace holds %zu bytes, needs %zu",
+                  workspace_bytes, p.workspace);
+  }
+  const int64_t e = (int64_t)io_bytes(batch->io);
+  const size_t quad = 4 * (size_t)e;           // o is written four elements at a time
+  lsq::AttendArgs a{};
+  a.s = slot_args(st, batch);
+  a.seg_len = p.seg_len;
+  a.ws = static_cast<float*>(workspace);
+  a.ws_decay = p.workspace ? reinterpret_cast<float*>(static_cast<char*>(workspace) + p.state_bytes) : nullptr;
+  a.slices = p.slices;
+  a.v_wide = aligned16(batch->v) && batch->v_stride * e % 16 == 0 && c.dv * e % 16 == 0;
+  a.o_wide = aligned_to(batch->o, quad) && batch->o_stride % 4 == 0 && c.dv % 4 == 0;
+  return slot_status(lsq::launch_attend(a, p.segments, batch->io, c.dk, hs), "attend launch");
 }
 
 lsq_status lsq_step_slots(lsq_state* st, const lsq_token_batch* batch, void* stream) {

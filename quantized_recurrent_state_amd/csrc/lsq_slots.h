@@ -28,6 +28,24 @@ struct SlotArgs {
   int32_t seqs, nslots, heads, share, dv;   // share: value heads per q/k head
 };
 
+// Chunked attention: the batch, its cut into segments and the workspace.
+struct AttendArgs {
+  SlotArgs s;
+  int64_t seg_len;         // tokens per segment, a multiple of 64; 0: whole sequences
+  float* ws;               // [segments][heads][dv][dk], then ws_decay (null without segments)
+  float* ws_decay;         // [segments][heads]
+  int32_t slices;          // value columns are taken 128 (or 64) at a time
+  int32_t v_wide, o_wide;  // 16-byte reads of v, 8- or 16-byte writes of o
+};
+
+struct AttendPlan {
+  int64_t seg_len, segments, state_bytes;
+  size_t workspace;        // bytes
+  int32_t slices;
+};
+
+AttendPlan attend_plan(int64_t tokens, int32_t seqs, int32_t heads, int32_t dk, int32_t dv);
+
 // Slots copied between an fp32 handle and a quantised one (same heads, dv, dk).
 struct CopyArgs {
   float* S;                // [S slots][heads][dv][dk]
@@ -41,6 +59,7 @@ struct CopyArgs {
 };
 
 hipError_t launch_walk(const SlotArgs& a, int io, int dk, int delta, int diag, hipStream_t s);
+hipError_t launch_attend(const AttendArgs& a, int64_t segments, int io, int dk, hipStream_t s);
 hipError_t launch_store_slots(const CopyArgs& a, int bits, int dk, hipStream_t s);
 hipError_t launch_load_slots(const CopyArgs& a, int bits, int dk, hipStream_t s);
 
