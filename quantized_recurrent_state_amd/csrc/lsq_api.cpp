@@ -595,7 +595,7 @@ lsq_status lsq_attend_workspace(const lsq_state* st, const lsq_token_batch* batc
   const lsq_config& c = st->cfg;
   *bytes = empty_batch(st, batch) || !chunked(c)
                ? 0
-               : lsq::attend_plan(batch->tokens, batch->seqs, c.heads, c.dk, c.dv).workspace;
+               : lsq::attend_plan(batch->tokens, batch->seqs, c.heads, c.dk, c.dv, batch->io).workspace;
   return ok();
 }
 
@@ -612,7 +612,7 @@ lsq_status lsq_attend(lsq_state* st, const lsq_token_batch* batch, void* workspa
   if (!chunked(c))
     return slot_status(lsq::launch_walk(slot_args(st, batch), batch->io, c.dk, c.delta,
                                         c.decay == LSQ_DECAY_DIAG, hs), "attend launch");
-  const lsq::AttendPlan p = lsq::attend_plan(batch->tokens, batch->seqs, c.heads, c.dk, c.dv);
+  const lsq::AttendPlan p = lsq::attend_plan(batch->tokens, batch->seqs, c.heads, c.dk, c.dv, batch->io);
   if (p.workspace) {
     if (!workspace || !aligned16(workspace))
       return fail(LSQ_ERR_INVALID_ARG, "the workspace must be non-null and 16-byte aligned");
@@ -621,6 +621,9 @@ lsq_status lsq_attend(lsq_state* st, const lsq_token_batch* batch, void* workspa
                   workspace_bytes, p.workspace);
   }
   const int64_t e = (int64_t)io_bytes(batch->io);
+  const int64_t far = (batch->q_stride > batch->k_stride ? batch->q_stride : batch->k_stride);
+  if ((far > batch->v_stride ? far : batch->v_stride) * e * 64 > INT32_MAX)
+    return fail(LSQ_ERR_UNSUPPORTED, "token strides above 32 MiB");   // lanes address a chunk with 32 bits
   const size_t quad = 4 * (size_t)e;           // o is written four elements at a time
   lsq::AttendArgs a{};
   a.s = slot_args(st, batch);
@@ -628,8 +631,8 @@ lsq_status lsq_attend(lsq_state* st, const lsq_token_batch* batch, void* workspa
   a.ws = static_cast<float*>(workspace);
   a.ws_decay = p.workspace ? reinterpret_cast<float*>(static_cast<char*>(workspace) + p.state_bytes) : nullptr;
   a.slices = p.slices;
-  a.v_wide = aligned16(batch->v) && batch->v_stride * e % 16 == 0 && c.dv * e % 16 == 0;
-  a.o_wide = aligned_to(batch->o, quad) && batch->o_stride % 4 == 0 && c.dv % 4 == 0;
+  a.wide = aligned16(batch->v) && batch->v_stride * e % 16 == 0 && c.dv * e % 16 == 0 &&
+           aligned_to(batch->o, quad) && batch->o_stride % 4 == 0;
   return slot_status(lsq::launch_attend(a, p.segments, batch->io, c.dk, hs), "attend launch");
 }
 

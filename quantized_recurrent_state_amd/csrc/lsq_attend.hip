@@ -28,22 +28,24 @@ namespace dev {
 
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
-// Tiling of one instance.  NW waves own 16 value columns each.
-template <int IO, int DK, int NW>
+// Tiling of one instance: four waves of CG groups of 16 value columns.
+template <int IO, int DK, int CG>
 struct Tile {
   static constexpr int NP = IO == IO_BF16 ? 1 : IO == IO_F16 ? 2 : 3;   // parts of an input
   static constexpr int NO = IO == IO_F32 ? 3 : 2;                       // parts on the output's side
   static constexpr int C = IO == IO_BF16 ? 64 : 32;                     // tokens per chunk
-  static constexpr int DV = 16 * NW, NT = 64 * NW;
+  static constexpr int NW = 4, NT = 256, DV = 16 * CG * NW;
   static constexpr int EU = IO == IO_F32 ? 4 : 8;                       // elements of a 16-byte unit
-  // LDS row pitches in elements: rows 32 bytes apart in the banks
-  static constexpr int PK = DK + 16, PV = DV + 16, PP = C + 8;
-  static constexpr int QU = (C * DK / EU + NT - 1) / NT;                // units of q (of k) per thread
-  static constexpr int VU = C * DV / EU / NT;
-  static constexpr bool QGUARD = QU * NT > C * DK / EU;
+  // LDS row pitches in elements.  k and v are read by columns, four rows of 32
+  // bytes by 16 lanes: rows 8 banks apart.  q and P are read by rows, 8 bytes of
+  // 16 rows: rows 4 banks apart.  Neither then meets in a bank.
+  static constexpr int PK = DK + 16, PV = DV + 16, PQ = DK + 8, PP = C + 8;
+  static constexpr int QU = C * DK / EU / NT, VU = C * DV / EU / NT;    // units of k (q), v per thread
 };
 
 // x as a sum of N bf16 parts, four values at a time.
@@ -51,9 +53,25 @@ template <int N>
 __device__ __forceinline__ void split4(f32x4 x, bf16x4 (&p)[N]) {
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    p[i] = __builtin_convertvector(x, bf16x4);
-    if (i + 1 < N) x = x - __builtin_convertvector(p[i], f32x4);
+    uint32_t w[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      w[h] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{x[2 * h], x[2 * h + 1]}, bf16x2));
+      if (i + 1 < N) {
+        x[2 * h] -= __uint_as_float(w[h] << 16);
+        x[2 * h + 1] -= __uint_as_float(w[h] & 0xFFFF0000u);
+      }
+    }
+    p[i] = __builtin_bit_cast(bf16x4, (uint64_t)w[1] << 32 | w[0]);
   }
+}
+
+// Four bf16 values as fp32.
+__device__ __forceinline__ f32x4 widen4(bf16x4 p) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, p);
+  const uint32_t lo = (uint32_t)b, hi = (uint32_t)(b >> 32);
+  return f32x4{__uint_as_float(lo << 16), __uint_as_float(lo & 0xFFFF0000u), __uint_as_float(hi << 16),
+               __uint_as_float(hi & 0xFFFF0000u)};
 }
 
 __device__ __forceinline__ bf16x8 join(bf16x4 a, bf16x4 b) {
@@ -72,40 +90,69 @@ __device__ __forceinline__ bf16x4 read_column4(const __bf16* p) {
                                         (__attribute__((address_space(3))) s16x4*)p));
 }
 
-// Decays of one chunk, per token.
-template <int C>
+// Decays of N tokens, by token; chunk borders are every C tokens.
+template <int N>
 struct Decays {
-  float hi[C], lo[C];      // L_t, the sum of log2(alpha) from the chunk's start
-  float beta[C];
-  float cin[C];            // c_t = 2^L_t
-  float w[C];              // (c_C / c_t) beta_t
-  float gamma;             // c_C
+  float hi[N], lo[N];      // L_t, the sum of log2(alpha) from the chunk's start
+  float beta[N];
+  float w[N];              // (c_C / c_t) beta_t
 };
 
-// One wave fills them from its lanes' tokens (alpha 1 and beta 0 behind the
-// sequence); returns L_C.
-template <int C>
-__device__ __forceinline__ double fill_decays(Decays<C>& d, float alpha, float beta, int lane) {
+// x of the lane that a DPP control names, 0 where it names none or the row is
+// masked out.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp_or_zero(double x) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = __builtin_amdgcn_update_dpp(0u, (uint32_t)b, CTRL, ROWS, 0xF, false);
+  const uint32_t hi = __builtin_amdgcn_update_dpp(0u, (uint32_t)(b >> 32), CTRL, ROWS, 0xF, false);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+
+__device__ __forceinline__ double lane_of(double x, int lane) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)b, lane);
+  const uint32_t hi = __builtin_amdgcn_readlane((uint32_t)(b >> 32), lane);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+
+// 2^x of a double, to fp32.
+__device__ __forceinline__ float exp2_of(double x) {
+  const float h = (float)x;
+  return exp2f(h) * (1.f + 0.69314718f * (float)(x - (double)h));
+}
+
+// One wave fills the decays of its 64 tokens (alpha 1 and beta 0 behind the
+// sequence) from at on; returns the lane's log2(alpha).
+template <int C, int N>
+__device__ __forceinline__ double fill_decays(Decays<N>& d, int at, float alpha, float beta, int lane) {
   double l = log2((double)alpha);
   l = l < -160.0 ? -160.0 : l;
+  const double own = l;
+  l += dpp_or_zero<0x111, 0xF>(l);               // row_shr 1, 2, 4, 8: sums within 16 lanes
+  l += dpp_or_zero<0x112, 0xF>(l);
+  l += dpp_or_zero<0x114, 0xF>(l);
+  l += dpp_or_zero<0x118, 0xF>(l);
+  l += dpp_or_zero<0x142, 0xA>(l);               // row_bcast 15 into rows 1 and 3: within 32
+  if constexpr (C == 64) l += dpp_or_zero<0x143, 0xC>(l);   // row_bcast 31 into rows 2 and 3
+  const double end = C == 64 || lane >= 32 ? lane_of(l, 63) : lane_of(l, 31);
+  const float hi = (float)l;
+  d.hi[at + lane] = hi;
+  d.lo[at + lane] = (float)(l - (double)hi);
+  d.beta[at + lane] = beta;
+  d.w[at + lane] = exp2_of(end - l) * beta;
+  return own;
+}
+
+// The first n elements of B bytes of a 16-byte unit, zeros behind them.
+template <int B>
+__device__ __forceinline__ uint4 keep_elements(uint4 x, int n) {
+  uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-  for (int o = 1; o < C; o *= 2) {
-    const double up = __shfl_up(l, o);
-    if (lane >= o) l += up;
+  for (int i = 0; i < 4; ++i) {
+    const int in = n * B - 4 * i;                // bytes of word i that stay
+    w[i] = in >= 4 ? w[i] : in <= 0 ? 0u : w[i] & 0xFFFFu;
   }
-  const double end = __shfl(l, C - 1);
-  if (lane < C) {
-    const float hi = (float)l;
-    d.hi[lane] = hi;
-    d.lo[lane] = (float)(l - (double)hi);
-    d.beta[lane] = beta;
-    d.cin[lane] = exp2f(hi) * (1.f + 0.69314718f * d.lo[lane]);
-    const double r = end - l;
-    const float rh = (float)r;
-    d.w[lane] = exp2f(rh) * (1.f + 0.69314718f * (float)(r - (double)rh)) * beta;
-    if (lane == C - 1) d.gamma = d.cin[lane];
-  }
-  return end;
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // The segment a workgroup takes: sequence i, its j-th of n segments.  With a
@@ -151,26 +198,28 @@ __device__ __forceinline__ int64_t xcd_item(int64_t b, int64_t n) {
   return x * q + (x < r ? x : r) + p;
 }
 
-// One workgroup walks the chunks of one segment of one head, 16 NW value
+// One workgroup walks the chunks of one segment of one head, 64 CG value
 // columns of it.  Per chunk: the chunk's rows (read one chunk ahead into
 // registers) go to LDS as bf16 parts; the waves share out P's lower tiles; then
-// each wave has its 16 columns of S in registers in the layout that the MFMA
+// each wave has its 16 CG columns of S in registers in the layout that the MFMA
 // both writes (S^T[dk, dv] accumulated from k^T and the scaled v) and reads (as
 // the operand of S q): the k index of an operand is only a labelling, so slots
 // 0-3 and 4-7 of a lane group g stand for rows 4 g .. and 16 + 4 g .. of a
 // 32-row step in every product.  OUT = false adds up a segment's writes alone
-// (no q, no output), for the segments behind it.
-template <int IO, int DK, int NW, bool OUT>
-__global__ __launch_bounds__(64 * NW) void attend_kernel(AttendArgs args) {
-  using T = Tile<IO, DK, NW>;
-  constexpr int NP = T::NP, NO = T::NO, C = T::C, PK = T::PK, PV = T::PV, PP = T::PP;
+// (no q, no output), for the segments behind it.  VEC: v and o by whole units
+// (else by element, for odd widths and addresses).
+template <int IO, int DK, int CG, bool VEC, bool OUT>
+__global__ __launch_bounds__(256, 2) void attend_kernel(AttendArgs args) {
+  using T = Tile<IO, DK, CG>;
+  constexpr int NP = T::NP, NO = T::NO, C = T::C, PK = T::PK, PV = T::PV, PQ = T::PQ, PP = T::PP;
+  constexpr int NT = T::NT, NW = T::NW, EU = T::EU, B = 16 / EU;   // B: bytes of an element
   constexpr int CT = C / 16, KT = DK / 16, KB = C / 32;
   const SlotArgs& a = args.s;
   __shared__ __align__(16) __bf16 kl[NP][C * PK];
   __shared__ __align__(16) __bf16 vl[NP][C * PV];
-  __shared__ __align__(16) __bf16 ql[OUT ? NP : 1][OUT ? C * PK : 8];
+  __shared__ __align__(16) __bf16 ql[OUT ? NP : 1][OUT ? C * PQ : 8];
   __shared__ __align__(16) __bf16 pl[OUT ? NO : 1][OUT ? C * PP : 8];
-  __shared__ __align__(16) Decays<C> dec[2];
+  __shared__ __align__(16) Decays<NT> d;         // a round of NT tokens
 
   const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, li = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -182,61 +231,61 @@ __global__ __launch_bounds__(64 * NW) void attend_kernel(AttendArgs args) {
   if (sg.j >= sg.n || (!OUT && sg.j == sg.n - 1)) return;
   const int slot = slot_of(a.slots, sg.i, a.nslots, lane);
   if (slot == kPadded) return;
-  const int d0 = slice * T::DV + 16 * wave;      // the wave's first value column
+  const int d0 = slice * T::DV, vcols = a.dv - d0 < T::DV ? a.dv - d0 : T::DV;   // the slice's columns
+  const int64_t hk = (int64_t)(h / a.share) * DK, hv = (int64_t)h * a.dv + d0;
   if (slot == kRefused) {
     if (OUT)
       for (int64_t t = sg.t0; t < sg.t1; ++t)
-        for (int c = tid; c < T::DV; c += T::NT)
-          if (slice * T::DV + c < a.dv)
-            store1<IO>(a.o, t * a.o_stride + (int64_t)h * a.dv + slice * T::DV + c,
-                       __uint_as_float(0x7FC00000u));
+        for (int c = tid; c < vcols; c += NT)
+          store1<IO>(a.o, t * a.o_stride + hv + c, __uint_as_float(0x7FC00000u));
     return;
   }
 
-  // ---- the chunk's rows, 16 bytes per unit
-  const int64_t hk = (int64_t)(h / a.share) * DK, hv = (int64_t)h * a.dv + slice * T::DV;
-  const int vcols = a.dv - slice * T::DV < T::DV ? a.dv - slice * T::DV : T::DV;
+  // ---- the chunk's rows, 16 bytes per unit.  Loads are unconditional (a load
+  // under a lane mask would be waited for at once): rows behind the segment
+  // read its last row, columns behind dv the last whole unit, and put_chunk
+  // clears both.
   uint4 rq[OUT ? T::QU : 1], rk[T::QU], rv[T::VU];
-  float ra = 1.f, rb = 0.f;
+  float ra, rb;
+  const uint32_t kstep = (uint32_t)a.k_stride * B, qstep = (uint32_t)a.q_stride * B, vstep = (uint32_t)a.v_stride * B;
+  auto read_decays = [&](int64_t t0) {           // one token of the round per thread
+    const int64_t t = t0 + tid < sg.t1 ? t0 + tid : sg.t1 - 1;
+    ra = a.alpha[t * a.heads + h];
+    rb = a.beta[t * a.heads + h];
+  };
   auto read_chunk = [&](int64_t t0) {
-    const int live = (int)(sg.t1 - t0 < C ? sg.t1 - t0 : C);
-    if (wave == NW - 1) {
-      ra = lane < live ? a.alpha[(t0 + lane) * a.heads + h] : 1.f;
-      rb = lane < live ? a.beta[(t0 + lane) * a.heads + h] : 0.f;
-    }
-    const uint4 zero = make_uint4(0, 0, 0, 0);
+    const int last = (int)(sg.t1 - t0 < C ? sg.t1 - t0 : C) - 1;
+    const char* kb = static_cast<const char*>(a.k) + (t0 * a.k_stride + hk) * B;
+    const char* qb = static_cast<const char*>(a.q) + (t0 * a.q_stride + hk) * B;
+    const char* vb = static_cast<const char*>(a.v) + (t0 * a.v_stride + hv) * B;
 #pragma unroll
     for (int n = 0; n < T::QU; ++n) {
-      const int u = n * T::NT + tid, row = u / (DK / T::EU), col = u % (DK / T::EU) * T::EU;
-      const bool in = row < live;
-      constexpr int B = 16 / T::EU;
-      rk[n] = in ? *reinterpret_cast<const uint4*>(static_cast<const char*>(a.k) +
-                                                   ((t0 + row) * a.k_stride + hk + col) * B) : zero;
-      if constexpr (OUT)
-        rq[n] = in ? *reinterpret_cast<const uint4*>(static_cast<const char*>(a.q) +
-                                                     ((t0 + row) * a.q_stride + hk + col) * B) : zero;
+      const int u = n * NT + tid, row = u / (DK / EU), col = u % (DK / EU) * 16;
+      const uint32_t r = row < last ? row : last;
+      rk[n] = *reinterpret_cast<const uint4*>(kb + (r * kstep + col));
+      if constexpr (OUT) rq[n] = *reinterpret_cast<const uint4*>(qb + (r * qstep + col));
     }
 #pragma unroll
     for (int n = 0; n < T::VU; ++n) {
-      const int u = n * T::NT + tid, row = u / (T::DV / T::EU), col = u % (T::DV / T::EU) * T::EU;
-      constexpr int B = 16 / T::EU;
-      const int64_t e = (t0 + row) * a.v_stride + hv + col;
-      rv[n] = zero;
-      if (row < live) {
-        if (args.v_wide) {
-          if (col < vcols) rv[n] = *reinterpret_cast<const uint4*>(static_cast<const char*>(a.v) + e * B);
-        } else {                                 // odd widths or addresses: by element
-          uint32_t w[4] = {0, 0, 0, 0};
+      const int u = n * NT + tid, row = u / (T::DV / EU), col = u % (T::DV / EU) * EU;
+      const uint32_t r = row < last ? row : last;
+      if constexpr (VEC) {
+        rv[n] = *reinterpret_cast<const uint4*>(vb + (r * vstep + (col < vcols ? col : vcols - EU) * B));
+      } else {
+        uint32_t w[EU];
 #pragma unroll
-          for (int x = 0; x < T::EU; ++x)
-            if (col + x < vcols) {
-              if constexpr (IO == IO_F32)
-                w[x] = static_cast<const uint32_t*>(a.v)[e + x];
-              else
-                w[x / 2] |= (uint32_t)static_cast<const uint16_t*>(a.v)[e + x] << (16 * (x & 1));
-            }
-          rv[n] = make_uint4(w[0], w[1], w[2], w[3]);
+        for (int x = 0; x < EU; ++x) {
+          const char* e = vb + (r * vstep + (col + x < vcols ? col + x : vcols - 1) * B);
+          if constexpr (IO == IO_F32)
+            w[x] = *reinterpret_cast<const uint32_t*>(e);
+          else
+            w[x] = *reinterpret_cast<const uint16_t*>(e);
         }
+        if constexpr (IO == IO_F32)
+          rv[n] = make_uint4(w[0], w[1], w[2], w[3]);
+        else
+          rv[n] = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4 % EU] | w[5 % EU] << 16,
+                             w[6 % EU] | w[7 % EU] << 16);
       }
     }
   };
@@ -252,24 +301,55 @@ __global__ __launch_bounds__(64 * NW) void attend_kernel(AttendArgs args) {
       for (int i = 0; i < NP; ++i) *reinterpret_cast<bf16x4*>(p + i * plane) = s[i];
     } else {
       const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+      bf16x4 s[2][NP];
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
+      for (int y = 0; y < 2; ++y) {
         f32x4 x;
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          x[e] = __half2float(__ushort_as_half((unsigned short)(w[2 * q + e / 2] >> (16 * (e & 1)))));
-        bf16x4 s[NP];
-        split4<NP>(x, s);
-#pragma unroll
-        for (int i = 0; i < NP; ++i) *reinterpret_cast<bf16x4*>(p + i * plane + 4 * q) = s[i];
+          x[e] = __half2float(__ushort_as_half((unsigned short)(w[2 * y + e / 2] >> (16 * (e & 1)))));
+        split4<NP>(x, s[y]);
       }
+#pragma unroll
+      for (int i = 0; i < NP; ++i) *reinterpret_cast<bf16x8*>(p + i * plane) = join(s[0][i], s[1][i]);
+    }
+  };
+  auto put_chunk = [&](int live) {
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    if (live < C) {                              // the last chunk
+#pragma unroll
+      for (int n = 0; n < T::QU; ++n)
+        if ((n * NT + tid) / (DK / EU) >= live) {
+          rk[n] = zero;
+          if constexpr (OUT) rq[n] = zero;
+        }
+#pragma unroll
+      for (int n = 0; n < T::VU; ++n)
+        if ((n * NT + tid) / (T::DV / EU) >= live) rv[n] = zero;
+    }
+    if (vcols < T::DV) {
+#pragma unroll
+      for (int n = 0; n < T::VU; ++n)
+        rv[n] = keep_elements<B>(rv[n], vcols - (n * NT + tid) % (T::DV / EU) * EU);
+    }
+#pragma unroll
+    for (int n = 0; n < T::QU; ++n) {
+      const int u = n * NT + tid, row = u / (DK / EU), col = u % (DK / EU) * EU;
+      put(rk[n], kl, row, PK, col);
+      if constexpr (OUT) put(rq[n], ql, row, PQ, col);
+    }
+#pragma unroll
+    for (int n = 0; n < T::VU; ++n) {
+      const int u = n * NT + tid, row = u / (T::DV / EU), col = u % (T::DV / EU) * EU;
+      put(rv[n], vl, row, PV, col);
     }
   };
 
-  // ---- the state's columns: lane li has column d0 + li, rows 16 I + 4 g + v of S^T
-  f32x4 S[KT];
-  const bool own = 16 * wave + li < vcols;
-  const int64_t state = ((int64_t)h * a.dv + d0 + li) * DK + 4 * g, per = (int64_t)a.heads * a.dv * DK;
+  // ---- the state's columns: lane li has columns 16 cg + li of the wave's, rows
+  // 16 I + 4 g + v of S^T
+  const int w0 = 16 * CG * wave;                 // the wave's first column in the slice
+  f32x4 S[CG][KT];
+  const int64_t state = ((int64_t)h * a.dv + d0 + w0 + li) * DK + 4 * g, per = (int64_t)a.heads * a.dv * DK;
   float* slot_S = a.S + slot * per + state;
   float* seg_S = args.ws + seg * per + state;
   {
@@ -277,34 +357,32 @@ __global__ __launch_bounds__(64 * NW) void attend_kernel(AttendArgs args) {
     const bool zero = !OUT || (!from_ws && a.fresh && a.fresh[sg.i]);
     const float* p = from_ws ? seg_S : slot_S;
 #pragma unroll
-    for (int I = 0; I < KT; ++I)
-      S[I] = own && !zero ? *reinterpret_cast<const f32x4*>(p + 16 * I) : f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int cg = 0; cg < CG; ++cg)
+#pragma unroll
+      for (int I = 0; I < KT; ++I)
+        S[cg][I] = !zero && w0 + 16 * cg + li < vcols ? *reinterpret_cast<const f32x4*>(p + 16 * cg * DK + 16 * I)
+                                                      : f32x4{0.f, 0.f, 0.f, 0.f};
   }
   if constexpr (OUT)                             // the tiles above the diagonal stay zero
-    for (int e = tid; e < NO * C * PP / 2; e += T::NT) reinterpret_cast<uint32_t*>(&pl[0][0])[e] = 0;
+    for (int e = tid; e < NO * C * PP / 2; e += NT) reinterpret_cast<uint32_t*>(&pl[0][0])[e] = 0;
 
+  // Two barriers per chunk.  Before A: the chunk's rows and decays are put.
+  // A to B: P's tiles, S q and the new S (the rows' last use).  After B: P v,
+  // the output and the next chunk's rows.
   double total = 0.0;
+  read_decays(sg.t0);
   read_chunk(sg.t0);
-  if (wave == NW - 1) total += fill_decays<C>(dec[0], ra, rb, lane);
-  int buf = 0;
-  for (int64_t t0 = sg.t0; t0 < sg.t1; t0 += C, buf ^= 1) {
-    const bool more = t0 + C < sg.t1;
-#pragma unroll
-    for (int n = 0; n < T::QU; ++n) {
-      const int u = n * T::NT + tid, row = u / (DK / T::EU), col = u % (DK / T::EU) * T::EU;
-      if (!T::QGUARD || row < C) {
-        put(rk[n], kl, row, PK, col);
-        if constexpr (OUT) put(rq[n], ql, row, PK, col);
-      }
-    }
-#pragma unroll
-    for (int n = 0; n < T::VU; ++n) {
-      const int u = n * T::NT + tid, row = u / (T::DV / T::EU), col = u % (T::DV / T::EU) * T::EU;
-      put(rv[n], vl, row, PV, col);
+  int at = NT;                                   // the chunk's first token within its round
+  for (int64_t t0 = sg.t0; t0 < sg.t1; t0 += C, at += C) {
+    put_chunk((int)(sg.t1 - t0 < C ? sg.t1 - t0 : C));
+    if (at == NT) {
+      at = 0;
+      const bool in = t0 + tid < sg.t1;
+      total += fill_decays<C>(d, 64 * wave, in ? ra : 1.f, in ? rb : 0.f, lane);
+      if (t0 + NT < sg.t1) read_decays(t0 + NT);
     }
     __syncthreads();
-    if (more) read_chunk(t0 + C);
-    const Decays<C>& d = dec[buf];
+    if (t0 + C < sg.t1) read_chunk(t0 + C);
     if constexpr (OUT) {
       // ---- P^T tiles: rows s, columns t
       for (int idx = wave; idx < CT * (CT + 1) / 2; idx += NW) {
@@ -316,7 +394,7 @@ __global__ __launch_bounds__(64 * NW) void attend_kernel(AttendArgs args) {
 #pragma unroll
           for (int i = 0; i < NP; ++i) {
             kp[i] = *reinterpret_cast<const bf16x8*>(&kl[i][(16 * si + li) * PK + 32 * ks + 8 * g]);
-            qp[i] = *reinterpret_cast<const bf16x8*>(&ql[i][(16 * ti + li) * PK + 32 * ks + 8 * g]);
+            qp[i] = *reinterpret_cast<const bf16x8*>(&ql[i][(16 * ti + li) * PQ + 32 * ks + 8 * g]);
           }
 #pragma unroll
           for (int i = NP - 1; i >= 0; --i)      // small products first
@@ -325,59 +403,119 @@ __global__ __launch_bounds__(64 * NW) void attend_kernel(AttendArgs args) {
               if (i + j < NO) acc = mfma(kp[i], qp[j], acc);
         }
         const int t = 16 * ti + li, s0 = 16 * si + 4 * g;
-        const float ht = d.hi[t], lt = d.lo[t];
-        const f32x4 hs = *reinterpret_cast<const f32x4*>(&d.hi[s0]), ls = *reinterpret_cast<const f32x4*>(&d.lo[s0]);
-        const f32x4 bs = *reinterpret_cast<const f32x4*>(&d.beta[s0]);
+        const float ht = d.hi[at + t], lt = d.lo[at + t];
+        const f32x4 hs = *reinterpret_cast<const f32x4*>(&d.hi[at + s0]), ls = *reinterpret_cast<const f32x4*>(&d.lo[at + s0]);
+        const f32x4 bs = *reinterpret_cast<const f32x4*>(&d.beta[at + s0]);
         f32x4 p;
 #pragma unroll
-        for (int v = 0; v < 4; ++v)
-          p[v] = s0 + v <= t ? acc[v] * (__builtin_amdgcn_exp2f((ht - hs[v]) + (lt - ls[v])) * bs[v]) : 0.f;
+        for (int v = 0; v < 4; ++v) {
+          const float x = acc[v] * (__builtin_amdgcn_exp2f((ht - hs[v]) + (lt - ls[v])) * bs[v]);
+          p[v] = s0 + v <= t ? x : 0.f;
+        }
         bf16x4 parts[NO];
         split4<NO>(p, parts);
 #pragma unroll
         for (int i = 0; i < NO; ++i) *reinterpret_cast<bf16x4*>(&pl[i][t * PP + s0]) = parts[i];
       }
-      __syncthreads();
     }
-    // ---- the wave's 16 columns of v, by columns
-    bf16x4 vr[KB][2][NP];
+    // ---- the wave's columns of v, by columns
+    bf16x4 vr[CG][KB][2][NP];
 #pragma unroll
-    for (int kb = 0; kb < KB; ++kb)
+    for (int cg = 0; cg < CG; ++cg)
 #pragma unroll
-      for (int y = 0; y < 2; ++y)
+      for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
-        for (int i = 0; i < NP; ++i)
-          vr[kb][y][i] = read_column4(&vl[i][(32 * kb + 16 * y + 4 * g + li / 4) * PV + 16 * wave + 4 * (li % 4)]);
+        for (int y = 0; y < 2; ++y)
+#pragma unroll
+          for (int i = 0; i < NP; ++i)
+            vr[cg][kb][y][i] = read_column4(&vl[i][(32 * kb + 16 * y + 4 * g + li / 4) * PV + w0 + 16 * cg + 4 * (li % 4)]);
+    // ---- o^T tiles: rows dv, columns t
+    f32x4 acc[CG][OUT ? CT : 1];
     if constexpr (OUT) {
-      // ---- o^T tiles: rows dv, columns t
-      f32x4 acc[CT];
 #pragma unroll
-      for (int ti = 0; ti < CT; ++ti) acc[ti] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int cg = 0; cg < CG; ++cg)
+#pragma unroll
+        for (int ti = 0; ti < CT; ++ti) acc[cg][ti] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int ks = 0; ks < DK / 32; ++ks) {
-        bf16x4 s0[NO], s1[NO];
-        split4<NO>(S[2 * ks], s0);
-        split4<NO>(S[2 * ks + 1], s1);
+        bf16x8 sp[CG][NO];
+#pragma unroll
+        for (int cg = 0; cg < CG; ++cg) {
+          bf16x4 s0[NO], s1[NO];
+          split4<NO>(S[cg][2 * ks], s0);
+          split4<NO>(S[cg][2 * ks + 1], s1);
+#pragma unroll
+          for (int i = 0; i < NO; ++i) sp[cg][i] = join(s0[i], s1[i]);
+        }
 #pragma unroll
         for (int ti = 0; ti < CT; ++ti) {
           bf16x8 qp[NP];
 #pragma unroll
           for (int i = 0; i < NP; ++i) {
-            const __bf16* p = &ql[i][(16 * ti + li) * PK + 32 * ks + 4 * g];
+            const __bf16* p = &ql[i][(16 * ti + li) * PQ + 32 * ks + 4 * g];
             qp[i] = join(*reinterpret_cast<const bf16x4*>(p), *reinterpret_cast<const bf16x4*>(p + 16));
           }
 #pragma unroll
           for (int i = NO - 1; i >= 0; --i)
 #pragma unroll
             for (int j = NP - 1; j >= 0; --j)
-              if (i + j < NO) acc[ti] = mfma(join(s0[i], s1[i]), qp[j], acc[ti]);
+              if (i + j < NO)
+#pragma unroll
+                for (int cg = 0; cg < CG; ++cg) acc[cg][ti] = mfma(sp[cg][i], qp[j], acc[cg][ti]);
         }
       }
 #pragma unroll
       for (int ti = 0; ti < CT; ++ti) {
-        const float c = d.cin[16 * ti + li];
+        const float c = exp2f(d.hi[at + 16 * ti + li]) * (1.f + 0.69314718f * d.lo[at + 16 * ti + li]);
 #pragma unroll
-        for (int v = 0; v < 4; ++v) acc[ti][v] *= c;
+        for (int cg = 0; cg < CG; ++cg) acc[cg][ti] = acc[cg][ti] * c;
+      }
+    }
+    // ---- S = c_C S + k^T (w v)
+    const float gamma = exp2f(d.hi[at + C - 1]) * (1.f + 0.69314718f * d.lo[at + C - 1]);   // c_C
+#pragma unroll
+    for (int cg = 0; cg < CG; ++cg)
+#pragma unroll
+      for (int I = 0; I < KT; ++I) S[cg][I] = S[cg][I] * gamma;
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb) {
+      bf16x8 vs[CG][3];
+#pragma unroll
+      for (int cg = 0; cg < CG; ++cg) {
+        bf16x4 half[2][3];
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          f32x4 x = widen4(vr[cg][kb][y][0]);
+#pragma unroll
+          for (int i = 1; i < NP; ++i) x = x + widen4(vr[cg][kb][y][i]);
+          x = x * *reinterpret_cast<const f32x4*>(&d.w[at + 32 * kb + 16 * y + 4 * g]);
+          split4<3>(x, half[y]);
+        }
+#pragma unroll
+        for (int i = 0; i < 3; ++i) vs[cg][i] = join(half[0][i], half[1][i]);
+      }
+#pragma unroll
+      for (int I = 0; I < KT; ++I) {
+        bf16x8 kp[NP];
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+          const __bf16* p = &kl[i][(32 * kb + 4 * g + li / 4) * PK + 16 * I + 4 * (li % 4)];
+          kp[i] = join(read_column4(p), read_column4(p + 16 * PK));
+        }
+#pragma unroll
+        for (int i = NP - 1; i >= 0; --i)
+#pragma unroll
+          for (int j = 2; j >= 0; --j)
+            if (i + j < 3)
+#pragma unroll
+              for (int cg = 0; cg < CG; ++cg) S[cg][I] = mfma(kp[i], vs[cg][j], S[cg][I]);
+      }
+    }
+    __syncthreads();
+    if constexpr (OUT) {
+      // ---- P v
+#pragma unroll
+      for (int ti = 0; ti < CT; ++ti) {
 #pragma unroll
         for (int kb = 0; kb <= ti / 2; ++kb) {
           bf16x8 pp[NO];
@@ -390,75 +528,58 @@ __global__ __launch_bounds__(64 * NW) void attend_kernel(AttendArgs args) {
           for (int i = NO - 1; i >= 0; --i)
 #pragma unroll
             for (int j = NP - 1; j >= 0; --j)
-              if (i + j < NO) acc[ti] = mfma(join(vr[kb][0][j], vr[kb][1][j]), pp[i], acc[ti]);
+              if (i + j < NO)
+#pragma unroll
+                for (int cg = 0; cg < CG; ++cg)
+                  acc[cg][ti] = mfma(join(vr[cg][kb][0][j], vr[cg][kb][1][j]), pp[i], acc[cg][ti]);
         }
         const int64_t t = t0 + 16 * ti + li;
-        const int c0 = 16 * wave + 4 * g;
         if (t < sg.t1) {
-          const int64_t e = t * a.o_stride + hv + c0;
-          if (args.o_wide) {
-            if (c0 < vcols) {
-              if constexpr (IO == IO_F32) {
-                *reinterpret_cast<f32x4*>(static_cast<float*>(a.o) + e) = acc[ti];
-              } else {
-                const uint32_t w0 = to16<IO>(acc[ti][0]) | (uint32_t)to16<IO>(acc[ti][1]) << 16;
-                const uint32_t w1 = to16<IO>(acc[ti][2]) | (uint32_t)to16<IO>(acc[ti][3]) << 16;
-                *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.o) + e) = make_uint2(w0, w1);
-              }
-            }
-          } else {
 #pragma unroll
-            for (int v = 0; v < 4; ++v)
-              if (c0 + v < vcols) store1<IO>(a.o, e + v, acc[ti][v]);
+          for (int cg = 0; cg < CG; ++cg) {
+            const int c0 = w0 + 16 * cg + 4 * g;
+            const int64_t e = t * a.o_stride + hv + c0;
+            const f32x4 x = acc[cg][ti];
+            if constexpr (VEC) {
+              if (c0 < vcols) {
+                if constexpr (IO == IO_F32)
+                  *reinterpret_cast<f32x4*>(static_cast<float*>(a.o) + e) = x;
+                else
+                  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.o) + e) =
+                      make_uint2(to16<IO>(x[0]) | (uint32_t)to16<IO>(x[1]) << 16,
+                                 to16<IO>(x[2]) | (uint32_t)to16<IO>(x[3]) << 16);
+              }
+            } else {
+#pragma unroll
+              for (int v = 0; v < 4; ++v)
+                if (c0 + v < vcols) store1<IO>(a.o, e + v, x[v]);
+            }
           }
         }
       }
     }
-    // ---- S = c_C S + k^T (w v)
-    bf16x8 vs[KB][3];
-#pragma unroll
-    for (int kb = 0; kb < KB; ++kb) {
-      bf16x4 half[2][3];
-#pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        f32x4 x = __builtin_convertvector(vr[kb][y][0], f32x4);
-#pragma unroll
-        for (int i = 1; i < NP; ++i) x = x + __builtin_convertvector(vr[kb][y][i], f32x4);
-        x = x * *reinterpret_cast<const f32x4*>(&d.w[32 * kb + 16 * y + 4 * g]);
-        split4<3>(x, half[y]);
-      }
-#pragma unroll
-      for (int i = 0; i < 3; ++i) vs[kb][i] = join(half[0][i], half[1][i]);
-    }
-    const float gamma = d.gamma;
-#pragma unroll
-    for (int I = 0; I < KT; ++I) {
-      S[I] = S[I] * gamma;
-#pragma unroll
-      for (int kb = 0; kb < KB; ++kb) {
-        bf16x8 kp[NP];
-#pragma unroll
-        for (int i = 0; i < NP; ++i) {
-          const __bf16* p = &kl[i][(32 * kb + 4 * g + li / 4) * PK + 16 * I + 4 * (li % 4)];
-          kp[i] = join(read_column4(p), read_column4(p + 16 * PK));
-        }
-#pragma unroll
-        for (int i = NP - 1; i >= 0; --i)
-#pragma unroll
-          for (int j = 2; j >= 0; --j)
-            if (i + j < 3) S[I] = mfma(kp[i], vs[kb][j], S[I]);
-      }
-    }
-    if (more && wave == NW - 1) total += fill_decays<C>(dec[buf ^ 1], ra, rb, lane);
-    __syncthreads();
   }
 
-  if (own && (!OUT || sg.j == sg.n - 1)) {
+  if (!OUT || sg.j == sg.n - 1) {
     float* p = OUT ? slot_S : seg_S;
 #pragma unroll
-    for (int I = 0; I < KT; ++I) *reinterpret_cast<f32x4*>(p + 16 * I) = S[I];
+    for (int cg = 0; cg < CG; ++cg)
+      if (w0 + 16 * cg + li < vcols) {
+#pragma unroll
+        for (int I = 0; I < KT; ++I) *reinterpret_cast<f32x4*>(p + 16 * cg * DK + 16 * I) = S[cg][I];
+      }
   }
-  if (!OUT && slice == 0 && tid == 64 * (NW - 1)) args.ws_decay[seg * a.heads + h] = exp2f((float)total);
+  if constexpr (!OUT) {                          // the segment's own decay
+    __shared__ double sum[NW];
+#pragma unroll
+    for (int o = 1; o < 64; o *= 2) total += __shfl_xor(total, o);
+    if (lane == 0) sum[wave] = total;
+    __syncthreads();
+    if (slice == 0 && tid == 0) {
+      for (int w = 1; w < NW; ++w) total += sum[w];
+      args.ws_decay[seg * a.heads + h] = exp2_of(total);
+    }
+  }
 }
 
 // The states before each segment of a sequence of several: S_0 is the slot's
@@ -494,24 +615,32 @@ __global__ __launch_bounds__(256) void combine_kernel(AttendArgs args, int block
 
 namespace {
 
-template <int IO, int DK, int NW>
+// Value columns of a workgroup.  Three bf16 parts of fp32 rows fill the LDS of
+// half a CU at 64.
+int slice_width(int io, int dv) { return io == IO_F32 || dv <= 64 ? 64 : 128; }
+
+template <int IO, int DK, int CG, bool VEC>
 hipError_t launch_instance(const AttendArgs& args, unsigned blocks, hipStream_t s) {
   const SlotArgs& a = args.s;
   if (args.seg_len) {
-    hipLaunchKernelGGL((dev::attend_kernel<IO, DK, NW, false>), dim3(blocks), dim3(64 * NW), 0, s, args);
+    hipLaunchKernelGGL((dev::attend_kernel<IO, DK, CG, VEC, false>), dim3(blocks), dim3(256), 0, s, args);
     const int64_t quads = (int64_t)a.heads * a.dv * DK / 4, per = (quads + 255) / 256;
     if (per * a.seqs > INT32_MAX) return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL(dev::combine_kernel, dim3((unsigned)(per * a.seqs)), dim3(256), 0, s, args,
                        (int)per, quads);
   }
-  hipLaunchKernelGGL((dev::attend_kernel<IO, DK, NW, true>), dim3(blocks), dim3(64 * NW), 0, s, args);
+  hipLaunchKernelGGL((dev::attend_kernel<IO, DK, CG, VEC, true>), dim3(blocks), dim3(256), 0, s, args);
   return hipGetLastError();
 }
 
 template <int IO, int DK>
 hipError_t launch_width(const AttendArgs& args, unsigned blocks, hipStream_t s) {
-  return args.s.dv <= 64 ? launch_instance<IO, DK, 4>(args, blocks, s)
-                         : launch_instance<IO, DK, 8>(args, blocks, s);
+  if constexpr (IO != IO_F32)
+    if (slice_width(IO, args.s.dv) == 128)
+      return args.wide ? launch_instance<IO, DK, 2, true>(args, blocks, s)
+                       : launch_instance<IO, DK, 2, false>(args, blocks, s);
+  return args.wide ? launch_instance<IO, DK, 1, true>(args, blocks, s)
+                   : launch_instance<IO, DK, 1, false>(args, blocks, s);
 }
 
 }  // namespace
@@ -523,9 +652,10 @@ hipError_t launch_width(const AttendArgs& args, unsigned blocks, hipStream_t s) 
 #define LSQ_ATT_MIN 512
 #endif
 
-AttendPlan attend_plan(int64_t tokens, int32_t seqs, int32_t heads, int32_t dk, int32_t dv) {
+AttendPlan attend_plan(int64_t tokens, int32_t seqs, int32_t heads, int32_t dk, int32_t dv, int io) {
   AttendPlan p{};
-  p.slices = (dv + 127) / 128;
+  const int width = slice_width(io, dv);
+  p.slices = (dv + width - 1) / width;
   const int64_t rows = (int64_t)heads * p.slices;
   int64_t L = (tokens * rows / LSQ_ATT_TARGET + 63) / 64 * 64;
   if (L < LSQ_ATT_MIN) L = LSQ_ATT_MIN;

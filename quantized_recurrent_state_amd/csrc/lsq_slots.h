@@ -34,8 +34,8 @@ struct AttendArgs {
   int64_t seg_len;         // tokens per segment, a multiple of 64; 0: whole sequences
   float* ws;               // [segments][heads][dv][dk], then ws_decay (null without segments)
   float* ws_decay;         // [segments][heads]
-  int32_t slices;          // value columns are taken 128 (or 64) at a time
-  int32_t v_wide, o_wide;  // 16-byte reads of v, 8- or 16-byte writes of o
+  int32_t slices;          // workgroups over a head's value columns
+  int32_t wide;            // v and o allow 16-byte reads and four-element writes
 };
 
 struct AttendPlan {
@@ -44,7 +44,7 @@ struct AttendPlan {
   int32_t slices;
 };
 
-AttendPlan attend_plan(int64_t tokens, int32_t seqs, int32_t heads, int32_t dk, int32_t dv);
+AttendPlan attend_plan(int64_t tokens, int32_t seqs, int32_t heads, int32_t dk, int32_t dv, int io);
 
 // Slots copied between an fp32 handle and a quantised one (same heads, dv, dk).
 struct CopyArgs {
