@@ -621,9 +621,9 @@ lsq_status lsq_attend(lsq_state* st, const lsq_token_batch* batch, void* workspa
                   workspace_bytes, p.workspace);
   }
   const int64_t e = (int64_t)io_bytes(batch->io);
-  const int64_t far = (batch->q_stride > batch->k_stride ? batch->q_stride : batch->k_stride);
-  if ((far > batch->v_stride ? far : batch->v_stride) * e * 64 > INT32_MAX)
-    return fail(LSQ_ERR_UNSUPPORTED, "token strides above 32 MiB");   // lanes address a chunk with 32 bits
+  for (const int64_t x : {batch->q_stride, batch->k_stride, batch->v_stride, batch->o_stride})
+    if (x * e > INT32_MAX / 64)                  // lanes address a chunk's rows with 32 bits
+      return fail(LSQ_ERR_UNSUPPORTED, "a token stride of 32 MiB or more");
   const size_t quad = 4 * (size_t)e;           // o is written four elements at a time
   lsq::AttendArgs a{};
   a.s = slot_args(st, batch);

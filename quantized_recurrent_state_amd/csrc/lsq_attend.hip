@@ -32,6 +32,18 @@ typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+// A chunk's rows of one tensor as a buffer: accesses behind its last byte read
+// 0 and write nothing, so that no lane computes a clamped or 64-bit address.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_of(const void* p, int64_t first, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(static_cast<const char*>(p)) + first, 0,
+                                           bytes, 0x00027000);
+}
+
+// A lane offset behind every buffer: chunks are below 2^31 bytes.
+constexpr uint32_t kNowhere = 0xFFFFFFF0u;
 
 // Tiling of one instance: four waves of CG groups of 16 value columns.
 template <int IO, int DK, int CG>
@@ -72,6 +84,13 @@ __device__ __forceinline__ f32x4 widen4(bf16x4 p) {
   const uint32_t lo = (uint32_t)b, hi = (uint32_t)(b >> 32);
   return f32x4{__uint_as_float(lo << 16), __uint_as_float(lo & 0xFFFF0000u), __uint_as_float(hi << 16),
                __uint_as_float(hi & 0xFFFF0000u)};
+}
+
+// Two values rounded once to a 16-bit type.
+template <int IO>
+__device__ __forceinline__ uint32_t pair16(float x, float y) {
+  if constexpr (IO == IO_BF16) return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{x, y}, bf16x2));
+  return to16<IO_F16>(x) | (uint32_t)to16<IO_F16>(y) << 16;
 }
 
 __device__ __forceinline__ bf16x8 join(bf16x4 a, bf16x4 b) {
@@ -145,14 +164,13 @@ __device__ __forceinline__ double fill_decays(Decays<N>& d, int at, float alpha,
 
 // The first n elements of B bytes of a 16-byte unit, zeros behind them.
 template <int B>
-__device__ __forceinline__ uint4 keep_elements(uint4 x, int n) {
-  uint32_t w[4] = {x.x, x.y, x.z, x.w};
+__device__ __forceinline__ u32x4 keep_elements(u32x4 x, int n) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int in = n * B - 4 * i;                // bytes of word i that stay
-    w[i] = in >= 4 ? w[i] : in <= 0 ? 0u : w[i] & 0xFFFFu;
+    x[i] = in >= 4 ? x[i] : in <= 0 ? 0u : x[i] & 0xFFFFu;
   }
-  return make_uint4(w[0], w[1], w[2], w[3]);
+  return x;
 }
 
 // The segment a workgroup takes: sequence i, its j-th of n segments.  With a
@@ -241,73 +259,67 @@ __global__ __launch_bounds__(256, 2) void attend_kernel(AttendArgs args) {
     return;
   }
 
-  // ---- the chunk's rows, 16 bytes per unit.  Loads are unconditional (a load
-  // under a lane mask would be waited for at once): rows behind the segment
-  // read its last row, columns behind dv the last whole unit, and put_chunk
-  // clears both.
-  uint4 rq[OUT ? T::QU : 1], rk[T::QU], rv[T::VU];
+  // ---- the chunk's rows, 16 bytes per unit, a unit's lane offset apart from
+  // its neighbour's by a whole number of rows.  put_chunk clears what lies
+  // behind the segment or behind dv.
+  u32x4 rq[OUT ? T::QU : 1], rk[T::QU], rv[T::VU];
   float ra, rb;
+  constexpr int KR = NT * EU / DK, VR = NT * EU / T::DV;               // rows per pass of the threads
   const uint32_t kstep = (uint32_t)a.k_stride * B, qstep = (uint32_t)a.q_stride * B, vstep = (uint32_t)a.v_stride * B;
+  const int krow = tid / (DK / EU), kcol = tid % (DK / EU) * EU, vrow = tid / (T::DV / EU), vcol = tid % (T::DV / EU) * EU;
   auto read_decays = [&](int64_t t0) {           // one token of the round per thread
     const int64_t t = t0 + tid < sg.t1 ? t0 + tid : sg.t1 - 1;
     ra = a.alpha[t * a.heads + h];
     rb = a.beta[t * a.heads + h];
   };
   auto read_chunk = [&](int64_t t0) {
-    const int last = (int)(sg.t1 - t0 < C ? sg.t1 - t0 : C) - 1;
-    const char* kb = static_cast<const char*>(a.k) + (t0 * a.k_stride + hk) * B;
-    const char* qb = static_cast<const char*>(a.q) + (t0 * a.q_stride + hk) * B;
-    const char* vb = static_cast<const char*>(a.v) + (t0 * a.v_stride + hv) * B;
+    const uint32_t last = (uint32_t)(sg.t1 - t0 < C ? sg.t1 - t0 : C) - 1;
+    const auto kb = rows_of(a.k, (t0 * a.k_stride + hk) * B, last * kstep + DK * B);
+    const auto qb = rows_of(a.q, (t0 * a.q_stride + hk) * B, last * qstep + DK * B);
+    const auto vb = rows_of(a.v, (t0 * a.v_stride + hv) * B, last * vstep + vcols * B);
+    uint32_t ko = krow * kstep + kcol * B, qo = krow * qstep + kcol * B, vo = vrow * vstep + vcol * B;
 #pragma unroll
     for (int n = 0; n < T::QU; ++n) {
-      const int u = n * NT + tid, row = u / (DK / EU), col = u % (DK / EU) * 16;
-      const uint32_t r = row < last ? row : last;
-      rk[n] = *reinterpret_cast<const uint4*>(kb + (r * kstep + col));
-      if constexpr (OUT) rq[n] = *reinterpret_cast<const uint4*>(qb + (r * qstep + col));
+      rk[n] = __builtin_amdgcn_raw_buffer_load_b128(kb, ko, 0, 0);
+      ko += KR * kstep;
+      if constexpr (OUT) rq[n] = __builtin_amdgcn_raw_buffer_load_b128(qb, qo, 0, 0);
+      qo += KR * qstep;
     }
 #pragma unroll
     for (int n = 0; n < T::VU; ++n) {
-      const int u = n * NT + tid, row = u / (T::DV / EU), col = u % (T::DV / EU) * EU;
-      const uint32_t r = row < last ? row : last;
       if constexpr (VEC) {
-        rv[n] = *reinterpret_cast<const uint4*>(vb + (r * vstep + (col < vcols ? col : vcols - EU) * B));
+        rv[n] = __builtin_amdgcn_raw_buffer_load_b128(vb, vo, 0, 0);
+      } else if constexpr (IO == IO_F32) {
+#pragma unroll
+        for (int x = 0; x < EU; ++x) rv[n][x] = __builtin_amdgcn_raw_buffer_load_b32(vb, vo + x * B, 0, 0);
       } else {
         uint32_t w[EU];
 #pragma unroll
-        for (int x = 0; x < EU; ++x) {
-          const char* e = vb + (r * vstep + (col + x < vcols ? col + x : vcols - 1) * B);
-          if constexpr (IO == IO_F32)
-            w[x] = *reinterpret_cast<const uint32_t*>(e);
-          else
-            w[x] = *reinterpret_cast<const uint16_t*>(e);
-        }
-        if constexpr (IO == IO_F32)
-          rv[n] = make_uint4(w[0], w[1], w[2], w[3]);
-        else
-          rv[n] = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4 % EU] | w[5 % EU] << 16,
-                             w[6 % EU] | w[7 % EU] << 16);
+        for (int x = 0; x < EU; ++x) w[x] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(vb, vo + x * B, 0, 0);
+#pragma unroll
+        for (int x = 0; x < EU / 2; ++x) rv[n][x] = w[2 * x] | w[2 * x + 1] << 16;
       }
+      vo += VR * vstep;
     }
   };
-  auto put = [&](uint4 r, auto* dst, int row, int pitch, int col) {   // one unit's parts
+  auto put = [&](u32x4 r, auto* dst, int row, int pitch, int col) {   // one unit's parts
     __bf16* p = &dst[0][row * pitch + col];
     constexpr int plane = sizeof(dst[0]) / sizeof(__bf16);
     if constexpr (IO == IO_BF16) {
-      *reinterpret_cast<uint4*>(p) = r;
+      *reinterpret_cast<u32x4*>(p) = r;
     } else if constexpr (IO == IO_F32) {
       bf16x4 s[NP];
       split4<NP>(__builtin_bit_cast(f32x4, r), s);
 #pragma unroll
       for (int i = 0; i < NP; ++i) *reinterpret_cast<bf16x4*>(p + i * plane) = s[i];
     } else {
-      const uint32_t w[4] = {r.x, r.y, r.z, r.w};
       bf16x4 s[2][NP];
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
         f32x4 x;
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          x[e] = __half2float(__ushort_as_half((unsigned short)(w[2 * y + e / 2] >> (16 * (e & 1)))));
+          x[e] = __half2float(__ushort_as_half((unsigned short)(r[2 * y + e / 2] >> (16 * (e & 1)))));
         split4<NP>(x, s[y]);
       }
 #pragma unroll
@@ -315,39 +327,35 @@ __global__ __launch_bounds__(256, 2) void attend_kernel(AttendArgs args) {
     }
   };
   auto put_chunk = [&](int live) {
-    const uint4 zero = make_uint4(0, 0, 0, 0);
+    const u32x4 zero = {0, 0, 0, 0};
     if (live < C) {                              // the last chunk
 #pragma unroll
       for (int n = 0; n < T::QU; ++n)
-        if ((n * NT + tid) / (DK / EU) >= live) {
+        if (n * KR + krow >= live) {
           rk[n] = zero;
           if constexpr (OUT) rq[n] = zero;
         }
 #pragma unroll
       for (int n = 0; n < T::VU; ++n)
-        if ((n * NT + tid) / (T::DV / EU) >= live) rv[n] = zero;
+        if (n * VR + vrow >= live) rv[n] = zero;
     }
     if (vcols < T::DV) {
 #pragma unroll
-      for (int n = 0; n < T::VU; ++n)
-        rv[n] = keep_elements<B>(rv[n], vcols - (n * NT + tid) % (T::DV / EU) * EU);
+      for (int n = 0; n < T::VU; ++n) rv[n] = keep_elements<B>(rv[n], vcols - vcol);
     }
 #pragma unroll
     for (int n = 0; n < T::QU; ++n) {
-      const int u = n * NT + tid, row = u / (DK / EU), col = u % (DK / EU) * EU;
-      put(rk[n], kl, row, PK, col);
-      if constexpr (OUT) put(rq[n], ql, row, PQ, col);
+      put(rk[n], kl, n * KR + krow, PK, kcol);
+      if constexpr (OUT) put(rq[n], ql, n * KR + krow, PQ, kcol);
     }
 #pragma unroll
-    for (int n = 0; n < T::VU; ++n) {
-      const int u = n * NT + tid, row = u / (T::DV / EU), col = u % (T::DV / EU) * EU;
-      put(rv[n], vl, row, PV, col);
-    }
+    for (int n = 0; n < T::VU; ++n) put(rv[n], vl, n * VR + vrow, PV, vcol);
   };
 
   // ---- the state's columns: lane li has columns 16 cg + li of the wave's, rows
   // 16 I + 4 g + v of S^T
   const int w0 = 16 * CG * wave;                 // the wave's first column in the slice
+  const uint32_t ostep = (uint32_t)a.o_stride * B;
   f32x4 S[CG][KT];
   const int64_t state = ((int64_t)h * a.dv + d0 + w0 + li) * DK + 4 * g, per = (int64_t)a.heads * a.dv * DK;
   float* slot_S = a.S + slot * per + state;
@@ -374,7 +382,8 @@ __global__ __launch_bounds__(256, 2) void attend_kernel(AttendArgs args) {
   read_chunk(sg.t0);
   int at = NT;                                   // the chunk's first token within its round
   for (int64_t t0 = sg.t0; t0 < sg.t1; t0 += C, at += C) {
-    put_chunk((int)(sg.t1 - t0 < C ? sg.t1 - t0 : C));
+    const int live = (int)(sg.t1 - t0 < C ? sg.t1 - t0 : C);
+    put_chunk(live);
     if (at == NT) {
       at = 0;
       const bool in = t0 + tid < sg.t1;
@@ -382,7 +391,6 @@ __global__ __launch_bounds__(256, 2) void attend_kernel(AttendArgs args) {
       if (t0 + NT < sg.t1) read_decays(t0 + NT);
     }
     __syncthreads();
-    if (t0 + C < sg.t1) read_chunk(t0 + C);
     if constexpr (OUT) {
       // ---- P^T tiles: rows s, columns t
       for (int idx = wave; idx < CT * (CT + 1) / 2; idx += NW) {
@@ -418,24 +426,9 @@ __global__ __launch_bounds__(256, 2) void attend_kernel(AttendArgs args) {
         for (int i = 0; i < NO; ++i) *reinterpret_cast<bf16x4*>(&pl[i][t * PP + s0]) = parts[i];
       }
     }
-    // ---- the wave's columns of v, by columns
-    bf16x4 vr[CG][KB][2][NP];
-#pragma unroll
-    for (int cg = 0; cg < CG; ++cg)
-#pragma unroll
-      for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-        for (int y = 0; y < 2; ++y)
-#pragma unroll
-          for (int i = 0; i < NP; ++i)
-            vr[cg][kb][y][i] = read_column4(&vl[i][(32 * kb + 16 * y + 4 * g + li / 4) * PV + w0 + 16 * cg + 4 * (li % 4)]);
     // ---- o^T tiles: rows dv, columns t
     f32x4 acc[CG][OUT ? CT : 1];
     if constexpr (OUT) {
-#pragma unroll
-      for (int cg = 0; cg < CG; ++cg)
-#pragma unroll
-        for (int ti = 0; ti < CT; ++ti) acc[cg][ti] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int ks = 0; ks < DK / 32; ++ks) {
         bf16x8 sp[CG][NO];
@@ -461,18 +454,36 @@ __global__ __launch_bounds__(256, 2) void attend_kernel(AttendArgs args) {
             for (int j = NP - 1; j >= 0; --j)
               if (i + j < NO)
 #pragma unroll
-                for (int cg = 0; cg < CG; ++cg) acc[cg][ti] = mfma(sp[cg][i], qp[j], acc[cg][ti]);
+                for (int cg = 0; cg < CG; ++cg)
+                  acc[cg][ti] = mfma(sp[cg][i], qp[j], ks == 0 && i == NO - 1 && j == (NP < 2 ? 0 : NO - 1 - i)
+                                                           ? f32x4{0.f, 0.f, 0.f, 0.f} : acc[cg][ti]);
         }
       }
 #pragma unroll
       for (int ti = 0; ti < CT; ++ti) {
-        const float c = exp2f(d.hi[at + 16 * ti + li]) * (1.f + 0.69314718f * d.lo[at + 16 * ti + li]);
+        const float c = __builtin_amdgcn_exp2f(d.hi[at + 16 * ti + li]) * (1.f + 0.69314718f * d.lo[at + 16 * ti + li]);
 #pragma unroll
         for (int cg = 0; cg < CG; ++cg) acc[cg][ti] = acc[cg][ti] * c;
       }
     }
+    // the next chunk's rows: held in registers from here on, past the products
+    // with S, which need the most of them
+    asm volatile("" ::: "memory");
+    if (t0 + C < sg.t1) read_chunk(t0 + C);
+    __builtin_amdgcn_sched_barrier(0);
+    // ---- the wave's columns of v, by columns
+    bf16x4 vr[CG][KB][2][NP];
+#pragma unroll
+    for (int cg = 0; cg < CG; ++cg)
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+#pragma unroll
+          for (int i = 0; i < NP; ++i)
+            vr[cg][kb][y][i] = read_column4(&vl[i][(32 * kb + 16 * y + 4 * g + li / 4) * PV + w0 + 16 * cg + 4 * (li % 4)]);
     // ---- S = c_C S + k^T (w v)
-    const float gamma = exp2f(d.hi[at + C - 1]) * (1.f + 0.69314718f * d.lo[at + C - 1]);   // c_C
+    const float gamma = __builtin_amdgcn_exp2f(d.hi[at + C - 1]) * (1.f + 0.69314718f * d.lo[at + C - 1]);   // c_C
 #pragma unroll
     for (int cg = 0; cg < CG; ++cg)
 #pragma unroll
@@ -533,29 +544,34 @@ __global__ __launch_bounds__(256, 2) void attend_kernel(AttendArgs args) {
                 for (int cg = 0; cg < CG; ++cg)
                   acc[cg][ti] = mfma(join(vr[cg][kb][0][j], vr[cg][kb][1][j]), pp[i], acc[cg][ti]);
         }
-        const int64_t t = t0 + 16 * ti + li;
-        if (t < sg.t1) {
+      }
+      // ---- the output: four columns of a token per lane and tile
+      const auto ob = rows_of(a.o, (t0 * a.o_stride + hv) * B, (uint32_t)(live - 1) * ostep + vcols * B);
+      uint32_t oo = li * ostep + (w0 + 4 * g) * B;
 #pragma unroll
-          for (int cg = 0; cg < CG; ++cg) {
-            const int c0 = w0 + 16 * cg + 4 * g;
-            const int64_t e = t * a.o_stride + hv + c0;
-            const f32x4 x = acc[cg][ti];
-            if constexpr (VEC) {
-              if (c0 < vcols) {
-                if constexpr (IO == IO_F32)
-                  *reinterpret_cast<f32x4*>(static_cast<float*>(a.o) + e) = x;
-                else
-                  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.o) + e) =
-                      make_uint2(to16<IO>(x[0]) | (uint32_t)to16<IO>(x[1]) << 16,
-                                 to16<IO>(x[2]) | (uint32_t)to16<IO>(x[3]) << 16);
-              }
-            } else {
+      for (int ti = 0; ti < CT; ++ti) {
 #pragma unroll
-              for (int v = 0; v < 4; ++v)
-                if (c0 + v < vcols) store1<IO>(a.o, e + v, x[v]);
+        for (int cg = 0; cg < CG; ++cg) {
+          const f32x4 x = acc[cg][ti];
+          const int left = vcols - (w0 + 16 * cg + 4 * g);             // columns to write
+          if constexpr (VEC) {
+            const uint32_t e = left > 0 ? oo + 16 * cg * B : kNowhere;
+            if constexpr (IO == IO_F32)
+              __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, x), ob, e, 0, 0);
+            else
+              __builtin_amdgcn_raw_buffer_store_b64(u32x2{pair16<IO>(x[0], x[1]), pair16<IO>(x[2], x[3])}, ob, e, 0, 0);
+          } else {
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+              const uint32_t e = v < left ? oo + (16 * cg + v) * B : kNowhere;
+              if constexpr (IO == IO_F32)
+                __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x[v]), ob, e, 0, 0);
+              else
+                __builtin_amdgcn_raw_buffer_store_b16(to16<IO>(x[v]), ob, e, 0, 0);
             }
           }
         }
+        oo += 16 * ostep;
       }
     }
   }
