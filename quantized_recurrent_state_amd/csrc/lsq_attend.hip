@@ -23,6 +23,9 @@
 #include "lsq_slots.h"
 #include "lsq_slots_dev.h"
 
+#ifndef LSQ_NW
+#define LSQ_NW 8
+#endif
 namespace lsq {
 namespace dev {
 
@@ -45,19 +48,24 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_of(const void* p, int64_t
 // A lane offset behind every buffer: chunks are below 2^31 bytes.
 constexpr uint32_t kNowhere = 0xFFFFFFF0u;
 
-// Tiling of one instance: four waves of CG groups of 16 value columns.
-template <int IO, int DK, int CG>
+// Tiling of one instance: NW waves of CG groups of 16 value columns, chunks of 32
+// tokens (one k-step of the MFMA over tokens).
+template <int IO, int DK, int NW, int CG>
 struct Tile {
   static constexpr int NP = IO == IO_BF16 ? 1 : IO == IO_F16 ? 2 : 3;   // parts of an input
   static constexpr int NO = IO == IO_F32 ? 3 : 2;                       // parts on the output's side
-  static constexpr int C = IO == IO_BF16 ? 64 : 32;                     // tokens per chunk
-  static constexpr int NW = 4, NT = 256, DV = 16 * CG * NW;
+  static constexpr int C = 32, NT = 64 * NW, DV = 16 * CG * NW, ROUND = 256;
   static constexpr int EU = IO == IO_F32 ? 4 : 8;                       // elements of a 16-byte unit
   // LDS row pitches in elements.  k and v are read by columns, four rows of 32
   // bytes by 16 lanes: rows 8 banks apart.  q and P are read by rows, 8 bytes of
   // 16 rows: rows 4 banks apart.  Neither then meets in a bank.
   static constexpr int PK = DK + 16, PV = DV + 16, PQ = DK + 8, PP = C + 8;
-  static constexpr int QU = C * DK / EU / NT, VU = C * DV / EU / NT;    // units of k (q), v per thread
+  static constexpr int QU = (C * DK / EU + NT - 1) / NT, VU = C * DV / EU / NT;   // units of k (q), v per thread
+  static constexpr bool SPARE = QU * NT > C * DK / EU;                  // some threads have no unit of k
+  // Two copies of the rows where two workgroups of a CU have room for them, and
+  // P of two chunks (its product with v runs one chunk behind).
+  static constexpr int RB = IO == IO_BF16 ? 2 : 1;
+  static constexpr bool BEHIND = IO != IO_F32;
 };
 
 // x as a sum of N bf16 parts, four values at a time.
@@ -217,27 +225,30 @@ __device__ __forceinline__ int64_t xcd_item(int64_t b, int64_t n) {
 }
 
 // One workgroup walks the chunks of one segment of one head, 64 CG value
-// columns of it.  Per chunk: the chunk's rows (read one chunk ahead into
-// registers) go to LDS as bf16 parts; the waves share out P's lower tiles; then
-// each wave has its 16 CG columns of S in registers in the layout that the MFMA
-// both writes (S^T[dk, dv] accumulated from k^T and the scaled v) and reads (as
-// the operand of S q): the k index of an operand is only a labelling, so slots
-// 0-3 and 4-7 of a lane group g stand for rows 4 g .. and 16 + 4 g .. of a
-// 32-row step in every product.  OUT = false adds up a segment's writes alone
-// (no q, no output), for the segments behind it.  VEC: v and o by whole units
-// (else by element, for odd widths and addresses).
-template <int IO, int DK, int CG, bool VEC, bool OUT>
-__global__ __launch_bounds__(256, 2) void attend_kernel(AttendArgs args) {
-  using T = Tile<IO, DK, CG>;
+// columns of it.  The waves share out P's four tiles; each has its 16 CG
+// columns of S in registers in the layout that the MFMA both writes (S^T[dk, dv]
+// accumulated from k^T and the scaled v) and reads (as the operand of S q): the
+// k index of an operand is only a labelling, so slots 0-3 and 4-7 of a lane
+// group g stand for rows 4 g .. and 16 + 4 g .. of a 32-row step in every
+// product.  What bounds it is the latency of a chunk's steps rather than any
+// rate, so a chunk's products are independent of each other: S q and the new S,
+// P of the same chunk, and (BEHIND) P v of the chunk before, with the next rows
+// on their way to LDS, all between two barriers.  OUT = false adds up a
+// segment's writes alone (no q, no output), for the segments behind it.  VEC: v
+// and o by whole units (else by element, for odd widths and addresses).
+template <int IO, int DK, int NW, int CG, bool VEC, bool OUT>
+__global__ __launch_bounds__(64 * NW, NW / 2) void attend_kernel(AttendArgs args) {
+  using T = Tile<IO, DK, NW, CG>;
   constexpr int NP = T::NP, NO = T::NO, C = T::C, PK = T::PK, PV = T::PV, PQ = T::PQ, PP = T::PP;
-  constexpr int NT = T::NT, NW = T::NW, EU = T::EU, B = 16 / EU;   // B: bytes of an element
-  constexpr int CT = C / 16, KT = DK / 16, KB = C / 32;
+  constexpr int NT = T::NT, EU = T::EU, RB = T::RB, ROUND = T::ROUND, B = 16 / EU;   // B: bytes of an element
+  constexpr bool BEHIND = T::BEHIND;
+  constexpr int CT = C / 16, KT = DK / 16;
   const SlotArgs& a = args.s;
-  __shared__ __align__(16) __bf16 kl[NP][C * PK];
-  __shared__ __align__(16) __bf16 vl[NP][C * PV];
-  __shared__ __align__(16) __bf16 ql[OUT ? NP : 1][OUT ? C * PQ : 8];
-  __shared__ __align__(16) __bf16 pl[OUT ? NO : 1][OUT ? C * PP : 8];
-  __shared__ __align__(16) Decays<NT> d;         // a round of NT tokens
+  __shared__ __align__(16) __bf16 kl[RB][NP][C * PK];
+  __shared__ __align__(16) __bf16 vl[RB][NP][C * PV];
+  __shared__ __align__(16) __bf16 ql[OUT ? RB : 1][OUT ? NP : 1][OUT ? C * PQ : 8];
+  __shared__ __align__(16) __bf16 pl[OUT && BEHIND ? 2 : 1][OUT ? NO : 1][OUT ? C * PP : 8];
+  __shared__ __align__(16) Decays<ROUND> dec[RB];
 
   const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, li = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -258,25 +269,40 @@ __global__ __launch_bounds__(256, 2) void attend_kernel(AttendArgs args) {
           store1<IO>(a.o, t * a.o_stride + hv + c, __uint_as_float(0x7FC00000u));
     return;
   }
+  const int len = (int)(sg.t1 - sg.t0), chunks = (len + C - 1) / C;
 
-  // ---- the chunk's rows, 16 bytes per unit, a unit's lane offset apart from
-  // its neighbour's by a whole number of rows.  put_chunk clears what lies
-  // behind the segment or behind dv.
+  // ---- a chunk's rows, 16 bytes per unit, a unit's lane offset apart from its
+  // neighbour's by a whole number of rows.  Rows behind the segment read as 0.
   u32x4 rq[OUT ? T::QU : 1], rk[T::QU], rv[T::VU];
   float ra, rb;
   constexpr int KR = NT * EU / DK, VR = NT * EU / T::DV;               // rows per pass of the threads
-  const uint32_t kstep = (uint32_t)a.k_stride * B, qstep = (uint32_t)a.q_stride * B, vstep = (uint32_t)a.v_stride * B;
+  const uint32_t kstep = (uint32_t)a.k_stride * B, qstep = (uint32_t)a.q_stride * B;
+  const uint32_t vstep = (uint32_t)a.v_stride * B, ostep = (uint32_t)a.o_stride * B;
   const int krow = tid / (DK / EU), kcol = tid % (DK / EU) * EU, vrow = tid / (T::DV / EU), vcol = tid % (T::DV / EU) * EU;
-  auto read_decays = [&](int64_t t0) {           // one token of the round per thread
-    const int64_t t = t0 + tid < sg.t1 ? t0 + tid : sg.t1 - 1;
-    ra = a.alpha[t * a.heads + h];
-    rb = a.beta[t * a.heads + h];
+  auto bytes_of = [&](int c, uint32_t step, uint32_t row) -> uint32_t {  // of chunk c's rows, 0 behind the last
+    const int live = len - c * C < C ? len - c * C : C;
+    return live > 0 ? (uint32_t)(live - 1) * step + row : 0u;
   };
-  auto read_chunk = [&](int64_t t0) {
-    const uint32_t last = (uint32_t)(sg.t1 - t0 < C ? sg.t1 - t0 : C) - 1;
-    const auto kb = rows_of(a.k, (t0 * a.k_stride + hk) * B, last * kstep + DK * B);
-    const auto qb = rows_of(a.q, (t0 * a.q_stride + hk) * B, last * qstep + DK * B);
-    const auto vb = rows_of(a.v, (t0 * a.v_stride + hv) * B, last * vstep + vcols * B);
+  // A round of decays: one token per thread of the last four waves.
+  const int dtok = tid - (NT - ROUND);
+  auto read_decays = [&](int t) {
+    const int64_t x = (sg.t0 + (t + dtok < len ? (dtok < 0 ? 0 : t + dtok) : len - 1)) * a.heads + h;
+    ra = a.alpha[x];
+    rb = a.beta[x];
+  };
+  double total = 0.0;
+  auto put_decays = [&](int t, int buf) {
+    if (dtok >= 0) {
+      const bool in = t + dtok < len;
+      total += fill_decays<C>(dec[buf], dtok & ~63, in ? ra : 1.f, in ? rb : 0.f, lane);
+      if (t + ROUND < len) read_decays(t + ROUND);
+    }
+  };
+  auto read_chunk = [&](int c) {
+    const int64_t t = sg.t0 + c * C;
+    const auto kb = rows_of(a.k, (t * a.k_stride + hk) * B, bytes_of(c, kstep, DK * B));
+    const auto qb = rows_of(a.q, (t * a.q_stride + hk) * B, bytes_of(c, qstep, DK * B));
+    const auto vb = rows_of(a.v, (t * a.v_stride + hv) * B, bytes_of(c, vstep, vcols * B));
     uint32_t ko = krow * kstep + kcol * B, qo = krow * qstep + kcol * B, vo = vrow * vstep + vcol * B;
 #pragma unroll
     for (int n = 0; n < T::QU; ++n) {
@@ -326,9 +352,13 @@ __global__ __launch_bounds__(256, 2) void attend_kernel(AttendArgs args) {
       for (int i = 0; i < NP; ++i) *reinterpret_cast<bf16x8*>(p + i * plane) = join(s[0][i], s[1][i]);
     }
   };
-  auto put_chunk = [&](int live) {
-    const u32x4 zero = {0, 0, 0, 0};
-    if (live < C) {                              // the last chunk
+  // Rows closer than their own length (a broadcast input) do not read as 0
+  // behind the segment, nor do columns behind dv.
+  const bool overlap = kstep < DK * B || qstep < DK * B || vstep < (uint32_t)vcols * B;
+  auto put_chunk = [&](int c, int buf) {
+    if (overlap && len - c * C < C) {
+      const u32x4 zero = {0, 0, 0, 0};
+      const int live = len - c * C;
 #pragma unroll
       for (int n = 0; n < T::QU; ++n)
         if (n * KR + krow >= live) {
@@ -344,18 +374,18 @@ __global__ __launch_bounds__(256, 2) void attend_kernel(AttendArgs args) {
       for (int n = 0; n < T::VU; ++n) rv[n] = keep_elements<B>(rv[n], vcols - vcol);
     }
 #pragma unroll
-    for (int n = 0; n < T::QU; ++n) {
-      put(rk[n], kl, n * KR + krow, PK, kcol);
-      if constexpr (OUT) put(rq[n], ql, n * KR + krow, PQ, kcol);
-    }
+    for (int n = 0; n < T::QU; ++n)
+      if (!T::SPARE || n * KR + krow < C) {
+        put(rk[n], kl[buf], n * KR + krow, PK, kcol);
+        if constexpr (OUT) put(rq[n], ql[buf], n * KR + krow, PQ, kcol);
+      }
 #pragma unroll
-    for (int n = 0; n < T::VU; ++n) put(rv[n], vl, n * VR + vrow, PV, vcol);
+    for (int n = 0; n < T::VU; ++n) put(rv[n], vl[buf], n * VR + vrow, PV, vcol);
   };
 
   // ---- the state's columns: lane li has columns 16 cg + li of the wave's, rows
   // 16 I + 4 g + v of S^T
   const int w0 = 16 * CG * wave;                 // the wave's first column in the slice
-  const uint32_t ostep = (uint32_t)a.o_stride * B;
   f32x4 S[CG][KT];
   const int64_t state = ((int64_t)h * a.dv + d0 + w0 + li) * DK + 4 * g, per = (int64_t)a.heads * a.dv * DK;
   float* slot_S = a.S + slot * per + state;
@@ -371,64 +401,113 @@ __global__ __launch_bounds__(256, 2) void attend_kernel(AttendArgs args) {
         S[cg][I] = !zero && w0 + 16 * cg + li < vcols ? *reinterpret_cast<const f32x4*>(p + 16 * cg * DK + 16 * I)
                                                       : f32x4{0.f, 0.f, 0.f, 0.f};
   }
-  if constexpr (OUT)                             // the tiles above the diagonal stay zero
-    for (int e = tid; e < NO * C * PP / 2; e += NT) reinterpret_cast<uint32_t*>(&pl[0][0])[e] = 0;
 
-  // Two barriers per chunk.  Before A: the chunk's rows and decays are put.
-  // A to B: P's tiles, S q and the new S (the rows' last use).  After B: P v,
-  // the output and the next chunk's rows.
-  double total = 0.0;
-  read_decays(sg.t0);
-  read_chunk(sg.t0);
-  int at = NT;                                   // the chunk's first token within its round
-  for (int64_t t0 = sg.t0; t0 < sg.t1; t0 += C, at += C) {
-    const int live = (int)(sg.t1 - t0 < C ? sg.t1 - t0 : C);
-    put_chunk(live);
-    if (at == NT) {
-      at = 0;
-      const bool in = t0 + tid < sg.t1;
-      total += fill_decays<C>(d, 64 * wave, in ? ra : 1.f, in ? rb : 0.f, lane);
-      if (t0 + NT < sg.t1) read_decays(t0 + NT);
+  bf16x4 vr[CG][2][NP];                          // the wave's columns of v, by columns
+  f32x4 acc[CG][OUT ? CT : 1];                   // o^T tiles: rows dv, columns t
+  // acc += P v of chunk c, and the output
+  auto finish = [&](int c, int buf) {
+    const auto ob = rows_of(a.o, ((sg.t0 + c * C) * a.o_stride + hv) * B, c < 0 ? 0u : bytes_of(c, ostep, vcols * B));
+    uint32_t oo = li * ostep + (w0 + 4 * g) * B;
+#pragma unroll
+    for (int ti = 0; ti < CT; ++ti) {
+      bf16x8 pp[NO];
+#pragma unroll
+      for (int i = 0; i < NO; ++i) {
+        const __bf16* p = &pl[buf][i][(16 * ti + li) * PP + 4 * g];
+        pp[i] = join(*reinterpret_cast<const bf16x4*>(p), *reinterpret_cast<const bf16x4*>(p + 16));
+      }
+#pragma unroll
+      for (int i = NO - 1; i >= 0; --i)          // small products first
+#pragma unroll
+        for (int j = NP - 1; j >= 0; --j)
+          if (i + j < NO)
+#pragma unroll
+            for (int cg = 0; cg < CG; ++cg) acc[cg][ti] = mfma(join(vr[cg][0][j], vr[cg][1][j]), pp[i], acc[cg][ti]);
     }
+#pragma unroll
+    for (int ti = 0; ti < CT; ++ti) {
+#pragma unroll
+      for (int cg = 0; cg < CG; ++cg) {
+        const f32x4 x = acc[cg][ti];
+        const int left = vcols - (w0 + 16 * cg + 4 * g);               // columns to write, four per lane
+        if constexpr (VEC) {
+          const uint32_t e = left > 0 ? oo + 16 * cg * B : kNowhere;
+          if constexpr (IO == IO_F32)
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, x), ob, e, 0, 0);
+          else
+            __builtin_amdgcn_raw_buffer_store_b64(u32x2{pair16<IO>(x[0], x[1]), pair16<IO>(x[2], x[3])}, ob, e, 0, 0);
+        } else {
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            const uint32_t e = v < left ? oo + (16 * cg + v) * B : kNowhere;
+            if constexpr (IO == IO_F32)
+              __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x[v]), ob, e, 0, 0);
+            else
+              __builtin_amdgcn_raw_buffer_store_b16(to16<IO>(x[v]), ob, e, 0, 0);
+          }
+        }
+      }
+      oo += 16 * ostep;
+    }
+  };
+
+  read_decays(0);
+  read_chunk(0);
+  put_decays(0, 0);
+  put_chunk(0, 0);
+  if constexpr (RB == 2) read_chunk(1);
+#pragma unroll
+  for (int cg = 0; cg < CG; ++cg) {
+#pragma unroll
+    for (int ti = 0; ti < (OUT ? CT : 1); ++ti) acc[cg][ti] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int y = 0; y < 2; ++y)
+#pragma unroll
+      for (int i = 0; i < NP; ++i) vr[cg][y][i] = bf16x4{};
+  }
+  for (int c = 0; c < chunks; ++c) {
+    const int buf = RB == 2 ? c & 1 : 0, at = c * C % ROUND;
+    const Decays<ROUND>& d = dec[RB == 2 ? c / (ROUND / C) & 1 : 0];
     __syncthreads();
+    if constexpr (RB == 2) {                     // rows of c + 1 to LDS, of c + 2 from memory
+      put_chunk(c + 1, buf ^ 1);
+      read_chunk(c + 2);
+    }
+    if constexpr (OUT && BEHIND) finish(c - 1, (c & 1) ^ 1);
     if constexpr (OUT) {
-      // ---- P^T tiles: rows s, columns t
-      for (int idx = wave; idx < CT * (CT + 1) / 2; idx += NW) {
-        const int ti = idx >= 6 ? 3 : idx >= 3 ? 2 : idx >= 1 ? 1 : 0, si = idx - ti * (ti + 1) / 2;
-        f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+      // ---- P^T tile of a wave: rows s, columns t (the tile above the diagonal is 0)
+      if (NW == 4 || wave < 4) {
+        const int ti = wave >> 1, si = wave & 1;
+        f32x4 x = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int ks = 0; ks < DK / 32; ++ks) {
           bf16x8 kp[NP], qp[NP];
 #pragma unroll
           for (int i = 0; i < NP; ++i) {
-            kp[i] = *reinterpret_cast<const bf16x8*>(&kl[i][(16 * si + li) * PK + 32 * ks + 8 * g]);
-            qp[i] = *reinterpret_cast<const bf16x8*>(&ql[i][(16 * ti + li) * PQ + 32 * ks + 8 * g]);
+            kp[i] = *reinterpret_cast<const bf16x8*>(&kl[buf][i][(16 * si + li) * PK + 32 * ks + 8 * g]);
+            qp[i] = *reinterpret_cast<const bf16x8*>(&ql[buf][i][(16 * ti + li) * PQ + 32 * ks + 8 * g]);
           }
 #pragma unroll
-          for (int i = NP - 1; i >= 0; --i)      // small products first
+          for (int i = NP - 1; i >= 0; --i)
 #pragma unroll
             for (int j = NP - 1; j >= 0; --j)
-              if (i + j < NO) acc = mfma(kp[i], qp[j], acc);
+              if (i + j < NO) x = mfma(kp[i], qp[j], x);
         }
         const int t = 16 * ti + li, s0 = 16 * si + 4 * g;
         const float ht = d.hi[at + t], lt = d.lo[at + t];
         const f32x4 hs = *reinterpret_cast<const f32x4*>(&d.hi[at + s0]), ls = *reinterpret_cast<const f32x4*>(&d.lo[at + s0]);
         const f32x4 bs = *reinterpret_cast<const f32x4*>(&d.beta[at + s0]);
-        f32x4 p;
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
-          const float x = acc[v] * (__builtin_amdgcn_exp2f((ht - hs[v]) + (lt - ls[v])) * bs[v]);
-          p[v] = s0 + v <= t ? x : 0.f;
+          const float y = x[v] * (__builtin_amdgcn_exp2f((ht - hs[v]) + (lt - ls[v])) * bs[v]);
+          x[v] = s0 + v <= t ? y : 0.f;
         }
         bf16x4 parts[NO];
-        split4<NO>(p, parts);
+        split4<NO>(x, parts);
 #pragma unroll
-        for (int i = 0; i < NO; ++i) *reinterpret_cast<bf16x4*>(&pl[i][t * PP + s0]) = parts[i];
+        for (int i = 0; i < NO; ++i) *reinterpret_cast<bf16x4*>(&pl[BEHIND ? c & 1 : 0][i][t * PP + s0]) = parts[i];
       }
-    }
-    // ---- o^T tiles: rows dv, columns t
-    f32x4 acc[CG][OUT ? CT : 1];
-    if constexpr (OUT) {
+      // ---- c_t S q
 #pragma unroll
       for (int ks = 0; ks < DK / 32; ++ks) {
         bf16x8 sp[CG][NO];
@@ -445,7 +524,7 @@ __global__ __launch_bounds__(256, 2) void attend_kernel(AttendArgs args) {
           bf16x8 qp[NP];
 #pragma unroll
           for (int i = 0; i < NP; ++i) {
-            const __bf16* p = &ql[i][(16 * ti + li) * PQ + 32 * ks + 4 * g];
+            const __bf16* p = &ql[buf][i][(16 * ti + li) * PQ + 32 * ks + 4 * g];
             qp[i] = join(*reinterpret_cast<const bf16x4*>(p), *reinterpret_cast<const bf16x4*>(p + 16));
           }
 #pragma unroll
@@ -455,125 +534,72 @@ __global__ __launch_bounds__(256, 2) void attend_kernel(AttendArgs args) {
               if (i + j < NO)
 #pragma unroll
                 for (int cg = 0; cg < CG; ++cg)
-                  acc[cg][ti] = mfma(sp[cg][i], qp[j], ks == 0 && i == NO - 1 && j == (NP < 2 ? 0 : NO - 1 - i)
-                                                           ? f32x4{0.f, 0.f, 0.f, 0.f} : acc[cg][ti]);
+                  acc[cg][ti] = mfma(sp[cg][i], qp[j], ks == 0 && i == NO - 1 && j == 0 ? f32x4{0.f, 0.f, 0.f, 0.f}
+                                                                                       : acc[cg][ti]);
         }
       }
 #pragma unroll
       for (int ti = 0; ti < CT; ++ti) {
-        const float c = __builtin_amdgcn_exp2f(d.hi[at + 16 * ti + li]) * (1.f + 0.69314718f * d.lo[at + 16 * ti + li]);
+        const float ct = __builtin_amdgcn_exp2f(d.hi[at + 16 * ti + li]) * (1.f + 0.69314718f * d.lo[at + 16 * ti + li]);
 #pragma unroll
-        for (int cg = 0; cg < CG; ++cg) acc[cg][ti] = acc[cg][ti] * c;
+        for (int cg = 0; cg < CG; ++cg) acc[cg][ti] = acc[cg][ti] * ct;
       }
     }
-    // the next chunk's rows: held in registers from here on, past the products
-    // with S, which need the most of them
-    asm volatile("" ::: "memory");
-    if (t0 + C < sg.t1) read_chunk(t0 + C);
-    __builtin_amdgcn_sched_barrier(0);
-    // ---- the wave's columns of v, by columns
-    bf16x4 vr[CG][KB][2][NP];
-#pragma unroll
-    for (int cg = 0; cg < CG; ++cg)
-#pragma unroll
-      for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-        for (int y = 0; y < 2; ++y)
-#pragma unroll
-          for (int i = 0; i < NP; ++i)
-            vr[cg][kb][y][i] = read_column4(&vl[i][(32 * kb + 16 * y + 4 * g + li / 4) * PV + w0 + 16 * cg + 4 * (li % 4)]);
+    if constexpr (RB == 1)
+      if (c + 1 < chunks) read_chunk(c + 1);
     // ---- S = c_C S + k^T (w v)
+    bf16x8 vs[CG][3];
+#pragma unroll
+    for (int cg = 0; cg < CG; ++cg) {
+      bf16x4 half[2][3];
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+#pragma unroll
+        for (int i = 0; i < NP; ++i)
+          vr[cg][y][i] = read_column4(&vl[buf][i][(16 * y + 4 * g + li / 4) * PV + w0 + 16 * cg + 4 * (li % 4)]);
+        f32x4 x = widen4(vr[cg][y][0]);
+#pragma unroll
+        for (int i = 1; i < NP; ++i) x = x + widen4(vr[cg][y][i]);
+        x = x * *reinterpret_cast<const f32x4*>(&d.w[at + 16 * y + 4 * g]);
+        split4<3>(x, half[y]);
+      }
+#pragma unroll
+      for (int i = 0; i < 3; ++i) vs[cg][i] = join(half[0][i], half[1][i]);
+    }
     const float gamma = __builtin_amdgcn_exp2f(d.hi[at + C - 1]) * (1.f + 0.69314718f * d.lo[at + C - 1]);   // c_C
 #pragma unroll
-    for (int cg = 0; cg < CG; ++cg)
+    for (int I = 0; I < KT; ++I) {
+      bf16x8 kp[NP];
 #pragma unroll
-      for (int I = 0; I < KT; ++I) S[cg][I] = S[cg][I] * gamma;
-#pragma unroll
-    for (int kb = 0; kb < KB; ++kb) {
-      bf16x8 vs[CG][3];
-#pragma unroll
-      for (int cg = 0; cg < CG; ++cg) {
-        bf16x4 half[2][3];
-#pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          f32x4 x = widen4(vr[cg][kb][y][0]);
-#pragma unroll
-          for (int i = 1; i < NP; ++i) x = x + widen4(vr[cg][kb][y][i]);
-          x = x * *reinterpret_cast<const f32x4*>(&d.w[at + 32 * kb + 16 * y + 4 * g]);
-          split4<3>(x, half[y]);
-        }
-#pragma unroll
-        for (int i = 0; i < 3; ++i) vs[cg][i] = join(half[0][i], half[1][i]);
+      for (int i = 0; i < NP; ++i) {
+        const __bf16* p = &kl[buf][i][(4 * g + li / 4) * PK + 16 * I + 4 * (li % 4)];
+        kp[i] = join(read_column4(p), read_column4(p + 16 * PK));
       }
 #pragma unroll
-      for (int I = 0; I < KT; ++I) {
-        bf16x8 kp[NP];
+      for (int cg = 0; cg < CG; ++cg) S[cg][I] = S[cg][I] * gamma;
 #pragma unroll
-        for (int i = 0; i < NP; ++i) {
-          const __bf16* p = &kl[i][(32 * kb + 4 * g + li / 4) * PK + 16 * I + 4 * (li % 4)];
-          kp[i] = join(read_column4(p), read_column4(p + 16 * PK));
-        }
+      for (int i = NP - 1; i >= 0; --i)
 #pragma unroll
-        for (int i = NP - 1; i >= 0; --i)
+        for (int j = 2; j >= 0; --j)
+          if (i + j < 3)
 #pragma unroll
-          for (int j = 2; j >= 0; --j)
-            if (i + j < 3)
-#pragma unroll
-              for (int cg = 0; cg < CG; ++cg) S[cg][I] = mfma(kp[i], vs[cg][j], S[cg][I]);
+            for (int cg = 0; cg < CG; ++cg) S[cg][I] = mfma(kp[i], vs[cg][j], S[cg][I]);
+    }
+    const bool round = at + C == ROUND;             // the next chunk opens a round of decays
+    if constexpr (RB == 2) {
+      if (round && c + 1 < chunks) put_decays((c + 1) * C, ((c + 1) / (ROUND / C)) & 1);
+    } else {
+      __syncthreads();
+      if constexpr (OUT && !BEHIND) finish(c, 0);
+      if (c + 1 < chunks) {
+        put_chunk(c + 1, 0);
+        if (round) put_decays((c + 1) * C, 0);
       }
     }
+  }
+  if constexpr (OUT && BEHIND) {
     __syncthreads();
-    if constexpr (OUT) {
-      // ---- P v
-#pragma unroll
-      for (int ti = 0; ti < CT; ++ti) {
-#pragma unroll
-        for (int kb = 0; kb <= ti / 2; ++kb) {
-          bf16x8 pp[NO];
-#pragma unroll
-          for (int i = 0; i < NO; ++i) {
-            const __bf16* p = &pl[i][(16 * ti + li) * PP + 32 * kb + 4 * g];
-            pp[i] = join(*reinterpret_cast<const bf16x4*>(p), *reinterpret_cast<const bf16x4*>(p + 16));
-          }
-#pragma unroll
-          for (int i = NO - 1; i >= 0; --i)
-#pragma unroll
-            for (int j = NP - 1; j >= 0; --j)
-              if (i + j < NO)
-#pragma unroll
-                for (int cg = 0; cg < CG; ++cg)
-                  acc[cg][ti] = mfma(join(vr[cg][kb][0][j], vr[cg][kb][1][j]), pp[i], acc[cg][ti]);
-        }
-      }
-      // ---- the output: four columns of a token per lane and tile
-      const auto ob = rows_of(a.o, (t0 * a.o_stride + hv) * B, (uint32_t)(live - 1) * ostep + vcols * B);
-      uint32_t oo = li * ostep + (w0 + 4 * g) * B;
-#pragma unroll
-      for (int ti = 0; ti < CT; ++ti) {
-#pragma unroll
-        for (int cg = 0; cg < CG; ++cg) {
-          const f32x4 x = acc[cg][ti];
-          const int left = vcols - (w0 + 16 * cg + 4 * g);             // columns to write
-          if constexpr (VEC) {
-            const uint32_t e = left > 0 ? oo + 16 * cg * B : kNowhere;
-            if constexpr (IO == IO_F32)
-              __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, x), ob, e, 0, 0);
-            else
-              __builtin_amdgcn_raw_buffer_store_b64(u32x2{pair16<IO>(x[0], x[1]), pair16<IO>(x[2], x[3])}, ob, e, 0, 0);
-          } else {
-#pragma unroll
-            for (int v = 0; v < 4; ++v) {
-              const uint32_t e = v < left ? oo + (16 * cg + v) * B : kNowhere;
-              if constexpr (IO == IO_F32)
-                __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x[v]), ob, e, 0, 0);
-              else
-                __builtin_amdgcn_raw_buffer_store_b16(to16<IO>(x[v]), ob, e, 0, 0);
-            }
-          }
-        }
-        oo += 16 * ostep;
-      }
-    }
+    finish(chunks - 1, (chunks - 1) & 1);
   }
 
   if (!OUT || sg.j == sg.n - 1) {
@@ -635,17 +661,17 @@ namespace {
 // half a CU at 64.
 int slice_width(int io, int dv) { return io == IO_F32 || dv <= 64 ? 64 : 128; }
 
-template <int IO, int DK, int CG, bool VEC>
+template <int IO, int DK, int NW, int CG, bool VEC>
 hipError_t launch_instance(const AttendArgs& args, unsigned blocks, hipStream_t s) {
   const SlotArgs& a = args.s;
   if (args.seg_len) {
-    hipLaunchKernelGGL((dev::attend_kernel<IO, DK, CG, VEC, false>), dim3(blocks), dim3(256), 0, s, args);
+    hipLaunchKernelGGL((dev::attend_kernel<IO, DK, NW, CG, VEC, false>), dim3(blocks), dim3(64 * NW), 0, s, args);
     const int64_t quads = (int64_t)a.heads * a.dv * DK / 4, per = (quads + 255) / 256;
     if (per * a.seqs > INT32_MAX) return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL(dev::combine_kernel, dim3((unsigned)(per * a.seqs)), dim3(256), 0, s, args,
                        (int)per, quads);
   }
-  hipLaunchKernelGGL((dev::attend_kernel<IO, DK, CG, VEC, true>), dim3(blocks), dim3(256), 0, s, args);
+  hipLaunchKernelGGL((dev::attend_kernel<IO, DK, NW, CG, VEC, true>), dim3(blocks), dim3(64 * NW), 0, s, args);
   return hipGetLastError();
 }
 
@@ -653,10 +679,10 @@ template <int IO, int DK>
 hipError_t launch_width(const AttendArgs& args, unsigned blocks, hipStream_t s) {
   if constexpr (IO != IO_F32)
     if (slice_width(IO, args.s.dv) == 128)
-      return args.wide ? launch_instance<IO, DK, 2, true>(args, blocks, s)
-                       : launch_instance<IO, DK, 2, false>(args, blocks, s);
-  return args.wide ? launch_instance<IO, DK, 1, true>(args, blocks, s)
-                   : launch_instance<IO, DK, 1, false>(args, blocks, s);
+      return args.wide ? launch_instance<IO, DK, LSQ_NW, 8 / LSQ_NW, true>(args, blocks, s)
+                       : launch_instance<IO, DK, LSQ_NW, 8 / LSQ_NW, false>(args, blocks, s);
+  return args.wide ? launch_instance<IO, DK, 4, 1, true>(args, blocks, s)
+                   : launch_instance<IO, DK, 4, 1, false>(args, blocks, s);
 }
 
 }  // namespace
