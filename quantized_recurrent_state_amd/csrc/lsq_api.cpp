@@ -628,12 +628,13 @@ lsq_status lsq_attend(lsq_state* st, const lsq_token_batch* batch, void* workspa
   lsq::AttendArgs a{};
   a.s = slot_args(st, batch);
   a.seg_len = p.seg_len;
+  a.segments = p.segments;
   a.ws = static_cast<float*>(workspace);
   a.ws_decay = p.workspace ? reinterpret_cast<float*>(static_cast<char*>(workspace) + p.state_bytes) : nullptr;
   a.slices = p.slices;
   a.wide = aligned16(batch->v) && batch->v_stride * e % 16 == 0 && c.dv * e % 16 == 0 &&
            aligned_to(batch->o, quad) && batch->o_stride % 4 == 0;
-  return slot_status(lsq::launch_attend(a, p.segments, batch->io, c.dk, hs), "attend launch");
+  return slot_status(lsq::launch_attend(a, batch->io, c.dk, hs), "attend launch");
 }
 
 lsq_status lsq_step_slots(lsq_state* st, const lsq_token_batch* batch, void* stream) {

@@ -23,9 +23,6 @@
 #include "lsq_slots.h"
 #include "lsq_slots_dev.h"
 
-#ifndef LSQ_NW
-#define LSQ_NW 8
-#endif
 namespace lsq {
 namespace dev {
 
@@ -181,47 +178,71 @@ __device__ __forceinline__ u32x4 keep_elements(u32x4 x, int n) {
   return x;
 }
 
-// The segment a workgroup takes: sequence i, its j-th of n segments.  With a
-// segment length L, sequence i's segments begin at number cu[i] / L + i (its
-// length over L rounded up is at most the distance to the next).
+// The segment a workgroup takes: sequence i, its j-th of n segments (n = 0:
+// none).  With a segment length L, a sequence of more than 2 L tokens is cut
+// into its length over L, rounded up.
 struct Segment {
   int i, j, n;
   int64_t t0, t1;
 };
 
-__device__ __forceinline__ Segment segment_of(const SlotArgs& a, int64_t L, int64_t s) {
+__device__ __forceinline__ int segments_of(const Span& sp, int64_t L) {
+  const int64_t len = sp.t1 > sp.t0 ? sp.t1 - sp.t0 : 0;
+  return L == 0 || len <= 2 * L ? len > 0 : (int)((len + L - 1) / L);
+}
+
+// Segments are numbered without gaps (idle workgroups between busy ones would
+// leave whole shader engines idle): a wave counts 64 sequences at a time.
+__device__ __forceinline__ int segments_upto(const SlotArgs& a, int64_t L, int i0, int lane) {
+  int n = i0 + lane < a.seqs ? segments_of(span_of(a, i0 + lane), L) : 0;
+#pragma unroll
+  for (int o = 1; o < 64; o *= 2) {
+    const int up = __shfl_up(n, o);
+    if (lane >= o) n += up;
+  }
+  return n;
+}
+
+__device__ __forceinline__ Segment segment_of(const SlotArgs& a, int64_t L, int64_t s, int lane) {
   Segment g{};
   if (L == 0) {
     g.i = (int)s;
   } else {
-    int lo = 0, hi = a.seqs - 1;             // the last sequence that begins at or before s
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) / 2;
-      if (span_of(a, mid).t0 / L + mid <= s) lo = mid; else hi = mid - 1;
+    for (int i0 = 0;; i0 += 64) {
+      if (i0 >= a.seqs) return g;
+      const int n = segments_upto(a, L, i0, lane), all = __builtin_amdgcn_readlane(n, 63);
+      if (s < all) {
+        const int at = __builtin_ctzll(__ballot(n > s));
+        g.i = i0 + at;
+        g.j = (int)s - (at ? __shfl(n, at - 1) : 0);
+        g.j = __builtin_amdgcn_readfirstlane(g.j);
+        break;
+      }
+      s -= all;
     }
-    g.i = lo;
   }
   const Span sp = span_of(a, g.i);
-  const int64_t len = sp.t1 > sp.t0 ? sp.t1 - sp.t0 : 0;
-  if (L == 0) {
-    g.n = len > 0;
-    g.t0 = sp.t0;
-    g.t1 = sp.t1;
-  } else {
-    const int64_t j = s - (sp.t0 / L + g.i);
-    g.n = (int)((len + L - 1) / L);
-    g.j = j < 0 || j >= g.n ? g.n : (int)j;
-    g.t0 = sp.t0 + (int64_t)g.j * L;
-    g.t1 = g.t0 + L < sp.t1 ? g.t0 + L : sp.t1;
-  }
+  g.n = segments_of(sp, L);
+  g.t0 = sp.t0 + (int64_t)g.j * L;
+  g.t1 = g.n < 2 || g.t0 + L > sp.t1 ? sp.t1 : g.t0 + L;
   return g;
 }
 
-// Block number -> work item, neighbours in one XCD (blocks go to the eight
-// XCDs in turn): heads that share q and k then share an L2.
-__device__ __forceinline__ int64_t xcd_item(int64_t b, int64_t n) {
-  const int64_t q = n / 8, r = n % 8, x = b % 8, p = b / 8;
-  return x * q + (x < r ? x : r) + p;
+// Block number -> segment and row (a head's slice of value columns).  Blocks go
+// to the eight XCDs in turn.  Where the rows divide by eight an XCD gets an
+// eighth of them in every segment: its heads share q and k in its L2, and
+// sequences of different lengths load the XCDs alike.  Segments come in order,
+// so that the numbers without one are the last blocks.
+struct Item {
+  int64_t seg;
+  int row;
+};
+
+__device__ __forceinline__ Item item_of(int64_t b, int rows) {
+  if (rows % 8) return {b / rows, (int)(b % rows)};
+  const int own = rows / 8;
+  const int64_t p = b / 8;
+  return {p / own, (int)(b % 8) * own + (int)(p % own)};
 }
 
 // One workgroup walks the chunks of one segment of one head, 64 CG value
@@ -252,12 +273,11 @@ __global__ __launch_bounds__(64 * NW, NW / 2) void attend_kernel(AttendArgs args
 
   const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, li = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int64_t item = xcd_item(blockIdx.x, gridDim.x);
-  const int slice = (int)(item % args.slices);
-  const int h = (int)(item / args.slices % a.heads);
-  const int64_t seg = item / args.slices / a.heads;
-  const Segment sg = segment_of(a, args.seg_len, seg);
-  if (sg.j >= sg.n || (!OUT && sg.j == sg.n - 1)) return;
+  const Item item = item_of(blockIdx.x, args.slices * a.heads);
+  const int64_t seg = item.seg;
+  const int h = item.row / args.slices, slice = item.row % args.slices;
+  const Segment sg = segment_of(a, args.seg_len, seg, lane);
+  if (sg.n == 0 || (!OUT && sg.j == sg.n - 1)) return;
   const int slot = slot_of(a.slots, sg.i, a.nslots, lane);
   if (slot == kPadded) return;
   const int d0 = slice * T::DV, vcols = a.dv - d0 < T::DV ? a.dv - d0 : T::DV;   // the slice's columns
@@ -626,29 +646,33 @@ __global__ __launch_bounds__(64 * NW, NW / 2) void attend_kernel(AttendArgs args
 
 // The states before each segment of a sequence of several: S_0 is the slot's
 // (or 0), S_{j+1} = decay_j S_j + writes_j; segment j's writes are replaced by
-// S_j.  One thread per four elements of a head, one pass over the segments.
+// S_j.  A thread takes four elements through all the segments.
 __global__ __launch_bounds__(256) void combine_kernel(AttendArgs args, int blocks, int64_t quads) {
   const SlotArgs& a = args.s;
-  const int lane = threadIdx.x & 63;
   const int b = blockIdx.x % blocks, i = blockIdx.x / blocks;
   const Span sp = span_of(a, i);
-  const int64_t L = args.seg_len, first = sp.t0 / L + i;
-  const int64_t n = sp.t1 > sp.t0 ? (sp.t1 - sp.t0 + L - 1) / L : 0;
+  const int n = segments_of(sp, args.seg_len);
   if (n < 2) return;
-  const int slot = slot_of(a.slots, i, a.nslots, lane);
-  const int64_t q = (int64_t)b * 256 + threadIdx.x;     // quad of the sequence's states
-  if (slot < 0 || q >= quads) return;
-  const int h = (int)(q / (quads / a.heads));
-  f32x4 S = {0.f, 0.f, 0.f, 0.f};
-  if (!(a.fresh && a.fresh[i])) S = reinterpret_cast<const f32x4*>(a.S)[slot * quads + q];
-  f32x4* ws = reinterpret_cast<f32x4*>(args.ws) + first * quads + q;
-  f32x4 x = ws[0];
-  for (int64_t j = 0; j < n; ++j) {
-    ws[j * quads] = S;
-    if (j + 1 < n) {
-      const f32x4 next = j + 2 < n ? ws[(j + 1) * quads] : x;   // the last segment's writes are not needed
-      S = S * args.ws_decay[(first + j) * a.heads + h] + x;
-      x = next;
+  const int lane = threadIdx.x & 63, slot = slot_of(a.slots, i, a.nslots, lane);
+  if (slot < 0) return;
+  int64_t first = 0;                             // the sequence's first segment
+  for (int i0 = 0; i0 < i; i0 += 64)
+    first += __shfl(segments_upto(a, args.seg_len, i0, lane), i - i0 > 64 ? 63 : i - i0 - 1);
+  const int64_t per_head = quads / a.heads;
+  const bool fresh = a.fresh && a.fresh[i];
+  for (int64_t q = (int64_t)b * 256 + threadIdx.x; q < quads; q += (int64_t)blocks * 256) {
+    const float* decay = args.ws_decay + first * a.heads + q / per_head;
+    f32x4 S = {0.f, 0.f, 0.f, 0.f};
+    if (!fresh) S = reinterpret_cast<const f32x4*>(a.S)[slot * quads + q];
+    f32x4* ws = reinterpret_cast<f32x4*>(args.ws) + first * quads + q;
+    f32x4 x = ws[0];
+    for (int j = 0; j < n; ++j) {
+      ws[j * quads] = S;
+      if (j + 1 < n) {
+        const f32x4 next = j + 2 < n ? ws[(j + 1) * quads] : x;   // the last segment's writes are not needed
+        S = S * decay[(int64_t)j * a.heads] + x;
+        x = next;
+      }
     }
   }
 }
@@ -666,8 +690,8 @@ hipError_t launch_instance(const AttendArgs& args, unsigned blocks, hipStream_t 
   const SlotArgs& a = args.s;
   if (args.seg_len) {
     hipLaunchKernelGGL((dev::attend_kernel<IO, DK, NW, CG, VEC, false>), dim3(blocks), dim3(64 * NW), 0, s, args);
-    const int64_t quads = (int64_t)a.heads * a.dv * DK / 4, per = (quads + 255) / 256;
-    if (per * a.seqs > INT32_MAX) return hipErrorInvalidConfiguration;
+    const int64_t quads = (int64_t)a.heads * a.dv * DK / 4, most = 4096 / a.seqs + 1;
+    const int64_t per = (quads + 255) / 256 < most ? (quads + 255) / 256 : most;
     hipLaunchKernelGGL(dev::combine_kernel, dim3((unsigned)(per * a.seqs)), dim3(256), 0, s, args,
                        (int)per, quads);
   }
@@ -679,41 +703,36 @@ template <int IO, int DK>
 hipError_t launch_width(const AttendArgs& args, unsigned blocks, hipStream_t s) {
   if constexpr (IO != IO_F32)
     if (slice_width(IO, args.s.dv) == 128)
-      return args.wide ? launch_instance<IO, DK, LSQ_NW, 8 / LSQ_NW, true>(args, blocks, s)
-                       : launch_instance<IO, DK, LSQ_NW, 8 / LSQ_NW, false>(args, blocks, s);
+      return args.wide ? launch_instance<IO, DK, 8, 1, true>(args, blocks, s)
+                       : launch_instance<IO, DK, 8, 1, false>(args, blocks, s);
   return args.wide ? launch_instance<IO, DK, 4, 1, true>(args, blocks, s)
                    : launch_instance<IO, DK, 4, 1, false>(args, blocks, s);
 }
 
 }  // namespace
 
-#ifndef LSQ_ATT_TARGET
-#define LSQ_ATT_TARGET 1024
-#endif
-#ifndef LSQ_ATT_MIN
-#define LSQ_ATT_MIN 512
-#endif
-
 AttendPlan attend_plan(int64_t tokens, int32_t seqs, int32_t heads, int32_t dk, int32_t dv, int io) {
   AttendPlan p{};
   const int width = slice_width(io, dv);
   p.slices = (dv + width - 1) / width;
-  const int64_t rows = (int64_t)heads * p.slices;
-  int64_t L = (tokens * rows / LSQ_ATT_TARGET + 63) / 64 * 64;
-  if (L < LSQ_ATT_MIN) L = LSQ_ATT_MIN;
   p.segments = seqs;
-  if (L < tokens) {
+  // Segments of a 512th of the work (two workgroups on each of 256 CUs), 512
+  // tokens at least.  The host does not see the lengths: a batch of fewer than
+  // eight segments' tokens is taken whole, in a longer one the kernels cut the
+  // sequences of more than two segments.
+  int64_t L = (tokens * heads * p.slices / 512 + 63) / 64 * 64;
+  if (L < 512) L = 512;
+  if (tokens >= 8 * L) {
     p.seg_len = L;
     p.segments = tokens / L + seqs;
-    const int64_t state = (int64_t)heads * dv * dk * 4;
-    p.state_bytes = p.segments * state;
+    p.state_bytes = p.segments * heads * dv * dk * 4;
     p.workspace = (size_t)(p.state_bytes + p.segments * heads * 4);
   }
   return p;
 }
 
-hipError_t launch_attend(const AttendArgs& args, int64_t segments, int io, int dk, hipStream_t s) {
-  const int64_t blocks = segments * args.s.heads * args.slices;
+hipError_t launch_attend(const AttendArgs& args, int io, int dk, hipStream_t s) {
+  const int64_t blocks = args.segments * args.s.heads * args.slices;
   if (blocks > INT32_MAX) return hipErrorInvalidConfiguration;
   const unsigned n = (unsigned)blocks;
   if (io == IO_F32) return dk == 128 ? launch_width<IO_F32, 128>(args, n, s) : launch_width<IO_F32, 64>(args, n, s);

@@ -32,6 +32,7 @@ struct SlotArgs {
 struct AttendArgs {
   SlotArgs s;
   int64_t seg_len;         // tokens per segment, a multiple of 64; 0: whole sequences
+  int64_t segments;        // upper bound of their number
   float* ws;               // [segments][heads][dv][dk], then ws_decay (null without segments)
   float* ws_decay;         // [segments][heads]
   int32_t slices;          // workgroups over a head's value columns
@@ -59,7 +60,7 @@ struct CopyArgs {
 };
 
 hipError_t launch_walk(const SlotArgs& a, int io, int dk, int delta, int diag, hipStream_t s);
-hipError_t launch_attend(const AttendArgs& a, int64_t segments, int io, int dk, hipStream_t s);
+hipError_t launch_attend(const AttendArgs& a, int io, int dk, hipStream_t s);
 hipError_t launch_store_slots(const CopyArgs& a, int bits, int dk, hipStream_t s);
 hipError_t launch_load_slots(const CopyArgs& a, int bits, int dk, hipStream_t s);
 
