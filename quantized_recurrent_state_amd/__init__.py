@@ -347,60 +347,7 @@ class LsqState:
         return self
 
 
-    # ---- slots: sequence b of the handle's batch axis is slot b (include/lsq.h)
-
-    def _on_device(self, stream, call):
-        """call(stream) with the state's device current and, for another stream than the
-        current one, with it current too (what is allocated in the call belongs to it)."""
-        import torch
-        index = (self.f32 if self.codes is None else self.codes).device.index
-        if stream is not None:
-            if not isinstance(stream, torch.cuda.Stream):
-                stream = torch.cuda.ExternalStream(int(stream), device=index)
-            with torch.cuda.stream(stream):
-                return call(stream)
-        if index == torch.cuda.current_device():
-            return call(torch.cuda.current_stream(index))
-        with torch.cuda.device(index):
-            return call(torch.cuda.current_stream(index))
-
-    def _token_batch(self, q, k, v, alpha, beta, cu_seqlens, slots, fresh, o):
-        """Checks a token batch's tensors; returns (lsq_token_batch, o)."""
-        import torch
-        c = self.cfg
-        if c.bits != 32:
-            raise ValueError("token batches run on an fp32 state (bits 32)")
-        dev = self.f32.device
-        io = {torch.float32: IO_F32, torch.float16: IO_F16, torch.bfloat16: IO_BF16}.get(q.dtype)
-        if io is None:
-            raise ValueError(f"q has type {q.dtype}, expected float32, float16 or bfloat16")
-        if q.dim() != 3:
-            raise ValueError(f"q has shape {tuple(q.shape)}, expected (tokens, qk_heads, {c.dk})")
-        n, hk = int(q.shape[0]), int(q.shape[1])
-        if hk == 0 or c.heads % hk:
-            raise ValueError(f"q has {hk} heads, which must divide the state's {c.heads}")
-        sq = _check_rows("q", q, (n, hk, c.dk), q.dtype, dev)
-        sk = _check_rows("k", k, (n, hk, c.dk), q.dtype, dev)
-        sv = _check_rows("v", v, (n, c.heads, c.dv), q.dtype, dev)
-        _check_on("alpha", alpha, (n, c.heads, c.dk) if c.decay == DECAY_DIAG else (n, c.heads),
-                  torch.float32, dev)
-        _check_on("beta", beta, (n, c.heads), torch.float32, dev)
-        if cu_seqlens is None:
-            m = n
-        else:
-            if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
-                raise ValueError("cu_seqlens must hold seqs + 1 offsets")
-            m = int(cu_seqlens.shape[0]) - 1
-            _check_on("cu_seqlens", cu_seqlens, (m + 1,), torch.int32, dev)
-        if slots is not None:
-            _check_on("slots", slots, (m,), torch.int32, dev)
-        if fresh is not None:
-            _check_on("fresh", fresh, (m,), torch.uint8 if fresh.dtype != torch.bool else torch.bool, dev)
-        if o is None:
-            o = torch.empty((n, c.heads, c.dv), dtype=q.dtype, device=dev)
-        so = _check_rows("o", o, (n, c.heads, c.dv), q.dtype, dev)
-        return token_batch(io, hk, m, n, q, k, v, alpha, beta, o, sq, sk, sv, so, cu_seqlens, slots,
-                           fresh), o
+    # ---- slots: sequence b of the handle's batch axis is slot b (include/lsq.h, slots.py)
 
     def attend(self, q, k, v, alpha, beta, cu_seqlens, slots=None, fresh=None, o=None, stream=None):
         """Linear attention over a packed batch of prompts (``lsq_attend``), on an fp32 state.
@@ -411,72 +358,36 @@ class LsqState:
         [seqs] starts those sequences from S = 0.  Returns o [tokens, heads, dv] in q's type; the
         slots hold the sequences' final states.  Rows of o outside every sequence, and those of
         negative slots, are not written."""
-        def call(s):
-            import torch
-            b, out = self._token_batch(q, k, v, alpha, beta, cu_seqlens, slots, fresh, o)
-            nb = lsq_attend_workspace(self.handle, b)
-            ws = torch.empty(nb, dtype=torch.uint8, device=out.device) if nb else None
-            lsq_attend(self.handle, b, ws, s)
-            return out
-        return self._on_device(stream, call)
+        return _slots().attend(self, q, k, v, alpha, beta, cu_seqlens, slots, fresh, o, stream)
 
     def step_slots(self, q, k, v, alpha, beta, slots=None, fresh=None, o=None, stream=None):
         """One token for each listed slot (``lsq_step_slots``), on an fp32 state: the tensors of
         ``attend`` with one token per entry.  Returns o [entries, heads, dv]."""
-        def call(s):
-            b, out = self._token_batch(q, k, v, alpha, beta, None, slots, fresh, o)
-            lsq_step_slots(self.handle, b, s)
-            return out
-        return self._on_device(stream, call)
-
-    def _copy_slots(self, fn, dst, src, dst_slots, src_slots, stream):
-        import torch
-        dev = (self.f32 if self.codes is None else self.codes).device
-        other = src if dst is self else dst
-        if not isinstance(other, LsqState):
-            raise TypeError("the other state must be an LsqState")
-        if (other.f32 if other.codes is None else other.codes).device != dev:
-            raise ValueError("both states must be on one device")
-        m = min(dst.cfg.batch, src.cfg.batch)
-        for t in (dst_slots, src_slots):
-            if t is not None:
-                m = int(t.shape[0])
-        for name, t in (("dst_slots", dst_slots), ("src_slots", src_slots)):
-            if t is not None:
-                _check_on(name, t, (m,), torch.int32, dev)
-        self._on_device(stream, lambda s: fn(dst.handle, src.handle, m, dst_slots, src_slots, s))
+        return _slots().step_slots(self, q, k, v, alpha, beta, slots, fresh, o, stream)
 
     def store_slots(self, src, slots=None, src_slots=None, stream=None):
         """Quantise slots of the fp32 state ``src`` into this quantised state
         (``lsq_state_store_slots``): entry i takes src_slots[i] to slots[i] (int32 device tensors;
         default: entry i is slot i)."""
-        self._copy_slots(lsq_state_store_slots, self, src, slots, src_slots, stream)
+        _slots().copy(lsq_state_store_slots, self, src, slots, src_slots, stream)
         return self
 
     def load_slots(self, dst, slots=None, dst_slots=None, stream=None):
         """Read slots of this quantised state back into slots of the fp32 state ``dst``
         (``lsq_state_load_slots``): entry i takes slots[i] to dst_slots[i].  Returns dst."""
-        self._copy_slots(lsq_state_load_slots, dst, self, dst_slots, slots, stream)
+        _slots().copy(lsq_state_load_slots, dst, self, dst_slots, slots, stream)
         return dst
 
 
-def _check_on(name, t, shape, dtype, device):
-    if t.dtype != dtype or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor on {device}")
-    if t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+_slots_module = None
 
 
-def _check_rows(name, t, shape, dtype, device):
-    """A [tokens, heads, d] tensor whose tokens may be strided; returns the token stride."""
-    if t.dtype != dtype or t.device != device:
-        raise ValueError(f"{name} must be a {dtype} tensor on {device}")
-    if t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    row, head, one = t.stride()
-    if (one != 1 and shape[2] != 1) or (head != shape[2] and shape[1] != 1):
-        raise ValueError(f"{name} must be contiguous within each token")
-    return row if shape[0] > 1 else shape[1] * shape[2]
+def _slots():
+    global _slots_module
+    if _slots_module is None:
+        from . import slots
+        _slots_module = slots
+    return _slots_module
 
 
 def _check_tensor(name, t, shape):

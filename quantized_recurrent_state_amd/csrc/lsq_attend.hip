@@ -84,7 +84,7 @@ __device__ __forceinline__ void split4(f32x4 x, bf16x4 (&p)[N]) {
 }
 
 // Four bf16 values as fp32.
-__device__ __forceinline__ f32x4 widen4(bf16x4 p) {
+__device__ __forceinline__ f32x4 widen_bf16x4(bf16x4 p) {
   const uint64_t b = __builtin_bit_cast(uint64_t, p);
   const uint32_t lo = (uint32_t)b, hi = (uint32_t)(b >> 32);
   return f32x4{__uint_as_float(lo << 16), __uint_as_float(lo & 0xFFFF0000u), __uint_as_float(hi << 16),
@@ -577,9 +577,9 @@ __global__ __launch_bounds__(64 * NW, NW / 2) void attend_kernel(AttendArgs args
 #pragma unroll
         for (int i = 0; i < NP; ++i)
           vr[cg][y][i] = read_column4(&vl[buf][i][(16 * y + 4 * g + li / 4) * PV + w0 + 16 * cg + 4 * (li % 4)]);
-        f32x4 x = widen4(vr[cg][y][0]);
+        f32x4 x = widen_bf16x4(vr[cg][y][0]);
 #pragma unroll
-        for (int i = 1; i < NP; ++i) x = x + widen4(vr[cg][y][i]);
+        for (int i = 1; i < NP; ++i) x = x + widen_bf16x4(vr[cg][y][i]);
         x = x * *reinterpret_cast<const f32x4*>(&d.w[at + 16 * y + 4 * g]);
         split4<3>(x, half[y]);
       }

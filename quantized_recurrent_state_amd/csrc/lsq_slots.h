@@ -57,9 +57,10 @@ struct CopyArgs {
   const int32_t* src_slots;
   int32_t count, dst_n, src_n;   // entries; slots of each handle
   int32_t heads, dv, group, sfmt;
+  int32_t nt;              // the read-back states take the non-temporal hint
 };
 
-hipError_t launch_walk(const SlotArgs& a, int io, int dk, int delta, int diag, hipStream_t s);
+hipError_t launch_walk(const SlotArgs& a, int io, int dk, int delta, int diag, int nt, hipStream_t s);
 hipError_t launch_attend(const AttendArgs& a, int io, int dk, hipStream_t s);
 hipError_t launch_store_slots(const CopyArgs& a, int bits, int dk, hipStream_t s);
 hipError_t launch_load_slots(const CopyArgs& a, int bits, int dk, hipStream_t s);

@@ -10,6 +10,24 @@
 namespace lsq {
 namespace dev {
 
+// The state's rows.  NT: with the non-temporal hint, for a state that does not
+// stay in the last-level cache between steps.
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+template <bool NT>
+__device__ __forceinline__ f32x4 load_state(const float* p) {
+  if constexpr (NT) return __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(p));
+  return *reinterpret_cast<const f32x4*>(p);
+}
+
+template <bool NT>
+__device__ __forceinline__ void store_state(float* p, f32x4 x) {
+  if constexpr (NT)
+    __builtin_nontemporal_store(x, reinterpret_cast<f32x4*>(p));
+  else
+    *reinterpret_cast<f32x4*>(p) = x;
+}
+
 // Token walk.  For every token of a sequence, Eq. (1) row by row,
 //   S' = fl(S alpha_c),  u = S'.k,  w = fl(beta fl(v - delta u)),
 //   S  = fma(w, k_c, S'), o = S.q,
@@ -17,9 +35,9 @@ namespace dev {
 // cover a row (lane lc owns columns 4 lc .. 4 lc + 3 of each 64), so that a
 // wave's state loads are whole 256-byte runs and both dot products end in a
 // 16-lane DPP butterfly; a wave owns 4 R rows, all loaded before the first
-// token.  With one token it is the recurrent form: bound by the state's bytes,
+// token, and reads the next token's vectors during the current one's sums.  With one token it is the recurrent form: bound by the state's bytes,
 // read and written once.
-template <int IO, int DK, int DELTA, int DIAG, int R>
+template <int IO, int DK, int DELTA, int DIAG, int R, bool NT>
 __global__ __launch_bounds__(256) void walk_kernel(SlotArgs a, int row_blocks) {
   constexpr int NJ = DK / 64, EPT = DK / 16;
   const int lane = threadIdx.x & 63, lr = lane >> 4, lc = lane & 15;
@@ -49,29 +67,51 @@ __global__ __launch_bounds__(256) void walk_kernel(SlotArgs a, int row_blocks) {
     const int row = row0 + 4 * r + lr;
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (!fresh && row < a.dv)
-        x = *reinterpret_cast<const float4*>(S + (int64_t)row * DK + 64 * j + 4 * lc);
-      s[r][4 * j] = x.x; s[r][4 * j + 1] = x.y; s[r][4 * j + 2] = x.z; s[r][4 * j + 3] = x.w;
+      f32x4 x = {0.f, 0.f, 0.f, 0.f};
+      if (!fresh && row < a.dv) x = load_state<NT>(S + (int64_t)row * DK + 64 * j + 4 * lc);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[r][4 * j + e] = x[e];
     }
   }
   const int64_t hk = (int64_t)(h / a.share) * DK;
+  struct Token {
+    typename Raw<IO>::Four k[NJ], q[NJ];
+    float4 a[DIAG ? NJ : 1];
+    typename Raw<IO>::One v[R];
+    float alpha, beta;
+  };
+  auto read = [&](int64_t t) {
+    Token x;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      x.k[j] = raw4<IO>(a.k, t * a.k_stride + hk + 64 * j + 4 * lc);
+      x.q[j] = raw4<IO>(a.q, t * a.q_stride + hk + 64 * j + 4 * lc);
+      if constexpr (DIAG) x.a[j] = raw4<IO_F32>(a.alpha, (t * a.heads + h) * DK + 64 * j + 4 * lc);
+    }
+    if constexpr (!DIAG) x.alpha = a.alpha[t * a.heads + h];
+    x.beta = a.beta[t * a.heads + h];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {                // rows behind dv repeat the last
+      const int row = row0 + 4 * r + lr;
+      x.v[r] = raw1<IO>(a.v, t * a.v_stride + (int64_t)h * a.dv + (row < a.dv ? row : a.dv - 1));
+    }
+    return x;
+  };
+  Token next = read(sp.t0);
   for (int64_t t = sp.t0; t < sp.t1; ++t) {
+    const Token x = next;
+    if (t + 1 < sp.t1) next = read(t + 1);
     float kk[EPT], qq[EPT], aa[DIAG ? EPT : 1], vv[R];
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
-      load4<IO>(&kk[4 * j], a.k, t * a.k_stride + hk + 64 * j + 4 * lc);
-      load4<IO>(&qq[4 * j], a.q, t * a.q_stride + hk + 64 * j + 4 * lc);
-      if constexpr (DIAG)
-        load4<IO_F32>(&aa[4 * j], a.alpha, (t * a.heads + h) * DK + 64 * j + 4 * lc);
+      widen4<IO>(&kk[4 * j], x.k[j]);
+      widen4<IO>(&qq[4 * j], x.q[j]);
+      if constexpr (DIAG) widen4<IO_F32>(&aa[4 * j], x.a[j]);
     }
-    if constexpr (!DIAG) aa[0] = a.alpha[t * a.heads + h];
-    const float beta = a.beta[t * a.heads + h];
+    if constexpr (!DIAG) aa[0] = x.alpha;
+    const float beta = x.beta;
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const int row = row0 + 4 * r + lr;
-      vv[r] = row < a.dv ? load1<IO>(a.v, t * a.v_stride + (int64_t)h * a.dv + row) : 0.f;
-    }
+    for (int r = 0; r < R; ++r) vv[r] = widen<IO>(x.v[r]);
     float out = 0.f;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
@@ -100,32 +140,37 @@ __global__ __launch_bounds__(256) void walk_kernel(SlotArgs a, int row_blocks) {
     if (row < a.dv) {
 #pragma unroll
       for (int j = 0; j < NJ; ++j)
-        *reinterpret_cast<float4*>(S + (int64_t)row * DK + 64 * j + 4 * lc) =
-            make_float4(s[r][4 * j], s[r][4 * j + 1], s[r][4 * j + 2], s[r][4 * j + 3]);
+        store_state<NT>(S + (int64_t)row * DK + 64 * j + 4 * lc,
+                        f32x4{s[r][4 * j], s[r][4 * j + 1], s[r][4 * j + 2], s[r][4 * j + 3]});
     }
   }
 }
 
 // Slots -> pages.  A slot's heads are one run of heads*dv*dk elements in both
-// handles, so a page is the run's codes and scales, group by group: eight
-// consecutive elements per lane, a group's absmax over its group/8 adjacent
-// lanes by DPP, the scale, reciprocal and rounding of the calibration.  Bound
-// by the fp32 bytes read.
-constexpr int kUnits = 4;                        // runs of eight elements per thread
+// handles, so a page is the run's codes and scales, group by group: four
+// consecutive elements per lane and unit (a wave reads whole 1 KiB runs), a
+// group's absmax over its group/4 adjacent lanes, the scale, reciprocal and
+// rounding of the calibration.  Bound by the fp32 bytes read.
+constexpr int kUnits = 4;                        // units per thread, all read before the first is used
+
+// Max over an aligned group of gl = 4, 8, 16 or 32 adjacent lanes.
+__device__ __forceinline__ float group_max32(float x, int gl) {
+  x = group_max(x, gl);
+  return gl > 16 ? fmaxf(x, __shfl_xor(x, 16)) : x;
+}
 
 template <int BITS>
-__device__ __forceinline__ void quantise8(const float (&x)[8], float inv, uint8_t* codes, int64_t unit) {
+__device__ __forceinline__ void quantise4(f32x4 x, float inv, uint8_t* codes, int64_t unit) {
   using F = Fmt<BITS>;
-  float t[8];
+  uint32_t t[4];
 #pragma unroll
-  for (int e = 0; e < 8; ++e)
-    t[e] = __builtin_amdgcn_fmed3f(fmaf(x[e], inv, F::MQ), F::MQ - F::QMAX, F::MQ + F::QMAX);
-  uint32_t X[2];
-  pack_block<BITS>(t, X);
+  for (int e = 0; e < 4; ++e)
+    t[e] = fbits(__builtin_amdgcn_fmed3f(fmaf(x[e], inv, F::MQ), F::MQ - F::QMAX, F::MQ + F::QMAX));
   if constexpr (BITS == 4)
-    reinterpret_cast<uint32_t*>(codes)[unit] = X[0] ^ F::OFF;
+    reinterpret_cast<uint16_t*>(codes)[unit] =
+        (uint16_t)(((t[0] & 0xF) | (t[1] & 0xF) << 4 | (t[2] & 0xF) << 8 | (t[3] & 0xF) << 12) ^ 0x8888u);
   else
-    reinterpret_cast<uint2*>(codes)[unit] = make_uint2(X[0] ^ F::OFF, X[1] ^ F::OFF);
+    reinterpret_cast<uint32_t*>(codes)[unit] = gather_low_bytes(t[0], t[1], t[2], t[3]) ^ F::OFF;
 }
 
 template <int BITS>
@@ -136,22 +181,20 @@ __global__ __launch_bounds__(256) void store_slots_kernel(CopyArgs a, int64_t un
   const int dst = slot_of(a.dst_slots, i, a.dst_n, lane);
   const int src = a.src_slots ? a.src_slots[i] : i;
   if (dst < 0 || src < 0 || src >= a.src_n) return;
-  const float* S = a.S + (int64_t)src * units * 8;
-  const int gl = a.group / 8;
-  float x[kUnits][8];
+  const f32x4* S = reinterpret_cast<const f32x4*>(a.S) + (int64_t)src * units;
+  const int gl = a.group / 4;
+  const int64_t u0 = (int64_t)b * kUnits * 256 + threadIdx.x;
+  f32x4 x[kUnits];
 #pragma unroll
   for (int n = 0; n < kUnits; ++n) {
-    int64_t u = ((int64_t)b * kUnits + n) * 256 + threadIdx.x;
-    u = u < units ? u : units - 1;
-    load_f32(x[n], S + u * 8);
+    const int64_t u = u0 + n * 256;
+    x[n] = S[u < units ? u : units - 1];
   }
 #pragma unroll
   for (int n = 0; n < kUnits; ++n) {
-    const int64_t u = ((int64_t)b * kUnits + n) * 256 + threadIdx.x;
-    float m = 0.f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(x[n][e]));
-    float s = group_max(m, gl) / F::QMAX;
+    const int64_t u = u0 + n * 256;
+    const float m = fmaxf(fmaxf(fabsf(x[n][0]), fabsf(x[n][1])), fmaxf(fabsf(x[n][2]), fabsf(x[n][3])));
+    float s = group_max32(m, gl) / F::QMAX;
     uint32_t s16 = 0;
     if (a.sfmt != SFMT_F32) {                    // codes are formed with the stored scale
       s16 = scale_to16(s, a.sfmt);
@@ -160,14 +203,14 @@ __global__ __launch_bounds__(256) void store_slots_kernel(CopyArgs a, int64_t un
     const float inv = inv_scale(s);
     if (u < units) {
       const int64_t to = (int64_t)dst * units + u;
-      quantise8<BITS>(x[n], inv, a.codes, to);
+      quantise4<BITS>(x[n], inv, a.codes, to);
       if (u % gl == 0) {
         if (a.sfmt != SFMT_F32)
           static_cast<uint16_t*>(a.scales)[to / gl] = (uint16_t)s16;
         else
           static_cast<float*>(a.scales)[to / gl] = s;
       }
-      if (a.ref) store_f32(a.ref + to * 8, x[n]);
+      if (a.ref) reinterpret_cast<f32x4*>(a.ref)[to] = x[n];
     }
   }
 }
@@ -182,13 +225,12 @@ __global__ __launch_bounds__(256) void store_head_kernel(CopyArgs a, int head_un
   const int dst = slot_of(a.dst_slots, i, a.dst_n, threadIdx.x & 63);
   const int src = a.src_slots ? a.src_slots[i] : i;
   if (dst < 0 || src < 0 || src >= a.src_n) return;
-  const float* S = a.S + ((int64_t)src * a.heads + h) * head_units * 8;
+  const f32x4* S = reinterpret_cast<const f32x4*>(a.S) + ((int64_t)src * a.heads + h) * head_units;
   const int64_t to = ((int64_t)dst * a.heads + h) * head_units;
-  float x[8], m = 0.f;
+  float m = 0.f;
   for (int u = threadIdx.x; u < head_units; u += 256) {
-    load_f32(x, S + (int64_t)u * 8);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(x[e]));
+    const f32x4 x = S[u];
+    m = fmaxf(m, fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3]))));
   }
 #pragma unroll
   for (int off = 32; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor(m, off));
@@ -196,16 +238,13 @@ __global__ __launch_bounds__(256) void store_head_kernel(CopyArgs a, int head_un
   __syncthreads();
   const float s = fmaxf(fmaxf(wmax[0], wmax[1]), fmaxf(wmax[2], wmax[3])) / F::QMAX;
   const float inv = inv_scale(s);
-  for (int u = threadIdx.x; u < head_units; u += 256) {
-    load_f32(x, S + (int64_t)u * 8);
-    quantise8<BITS>(x, inv, a.codes, to + u);
-  }
+  for (int u = threadIdx.x; u < head_units; u += 256) quantise4<BITS>(S[u], inv, a.codes, to + u);
   if (threadIdx.x == 0) static_cast<float*>(a.scales)[(int64_t)dst * a.heads + h] = s;
 }
 
-// Pages -> slots: S = fl(C s), eight consecutive elements per lane.  Bound by
-// the fp32 bytes written.
-template <int BITS>
+// Pages -> slots: S = fl(C s), four consecutive elements per lane and unit.
+// Bound by the fp32 bytes written.
+template <int BITS, bool NT>
 __global__ __launch_bounds__(256) void load_slots_kernel(CopyArgs a, int64_t units, int blocks,
                                                          int64_t group_units) {
   const int i = blockIdx.x / blocks, b = blockIdx.x % blocks;
@@ -213,49 +252,49 @@ __global__ __launch_bounds__(256) void load_slots_kernel(CopyArgs a, int64_t uni
   const int dst = slot_of(a.dst_slots, i, a.dst_n, lane);
   const int src = a.src_slots ? a.src_slots[i] : i;
   if (dst < 0 || src < 0 || src >= a.src_n) return;
-  float* S = a.S + (int64_t)dst * units * 8;
+  f32x4* S = reinterpret_cast<f32x4*>(a.S) + (int64_t)dst * units;
+  const int64_t u0 = (int64_t)b * kUnits * 256 + threadIdx.x;
+  uint32_t w[kUnits];
+  float s[kUnits];
 #pragma unroll
   for (int n = 0; n < kUnits; ++n) {
-    const int64_t u = ((int64_t)b * kUnits + n) * 256 + threadIdx.x;
-    if (u >= units) break;
-    const int64_t from = (int64_t)src * units + u;
-    const int64_t si = from / group_units;
-    const float s = a.sfmt == SFMT_F32
-                        ? static_cast<const float*>(a.scales)[si]
-                        : scale_from16(static_cast<const uint16_t*>(a.scales)[si], a.sfmt);
-    float x[8];
-    if constexpr (BITS == 4) {
-      const int w = (int)reinterpret_cast<const uint32_t*>(a.codes)[from];
+    const int64_t u = u0 + n * 256;
+    const int64_t from = (int64_t)src * units + (u < units ? u : units - 1), si = from / group_units;
+    w[n] = BITS == 4 ? reinterpret_cast<const uint16_t*>(a.codes)[from]
+                     : reinterpret_cast<const uint32_t*>(a.codes)[from];
+    s[n] = a.sfmt == SFMT_F32 ? static_cast<const float*>(a.scales)[si]
+                              : scale_from16(static_cast<const uint16_t*>(a.scales)[si], a.sfmt);
+  }
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = (float)((w << (28 - 4 * e)) >> 28) * s;
-    } else {
-      const uint2 w = reinterpret_cast<const uint2*>(a.codes)[from];
+  for (int n = 0; n < kUnits; ++n) {
+    const int64_t u = u0 + n * 256;
+    f32x4 x;
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        x[e] = (float)(int)(int8_t)((e < 4 ? w.x : w.y) >> (8 * (e & 3))) * s;
-    }
-    store_f32(S + u * 8, x);
+    for (int e = 0; e < 4; ++e)
+      x[e] = (float)((int)(w[n] << (32 - BITS - BITS * e)) >> (32 - BITS)) * s[n];
+    if (u < units) store_state<NT>(reinterpret_cast<float*>(S + u), x);
   }
 }
 
 }  // namespace dev
 
-hipError_t launch_walk(const SlotArgs& a, int io, int dk, int delta, int diag, hipStream_t s) {
+hipError_t launch_walk(const SlotArgs& a, int io, int dk, int delta, int diag, int nt, hipStream_t s) {
   constexpr int R = 4;
   const int row_blocks = (a.dv + 16 * R - 1) / (16 * R);
   const int64_t blocks = (int64_t)a.seqs * a.heads * row_blocks;
   if (blocks > INT32_MAX) return hipErrorInvalidConfiguration;
-#define LSQ_WALK(IO, DK, D, G)                                                                 \
-  if (io == IO && dk == DK && delta == D && diag == G) {                                       \
-    hipLaunchKernelGGL((dev::walk_kernel<IO, DK, D, G, R>), dim3((unsigned)blocks), dim3(256), \
-                       0, s, a, row_blocks);                                                   \
-    return hipGetLastError();                                                                  \
+#define LSQ_WALK(IO, DK, D, G, N)                                                                 \
+  if (io == IO && dk == DK && delta == D && diag == G && nt == N) {                               \
+    hipLaunchKernelGGL((dev::walk_kernel<IO, DK, D, G, R, N>), dim3((unsigned)blocks), dim3(256), \
+                       0, s, a, row_blocks);                                                      \
+    return hipGetLastError();                                                                     \
   }
-#define LSQ_WALK_IO(IO)                                                                  \
-  LSQ_WALK(IO, 128, 0, 0) LSQ_WALK(IO, 128, 0, 1) LSQ_WALK(IO, 128, 1, 0)                \
-  LSQ_WALK(IO, 128, 1, 1) LSQ_WALK(IO, 64, 0, 0) LSQ_WALK(IO, 64, 0, 1)                  \
-  LSQ_WALK(IO, 64, 1, 0) LSQ_WALK(IO, 64, 1, 1)
-  LSQ_WALK_IO(IO_F32) LSQ_WALK_IO(IO_F16) LSQ_WALK_IO(IO_BF16)
+#define LSQ_WALK_IO(IO, N)                                                                  \
+  LSQ_WALK(IO, 128, 0, 0, N) LSQ_WALK(IO, 128, 0, 1, N) LSQ_WALK(IO, 128, 1, 0, N)          \
+  LSQ_WALK(IO, 128, 1, 1, N) LSQ_WALK(IO, 64, 0, 0, N) LSQ_WALK(IO, 64, 0, 1, N)            \
+  LSQ_WALK(IO, 64, 1, 0, N) LSQ_WALK(IO, 64, 1, 1, N)
+  LSQ_WALK_IO(IO_F32, 0) LSQ_WALK_IO(IO_F16, 0) LSQ_WALK_IO(IO_BF16, 0)
+  LSQ_WALK_IO(IO_F32, 1) LSQ_WALK_IO(IO_F16, 1) LSQ_WALK_IO(IO_BF16, 1)
 #undef LSQ_WALK_IO
 #undef LSQ_WALK
   return hipErrorInvalidValue;
@@ -267,12 +306,12 @@ hipError_t launch_store_slots(const CopyArgs& a, int bits, int dk, hipStream_t s
     if (blocks > INT32_MAX) return hipErrorInvalidConfiguration;
     const dim3 grid((unsigned)blocks), block(256);
     if (bits == 4)
-      hipLaunchKernelGGL(dev::store_head_kernel<4>, grid, block, 0, s, a, a.dv * dk / 8);
+      hipLaunchKernelGGL(dev::store_head_kernel<4>, grid, block, 0, s, a, a.dv * dk / 4);
     else
-      hipLaunchKernelGGL(dev::store_head_kernel<8>, grid, block, 0, s, a, a.dv * dk / 8);
+      hipLaunchKernelGGL(dev::store_head_kernel<8>, grid, block, 0, s, a, a.dv * dk / 4);
     return hipGetLastError();
   }
-  const int64_t units = (int64_t)a.heads * a.dv * dk / 8;
+  const int64_t units = (int64_t)a.heads * a.dv * dk / 4;
   const int64_t per = (units + 256 * dev::kUnits - 1) / (256 * dev::kUnits);
   if (per * a.count > INT32_MAX) return hipErrorInvalidConfiguration;
   const dim3 grid((unsigned)(per * a.count)), block(256);
@@ -284,15 +323,14 @@ hipError_t launch_store_slots(const CopyArgs& a, int bits, int dk, hipStream_t s
 }
 
 hipError_t launch_load_slots(const CopyArgs& a, int bits, int dk, hipStream_t s) {
-  const int64_t units = (int64_t)a.heads * a.dv * dk / 8;
+  const int64_t units = (int64_t)a.heads * a.dv * dk / 4;
   const int64_t per = (units + 256 * dev::kUnits - 1) / (256 * dev::kUnits);
-  const int64_t group_units = a.group ? a.group / 8 : (int64_t)a.dv * dk / 8;
+  const int64_t group_units = a.group ? a.group / 4 : (int64_t)a.dv * dk / 4;
   if (per * a.count > INT32_MAX) return hipErrorInvalidConfiguration;
   const dim3 grid((unsigned)(per * a.count)), block(256);
-  if (bits == 4)
-    hipLaunchKernelGGL(dev::load_slots_kernel<4>, grid, block, 0, s, a, units, (int)per, group_units);
-  else
-    hipLaunchKernelGGL(dev::load_slots_kernel<8>, grid, block, 0, s, a, units, (int)per, group_units);
+  const auto kernel = bits == 4 ? (a.nt ? dev::load_slots_kernel<4, true> : dev::load_slots_kernel<4, false>)
+                                : (a.nt ? dev::load_slots_kernel<8, true> : dev::load_slots_kernel<8, false>);
+  hipLaunchKernelGGL(kernel, grid, block, 0, s, a, units, (int)per, group_units);
   return hipGetLastError();
 }
 

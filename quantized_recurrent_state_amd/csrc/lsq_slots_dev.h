@@ -11,30 +11,45 @@
 namespace lsq {
 namespace dev {
 
-// Element e of an IO-typed array as fp32.
+// Elements of an IO-typed array as loaded; converted where they are used, so
+// that the next token's are in flight during this one's arithmetic.
 template <int IO>
-__device__ __forceinline__ float load1(const void* p, int64_t e) {
-  if constexpr (IO == IO_F32) return static_cast<const float*>(p)[e];
-  const uint16_t b = static_cast<const uint16_t*>(p)[e];
-  if constexpr (IO == IO_F16) return __half2float(__ushort_as_half(b));
-  return __uint_as_float((uint32_t)b << 16);
+struct Raw {
+  using One = uint16_t;
+  using Four = uint2;
+};
+template <>
+struct Raw<IO_F32> {
+  using One = float;
+  using Four = float4;
+};
+
+template <int IO>
+__device__ __forceinline__ typename Raw<IO>::One raw1(const void* p, int64_t e) {
+  return static_cast<const typename Raw<IO>::One*>(p)[e];
 }
 
 // Four consecutive elements from e (8-byte aligned; 16 for fp32).
 template <int IO>
-__device__ __forceinline__ void load4(float* dst, const void* p, int64_t e) {
+__device__ __forceinline__ typename Raw<IO>::Four raw4(const void* p, int64_t e) {
+  return *reinterpret_cast<const typename Raw<IO>::Four*>(static_cast<const typename Raw<IO>::One*>(p) + e);
+}
+
+template <int IO>
+__device__ __forceinline__ float widen(typename Raw<IO>::One x) {
+  if constexpr (IO == IO_F32) return x;
+  else if constexpr (IO == IO_F16) return __half2float(__ushort_as_half(x));
+  else return __uint_as_float((uint32_t)x << 16);
+}
+
+template <int IO>
+__device__ __forceinline__ void widen4(float* dst, typename Raw<IO>::Four x) {
   if constexpr (IO == IO_F32) {
-    const float4 x = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + e);
     dst[0] = x.x; dst[1] = x.y; dst[2] = x.z; dst[3] = x.w;
   } else {
-    const uint2 x = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + e);
     const uint32_t w[2] = {x.x, x.y};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t b = (i & 1) ? w[i >> 1] >> 16 : w[i >> 1] & 0xFFFFu;
-      dst[i] = IO == IO_F16 ? __half2float(__ushort_as_half((unsigned short)b))
-                            : __uint_as_float(b << 16);
-    }
+    for (int i = 0; i < 4; ++i) dst[i] = widen<IO>((uint16_t)(w[i >> 1] >> (16 * (i & 1))));
   }
 }
 

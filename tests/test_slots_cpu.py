@@ -9,7 +9,7 @@ import pytest
 import torch
 
 import quantized_recurrent_state_amd as lsq
-from quantized_recurrent_state_amd import _lib
+from quantized_recurrent_state_amd import _lib, slots
 
 FAKE = 0x7F0000000000
 
@@ -134,13 +134,13 @@ def test_python_checks():
                 v=torch.zeros(n, 4, 32, dtype=bf), alpha=torch.zeros(n, 4), beta=torch.zeros(n, 4),
                 cu_seqlens=torch.zeros(4, dtype=torch.int32), slots=torch.zeros(3, dtype=torch.int32),
                 fresh=torch.zeros(3, dtype=torch.bool), o=None)
-    b, o = st._token_batch(**good)
+    b, o = slots.token_batch(st, **good)
     assert (b.io, b.qk_heads, b.seqs, b.tokens) == (lsq.IO_BF16, 2, 3, n)
     assert (b.q_stride, b.v_stride, b.o_stride) == (128, 128, 128) and o.shape == (n, 4, 32)
     wide = torch.zeros(n, 4 * 32 + 24, dtype=bf)
-    b, _ = st._token_batch(**{**good, "v": wide[:, :128].unflatten(1, (4, 32))})
+    b, _ = slots.token_batch(st, **{**good, "v": wide[:, :128].unflatten(1, (4, 32))})
     assert b.v_stride == 152
-    b, _ = st._token_batch(**{**good, "q": torch.zeros(1, 2, 64, dtype=bf).expand(n, 2, 64)})
+    b, _ = slots.token_batch(st, **{**good, "q": torch.zeros(1, 2, 64, dtype=bf).expand(n, 2, 64)})
     assert b.q_stride == 0
     for name, t in [("q", torch.zeros(n, 3, 64, dtype=bf)), ("q", torch.zeros(n, 2, 32, dtype=bf)),
                     ("q", torch.zeros(n, 128, dtype=bf)), ("q", torch.zeros(n, 2, 64, dtype=torch.float64)),
@@ -153,7 +153,7 @@ def test_python_checks():
                     ("fresh", torch.zeros(3)), ("fresh", torch.zeros(2, dtype=torch.bool)),
                     ("o", torch.zeros(n, 4, 32)), ("o", torch.zeros(n, 4, 31, dtype=bf))]:
         with pytest.raises(ValueError):
-            st._token_batch(**{**good, name: t})
+            slots.token_batch(st, **{**good, name: t})
     with pytest.raises(TypeError):
         st.store_slots(None)
     st.handle = None
