@@ -45,24 +45,27 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_of(const void* p, int64_t
 // A lane offset behind every buffer: chunks are below 2^31 bytes.
 constexpr uint32_t kNowhere = 0xFFFFFFF0u;
 
-// Tiling of one instance: NW waves of CG groups of 16 value columns, chunks of 32
-// tokens (one k-step of the MFMA over tokens).
-template <int IO, int DK, int NW, int CG>
+// Tiling of one instance: NW waves, KS of them to the same CG groups of 16 value
+// columns with a share of dk each; chunks of 32 tokens (one k-step of the MFMA
+// over tokens).
+template <int IO, int DK, int NW, int CG, int KS>
 struct Tile {
   static constexpr int NP = IO == IO_BF16 ? 1 : IO == IO_F16 ? 2 : 3;   // parts of an input
   static constexpr int NO = IO == IO_F32 ? 3 : 2;                       // parts on the output's side
-  static constexpr int C = 32, NT = 64 * NW, DV = 16 * CG * NW, ROUND = 256;
+  static constexpr int C = 32, NT = 64 * NW, DV = 16 * CG * NW / KS, ROUND = 256;
   static constexpr int EU = IO == IO_F32 ? 4 : 8;                       // elements of a 16-byte unit
-  // LDS row pitches in elements.  k and v are read by columns, four rows of 32
-  // bytes by 16 lanes: rows 8 banks apart.  q and P are read by rows, 8 bytes of
-  // 16 rows: rows 4 banks apart.  Neither then meets in a bank.
-  static constexpr int PK = DK + 16, PV = DV + 16, PQ = DK + 8, PP = C + 8;
+  // LDS row pitches in elements.  v is read by columns, four rows of 32 bytes by
+  // 16 lanes: rows 8 banks apart; k too, its 8-byte pieces 16 bytes apart: rows
+  // 16 banks apart.  q and P are read by rows, 16 and 8 bytes of 16 rows: rows 4
+  // banks apart.  None then meet in a bank.
+  static constexpr int PK = DK + 32, PV = DV + 16, PQ = DK + 8, PP = C + 8;
   static constexpr int QU = (C * DK / EU + NT - 1) / NT, VU = C * DV / EU / NT;   // units of k (q), v per thread
   static constexpr bool SPARE = QU * NT > C * DK / EU;                  // some threads have no unit of k
   // Two copies of the rows where two workgroups of a CU have room for them, and
   // P of two chunks (its product with v runs one chunk behind).
   static constexpr int RB = IO == IO_BF16 ? 2 : 1;
   static constexpr bool BEHIND = IO != IO_F32;
+  static_assert(KS == 1 || (KS == 2 && !BEHIND), "the shared sums are read between the same two barriers");
 };
 
 // x as a sum of N bf16 parts, four values at a time.
@@ -245,30 +248,32 @@ __device__ __forceinline__ Item item_of(int64_t b, int rows) {
   return {p / own, (int)(b % 8) * own + (int)(p % own)};
 }
 
-// One workgroup walks the chunks of one segment of one head, 64 CG value
-// columns of it.  The waves share out P's four tiles; each has its 16 CG
+// One workgroup walks the chunks of one segment of one head, 16 CG NW value
+// columns of it.  Four waves compute P's four tiles; every wave has its 16 CG
 // columns of S in registers in the layout that the MFMA both writes (S^T[dk, dv]
 // accumulated from k^T and the scaled v) and reads (as the operand of S q): the
-// k index of an operand is only a labelling, so slots 0-3 and 4-7 of a lane
-// group g stand for rows 4 g .. and 16 + 4 g .. of a 32-row step in every
-// product.  What bounds it is the latency of a chunk's steps rather than any
-// rate, so a chunk's products are independent of each other: S q and the new S,
-// P of the same chunk, and (BEHIND) P v of the chunk before, with the next rows
-// on their way to LDS, all between two barriers.  OUT = false adds up a
-// segment's writes alone (no q, no output), for the segments behind it.  VEC: v
-// and o by whole units (else by element, for odd widths and addresses).
-template <int IO, int DK, int NW, int CG, bool VEC, bool OUT>
-__global__ __launch_bounds__(64 * NW, NW / 2) void attend_kernel(AttendArgs args) {
-  using T = Tile<IO, DK, NW, CG>;
+// k index of an operand is only a labelling, so the tiles' rows are dealt to
+// the lanes as S q wants them, and in the products over tokens slots 0-3 and 4-7
+// of a lane group g stand for tokens 4 g .. and 16 + 4 g ...  A chunk's
+// products are independent of each other: S q and the new S, P of the same
+// chunk, and (BEHIND) P v of the chunk before, with the next rows on their way
+// to LDS, all between two barriers.  OUT = false adds up a segment's writes alone
+// (no q, no output), for the segments behind it.  VEC: v and o by whole units
+// (else by element, for odd widths and addresses).
+template <int IO, int DK, int NW, int CG, int KS, bool VEC, bool OUT>
+__global__ __launch_bounds__(64 * NW, NW / 2 / KS) void attend_kernel(AttendArgs args) {
+  using T = Tile<IO, DK, NW, CG, KS>;
   constexpr int NP = T::NP, NO = T::NO, C = T::C, PK = T::PK, PV = T::PV, PQ = T::PQ, PP = T::PP;
   constexpr int NT = T::NT, EU = T::EU, RB = T::RB, ROUND = T::ROUND, B = 16 / EU;   // B: bytes of an element
   constexpr bool BEHIND = T::BEHIND;
-  constexpr int CT = C / 16, KT = DK / 16;
+  constexpr int CT = C / 16, DW = DK / KS, KT = DW / 16;   // a wave's part of dk
+  constexpr int OT = CT / KS;                    // tiles of 16 tokens whose output a wave finishes
   const SlotArgs& a = args.s;
   __shared__ __align__(16) __bf16 kl[RB][NP][C * PK];
   __shared__ __align__(16) __bf16 vl[RB][NP][C * PV];
   __shared__ __align__(16) __bf16 ql[OUT ? RB : 1][OUT ? NP : 1][OUT ? C * PQ : 8];
   __shared__ __align__(16) __bf16 pl[OUT && BEHIND ? 2 : 1][OUT ? NO : 1][OUT ? C * PP : 8];
+  __shared__ __align__(16) f32x4 part[OUT && KS > 1 ? NW * CG * 64 : 1];
   __shared__ __align__(16) Decays<ROUND> dec[RB];
 
   const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, li = lane & 15;
@@ -403,11 +408,12 @@ __global__ __launch_bounds__(64 * NW, NW / 2) void attend_kernel(AttendArgs args
     for (int n = 0; n < T::VU; ++n) put(rv[n], vl[buf], n * VR + vrow, PV, vcol);
   };
 
-  // ---- the state's columns: lane li has columns 16 cg + li of the wave's, rows
-  // 16 I + 4 g + v of S^T
-  const int w0 = 16 * CG * wave;                 // the wave's first column in the slice
+  // ---- the state's columns: lane li has columns 16 cg + li of the wave's, and of
+  // S^T the rows 32 (I / 2) + 8 g + 4 (I % 2) + v (tiles I = 2 m and 2 m + 1
+  // together hold eight consecutive rows per lane, an operand's k-slots)
+  const int w0 = 16 * CG * (wave / KS), kh = wave % KS;   // the wave's first column in the slice; its part of dk
   f32x4 S[CG][KT];
-  const int64_t state = ((int64_t)h * a.dv + d0 + w0 + li) * DK + 4 * g, per = (int64_t)a.heads * a.dv * DK;
+  const int64_t state = ((int64_t)h * a.dv + d0 + w0 + li) * DK + kh * DW + 8 * g, per = (int64_t)a.heads * a.dv * DK;
   float* slot_S = a.S + slot * per + state;
   float* seg_S = args.ws + seg * per + state;
   {
@@ -418,23 +424,27 @@ __global__ __launch_bounds__(64 * NW, NW / 2) void attend_kernel(AttendArgs args
     for (int cg = 0; cg < CG; ++cg)
 #pragma unroll
       for (int I = 0; I < KT; ++I)
-        S[cg][I] = !zero && w0 + 16 * cg + li < vcols ? *reinterpret_cast<const f32x4*>(p + 16 * cg * DK + 16 * I)
+        S[cg][I] = !zero && w0 + 16 * cg + li < vcols ? *reinterpret_cast<const f32x4*>(p + 16 * cg * DK + 32 * (I / 2) + 4 * (I % 2))
                                                       : f32x4{0.f, 0.f, 0.f, 0.f};
   }
 
   bf16x4 vr[CG][2][NP];                          // the wave's columns of v, by columns
-  f32x4 acc[CG][OUT ? CT : 1];                   // o^T tiles: rows dv, columns t
+  f32x4 acc[CG][OUT ? CT : 1];                   // o^T tiles: rows dv, columns t (KS = 2: only tile 0 from share() on)
   // acc += P v of chunk c, and the output
   auto finish = [&](int c, int buf) {
     const auto ob = rows_of(a.o, ((sg.t0 + c * C) * a.o_stride + hv) * B, c < 0 ? 0u : bytes_of(c, ostep, vcols * B));
-    uint32_t oo = li * ostep + (w0 + 4 * g) * B;
+    const int t0 = KS > 1 ? 16 * kh : 0;         // the wave's first token
+    uint32_t oo = (t0 + li) * ostep + (w0 + 4 * g) * B;
+    if constexpr (KS > 1) {
 #pragma unroll
-    for (int ti = 0; ti < CT; ++ti) {
+      for (int cg = 0; cg < CG; ++cg) acc[cg][0] = acc[cg][0] + part[(wave * CG + cg) * 64 + lane];
+    }
+#pragma unroll
+    for (int ti = 0; ti < OT; ++ti) {
       bf16x8 pp[NO];
 #pragma unroll
       for (int i = 0; i < NO; ++i) {
-        const __bf16* p = &pl[buf][i][(16 * ti + li) * PP + 4 * g];
-        pp[i] = join(*reinterpret_cast<const bf16x4*>(p), *reinterpret_cast<const bf16x4*>(p + 16));
+        pp[i] = *reinterpret_cast<const bf16x8*>(&pl[buf][i][(t0 + 16 * ti + li) * PP + 8 * g]);
       }
 #pragma unroll
       for (int i = NO - 1; i >= 0; --i)          // small products first
@@ -445,7 +455,7 @@ __global__ __launch_bounds__(64 * NW, NW / 2) void attend_kernel(AttendArgs args
             for (int cg = 0; cg < CG; ++cg) acc[cg][ti] = mfma(join(vr[cg][0][j], vr[cg][1][j]), pp[i], acc[cg][ti]);
     }
 #pragma unroll
-    for (int ti = 0; ti < CT; ++ti) {
+    for (int ti = 0; ti < OT; ++ti) {
 #pragma unroll
       for (int cg = 0; cg < CG; ++cg) {
         const f32x4 x = acc[cg][ti];
@@ -525,11 +535,11 @@ __global__ __launch_bounds__(64 * NW, NW / 2) void attend_kernel(AttendArgs args
         bf16x4 parts[NO];
         split4<NO>(x, parts);
 #pragma unroll
-        for (int i = 0; i < NO; ++i) *reinterpret_cast<bf16x4*>(&pl[BEHIND ? c & 1 : 0][i][t * PP + s0]) = parts[i];
+        for (int i = 0; i < NO; ++i) *reinterpret_cast<bf16x4*>(&pl[BEHIND ? c & 1 : 0][i][t * PP + 8 * g + 4 * si]) = parts[i];
       }
       // ---- c_t S q
 #pragma unroll
-      for (int ks = 0; ks < DK / 32; ++ks) {
+      for (int ks = 0; ks < DW / 32; ++ks) {
         bf16x8 sp[CG][NO];
 #pragma unroll
         for (int cg = 0; cg < CG; ++cg) {
@@ -544,8 +554,7 @@ __global__ __launch_bounds__(64 * NW, NW / 2) void attend_kernel(AttendArgs args
           bf16x8 qp[NP];
 #pragma unroll
           for (int i = 0; i < NP; ++i) {
-            const __bf16* p = &ql[buf][i][(16 * ti + li) * PQ + 32 * ks + 4 * g];
-            qp[i] = join(*reinterpret_cast<const bf16x4*>(p), *reinterpret_cast<const bf16x4*>(p + 16));
+            qp[i] = *reinterpret_cast<const bf16x8*>(&ql[buf][i][(16 * ti + li) * PQ + kh * DW + 32 * ks + 8 * g]);
           }
 #pragma unroll
           for (int i = NO - 1; i >= 0; --i)
@@ -563,6 +572,13 @@ __global__ __launch_bounds__(64 * NW, NW / 2) void attend_kernel(AttendArgs args
         const float ct = __builtin_amdgcn_exp2f(d.hi[at + 16 * ti + li]) * (1.f + 0.69314718f * d.lo[at + 16 * ti + li]);
 #pragma unroll
         for (int cg = 0; cg < CG; ++cg) acc[cg][ti] = acc[cg][ti] * ct;
+      }
+      if constexpr (KS > 1) {                    // the other wave's tile to it, the own one to place 0
+#pragma unroll
+        for (int cg = 0; cg < CG; ++cg) {
+          part[((wave ^ 1) * CG + cg) * 64 + lane] = kh ? acc[cg][0] : acc[cg][1];
+          acc[cg][0] = kh ? acc[cg][1] : acc[cg][0];
+        }
       }
     }
     if constexpr (RB == 1)
@@ -592,7 +608,7 @@ __global__ __launch_bounds__(64 * NW, NW / 2) void attend_kernel(AttendArgs args
       bf16x8 kp[NP];
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
-        const __bf16* p = &kl[buf][i][(4 * g + li / 4) * PK + 16 * I + 4 * (li % 4)];
+        const __bf16* p = &kl[buf][i][(4 * g + li / 4) * PK + kh * DW + 32 * (I / 2) + 8 * (li % 4) + 4 * (I % 2)];
         kp[i] = join(read_column4(p), read_column4(p + 16 * PK));
       }
 #pragma unroll
@@ -628,7 +644,7 @@ __global__ __launch_bounds__(64 * NW, NW / 2) void attend_kernel(AttendArgs args
     for (int cg = 0; cg < CG; ++cg)
       if (w0 + 16 * cg + li < vcols) {
 #pragma unroll
-        for (int I = 0; I < KT; ++I) *reinterpret_cast<f32x4*>(p + 16 * cg * DK + 16 * I) = S[cg][I];
+        for (int I = 0; I < KT; ++I) *reinterpret_cast<f32x4*>(p + 16 * cg * DK + 32 * (I / 2) + 4 * (I % 2)) = S[cg][I];
       }
   }
   if constexpr (!OUT) {                          // the segment's own decay
@@ -685,28 +701,32 @@ namespace {
 // half a CU at 64.
 int slice_width(int io, int dv) { return io == IO_F32 || dv <= 64 ? 64 : 128; }
 
-template <int IO, int DK, int NW, int CG, bool VEC>
+template <int IO, int DK, int NW, int CG, int KS, bool VEC>
 hipError_t launch_instance(const AttendArgs& args, unsigned blocks, hipStream_t s) {
   const SlotArgs& a = args.s;
   if (args.seg_len) {
-    hipLaunchKernelGGL((dev::attend_kernel<IO, DK, NW, CG, VEC, false>), dim3(blocks), dim3(64 * NW), 0, s, args);
+    hipLaunchKernelGGL((dev::attend_kernel<IO, DK, NW, CG, KS, VEC, false>), dim3(blocks), dim3(64 * NW), 0, s, args);
     const int64_t quads = (int64_t)a.heads * a.dv * DK / 4, most = 4096 / a.seqs + 1;
     const int64_t per = (quads + 255) / 256 < most ? (quads + 255) / 256 : most;
     hipLaunchKernelGGL(dev::combine_kernel, dim3((unsigned)(per * a.seqs)), dim3(256), 0, s, args,
                        (int)per, quads);
   }
-  hipLaunchKernelGGL((dev::attend_kernel<IO, DK, NW, CG, VEC, true>), dim3(blocks), dim3(64 * NW), 0, s, args);
+  hipLaunchKernelGGL((dev::attend_kernel<IO, DK, NW, CG, KS, VEC, true>), dim3(blocks), dim3(64 * NW), 0, s, args);
   return hipGetLastError();
 }
 
 template <int IO, int DK>
 hipError_t launch_width(const AttendArgs& args, unsigned blocks, hipStream_t s) {
-  if constexpr (IO != IO_F32)
+  if constexpr (IO == IO_F32) {
+    return args.wide ? launch_instance<IO, DK, 8, 1, 2, true>(args, blocks, s)
+                     : launch_instance<IO, DK, 8, 1, 2, false>(args, blocks, s);
+  } else {
     if (slice_width(IO, args.s.dv) == 128)
-      return args.wide ? launch_instance<IO, DK, 8, 1, true>(args, blocks, s)
-                       : launch_instance<IO, DK, 8, 1, false>(args, blocks, s);
-  return args.wide ? launch_instance<IO, DK, 4, 1, true>(args, blocks, s)
-                   : launch_instance<IO, DK, 4, 1, false>(args, blocks, s);
+      return args.wide ? launch_instance<IO, DK, 8, 1, 1, true>(args, blocks, s)
+                       : launch_instance<IO, DK, 8, 1, 1, false>(args, blocks, s);
+    return args.wide ? launch_instance<IO, DK, 4, 1, 1, true>(args, blocks, s)
+                     : launch_instance<IO, DK, 4, 1, 1, false>(args, blocks, s);
+  }
 }
 
 }  // namespace

@@ -33,26 +33,28 @@ def _on_device(index, stream, call):
         return call(torch.cuda.current_stream(index).cuda_stream)
 
 
-def _plain(name, t, shape, dtype, device):
-    """A contiguous tensor of this shape, type and device; its address."""
-    if t.dtype != dtype or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor on {device}")
+def _plain(name, t, shape, dtype, index):
+    """Address of a contiguous tensor of this shape and type on device index."""
+    if t.dtype is not dtype or t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor on device {index}")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     return t.data_ptr()
 
 
-def _rows(name, t, shape, dtype, device):
-    """A [tokens, heads, d] tensor whose tokens may be strided; its address and token stride."""
-    if t.dtype != dtype or t.device != device:
-        raise ValueError(f"{name} must be a {dtype} tensor on {device}")
+def _rows(name, t, shape, dtype, index):
+    """Address and token stride of a [tokens, heads, d] tensor whose tokens may be strided."""
+    if t.dtype is not dtype or t.get_device() != index:
+        raise ValueError(f"{name} must be a {dtype} tensor on device {index}")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     n, heads, d = shape
+    if t.is_contiguous():                    # also one token of any stride
+        return t.data_ptr(), heads * d
     row, head, one = t.stride()
     if (one != 1 and d != 1) or (head != d and heads != 1):
         raise ValueError(f"{name} must be contiguous within each token")
-    return t.data_ptr(), (row if n > 1 else heads * d)
+    return t.data_ptr(), row
 
 
 def token_batch(state, q, k, v, alpha, beta, cu_seqlens, slots, fresh, o):
@@ -60,7 +62,7 @@ def token_batch(state, q, k, v, alpha, beta, cu_seqlens, slots, fresh, o):
     c = state.cfg
     if c.bits != 32:
         raise ValueError("token batches run on an fp32 state (bits 32)")
-    dev, dtype = state.f32.device, q.dtype
+    dev, dtype = state.f32.get_device(), q.dtype
     io = _IO.get(dtype)
     if io is None:
         raise ValueError(f"q has type {dtype}, expected float32, float16 or bfloat16")
@@ -84,9 +86,9 @@ def token_batch(state, q, k, v, alpha, beta, cu_seqlens, slots, fresh, o):
     if slots is not None:
         sp = _plain("slots", slots, (m,), torch.int32, dev)
     if fresh is not None:
-        fp = _plain("fresh", fresh, (m,), torch.bool if fresh.dtype == torch.bool else torch.uint8, dev)
+        fp = _plain("fresh", fresh, (m,), torch.bool if fresh.dtype is torch.bool else torch.uint8, dev)
     if o is None:
-        o = torch.empty((n, heads, dv), dtype=dtype, device=dev)
+        o = torch.empty((n, heads, dv), dtype=dtype, device=state.f32.device)
         op, so = o.data_ptr(), heads * dv
     else:
         op, so = _rows("o", o, (n, heads, dv), dtype, dev)
@@ -111,7 +113,7 @@ def attend(state, q, k, v, alpha, beta, cu_seqlens, slots, fresh, o, stream):
             _lib.check(status, "lsq_attend")
         return out
 
-    return _on_device(_buffer(state).device.index, stream, call)
+    return _on_device(_buffer(state).get_device(), stream, call)
 
 
 def step_slots(state, q, k, v, alpha, beta, slots, fresh, o, stream):
@@ -122,15 +124,15 @@ def step_slots(state, q, k, v, alpha, beta, slots, fresh, o, stream):
             _lib.check(status, "lsq_step_slots")
         return out
 
-    return _on_device(_buffer(state).device.index, stream, call)
+    return _on_device(_buffer(state).get_device(), stream, call)
 
 
 def copy(fn, dst, src, dst_slots, src_slots, stream):
     """fn (lsq_state_store_slots or lsq_state_load_slots) of the entries that the slots list."""
     if not isinstance(dst, LsqState) or not isinstance(src, LsqState):
         raise TypeError("both states must be LsqState")
-    dev = _buffer(dst).device
-    if _buffer(src).device != dev:
+    dev = _buffer(dst).get_device()
+    if _buffer(src).get_device() != dev:
         raise ValueError("both states must be on one device")
     m = min(dst.cfg.batch, src.cfg.batch)
     for t in (dst_slots, src_slots):
@@ -139,4 +141,4 @@ def copy(fn, dst, src, dst_slots, src_slots, stream):
     for name, t in (("dst_slots", dst_slots), ("src_slots", src_slots)):
         if t is not None:
             _plain(name, t, (m,), torch.int32, dev)
-    _on_device(dev.index, stream, lambda s: fn(dst.handle, src.handle, m, dst_slots, src_slots, s))
+    _on_device(dev, stream, lambda s: fn(dst.handle, src.handle, m, dst_slots, src_slots, s))
