@@ -42,6 +42,8 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_of(const void* p, int64_t
                                            bytes, 0x00027000);
 }
 
+constexpr int kCUs = 256;
+
 // A lane offset behind every buffer: chunks are below 2^31 bytes.
 constexpr uint32_t kNowhere = 0xFFFFFFF0u;
 
@@ -54,11 +56,13 @@ struct Tile {
   static constexpr int NO = IO == IO_F32 ? 3 : 2;                       // parts on the output's side
   static constexpr int C = 32, NT = 64 * NW, DV = 16 * CG * NW / KS, ROUND = 256;
   static constexpr int EU = IO == IO_F32 ? 4 : 8;                       // elements of a 16-byte unit
-  // LDS row pitches in elements.  v is read by columns, four rows of 32 bytes by
-  // 16 lanes: rows 8 banks apart; k too, its 8-byte pieces 16 bytes apart: rows
-  // 16 banks apart.  q and P are read by rows, 16 and 8 bytes of 16 rows: rows 4
-  // banks apart.  None then meet in a bank.
-  static constexpr int PK = DK + 32, PV = DV + 16, PQ = DK + 8, PP = C + 8;
+  // LDS row pitches in elements: rows 8 banks apart (P: 24), which keeps the
+  // 16-byte reads of 16 rows (q, P) and the four-row reads by columns (v) free
+  // of bank conflicts, and those of k, its 8-byte pieces 16 bytes apart, nearly
+  // so (counters: 22% of the LDS cycles of the bf16 instance; 35% at rows 4 and
+  // 20 banks apart).  P's columns are stored in the order of the k-slots: token
+  // s at 8 (s % 16 / 4) + 4 (s / 16) + s % 4.
+  static constexpr int PK = DK + 16, PV = DV + 16, PQ = DK + 16, PP = C + 16;
   static constexpr int QU = (C * DK / EU + NT - 1) / NT, VU = C * DV / EU / NT;   // units of k (q), v per thread
   static constexpr bool SPARE = QU * NT > C * DK / EU;                  // some threads have no unit of k
   // Two copies of the rows where two workgroups of a CU have room for them, and
@@ -182,11 +186,11 @@ __device__ __forceinline__ u32x4 keep_elements(u32x4 x, int n) {
 }
 
 // The segment a workgroup takes: sequence i, its j-th of n segments (n = 0:
-// none).  With a segment length L, a sequence of more than 2 L tokens is cut
-// into its length over L, rounded up.
+// none), number seg.  With a segment length L, a sequence of more than 2 L
+// tokens is cut into its length over L, rounded up.
 struct Segment {
   int i, j, n;
-  int64_t t0, t1;
+  int64_t seg, t0, t1;
 };
 
 __device__ __forceinline__ int segments_of(const Span& sp, int64_t L) {
@@ -195,33 +199,57 @@ __device__ __forceinline__ int segments_of(const Span& sp, int64_t L) {
 }
 
 // Segments are numbered without gaps (idle workgroups between busy ones would
-// leave whole shader engines idle): a wave counts 64 sequences at a time.
-__device__ __forceinline__ int segments_upto(const SlotArgs& a, int64_t L, int i0, int lane) {
-  int n = i0 + lane < a.seqs ? segments_of(span_of(a, i0 + lane), L) : 0;
+// leave whole shader engines idle), 64 sequences at a time: lane r has the
+// group's r-th sequence and the segments up to it.  Up to 64 sequences are
+// ordered by length, the longest first; with more of them the order matters
+// little, and a workgroup's search stays short.
+struct Numbered {
+  int seq, upto;
+};
+
+__device__ __forceinline__ Numbered number_segments(const SlotArgs& a, int64_t L, int i0, int lane) {
+  const bool in = i0 + lane < a.seqs;
+  const Span sp = in ? span_of(a, i0 + lane) : Span{0, 0};
+  const int len = sp.t1 > sp.t0 ? (int)(sp.t1 - sp.t0) : 0;
+  int rank = lane;
+  if (a.seqs <= 64 && in) rank = 0;              // lanes without a sequence stay behind the others
+  if (a.seqs <= 64)
+    for (int j = 0; j < a.seqs; ++j) {
+      const int x = __builtin_amdgcn_readlane(len, j);
+      rank += in && (x > len || (x == len && j < lane));
+    }
+  int n = __builtin_amdgcn_ds_permute(4 * rank, segments_of(sp, L));
+  const int seq = __builtin_amdgcn_ds_permute(4 * rank, i0 + lane);
 #pragma unroll
   for (int o = 1; o < 64; o *= 2) {
     const int up = __shfl_up(n, o);
     if (lane >= o) n += up;
   }
-  return n;
+  return {seq, n};
 }
 
-__device__ __forceinline__ Segment segment_of(const SlotArgs& a, int64_t L, int64_t s, int lane) {
+__device__ __forceinline__ Segment segment_of(const SlotArgs& a, int64_t L, int64_t s, int rows, int lane) {
   Segment g{};
-  if (L == 0) {
-    g.i = (int)s;
-  } else {
+  g.seg = s;
+  g.i = (int)s;
+  if (L || (int64_t)a.seqs * rows > kCUs) {
+    int64_t before = 0;
     for (int i0 = 0;; i0 += 64) {
       if (i0 >= a.seqs) return g;
-      const int n = segments_upto(a, L, i0, lane), all = __builtin_amdgcn_readlane(n, 63);
-      if (s < all) {
-        const int at = __builtin_ctzll(__ballot(n > s));
-        g.i = i0 + at;
-        g.j = (int)s - (at ? __shfl(n, at - 1) : 0);
-        g.j = __builtin_amdgcn_readfirstlane(g.j);
+      const Numbered m = number_segments(a, L, i0, lane);
+      const int all = __builtin_amdgcn_readlane(m.upto, 63);
+      // Two workgroups share a CU: those of the second round in reverse, a long
+      // sequence beside a short one.
+      const int64_t round = kCUs / rows;
+      if (a.seqs <= 64 && s >= round && s < 2 * round && s < all)
+        g.seg = (all < 2 * round ? all : 2 * round) - 1 - (s - round);
+      if (g.seg < before + all) {
+        const int x = (int)(g.seg - before), at = __builtin_ctzll(__ballot(m.upto > x));
+        g.i = __builtin_amdgcn_readlane(m.seq, at);
+        g.j = x - (at ? __builtin_amdgcn_readlane(m.upto, at - 1) : 0);
         break;
       }
-      s -= all;
+      before += all;
     }
   }
   const Span sp = span_of(a, g.i);
@@ -279,9 +307,8 @@ __global__ __launch_bounds__(64 * NW, NW / 2 / KS) void attend_kernel(AttendArgs
   const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, li = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const Item item = item_of(blockIdx.x, args.slices * a.heads);
-  const int64_t seg = item.seg;
   const int h = item.row / args.slices, slice = item.row % args.slices;
-  const Segment sg = segment_of(a, args.seg_len, seg, lane);
+  const Segment sg = segment_of(a, args.seg_len, item.seg, args.slices * a.heads, lane);
   if (sg.n == 0 || (!OUT && sg.j == sg.n - 1)) return;
   const int slot = slot_of(a.slots, sg.i, a.nslots, lane);
   if (slot == kPadded) return;
@@ -415,7 +442,7 @@ __global__ __launch_bounds__(64 * NW, NW / 2 / KS) void attend_kernel(AttendArgs
   f32x4 S[CG][KT];
   const int64_t state = ((int64_t)h * a.dv + d0 + w0 + li) * DK + kh * DW + 8 * g, per = (int64_t)a.heads * a.dv * DK;
   float* slot_S = a.S + slot * per + state;
-  float* seg_S = args.ws + seg * per + state;
+  float* seg_S = args.ws + sg.seg * per + state;
   {
     const bool from_ws = OUT && sg.n > 1;
     const bool zero = !OUT || (!from_ws && a.fresh && a.fresh[sg.i]);
@@ -499,10 +526,6 @@ __global__ __launch_bounds__(64 * NW, NW / 2 / KS) void attend_kernel(AttendArgs
     const int buf = RB == 2 ? c & 1 : 0, at = c * C % ROUND;
     const Decays<ROUND>& d = dec[RB == 2 ? c / (ROUND / C) & 1 : 0];
     __syncthreads();
-    if constexpr (RB == 2) {                     // rows of c + 1 to LDS, of c + 2 from memory
-      put_chunk(c + 1, buf ^ 1);
-      read_chunk(c + 2);
-    }
     if constexpr (OUT && BEHIND) finish(c - 1, (c & 1) ^ 1);
     if constexpr (OUT) {
       // ---- P^T tile of a wave: rows s, columns t (the tile above the diagonal is 0)
@@ -537,6 +560,7 @@ __global__ __launch_bounds__(64 * NW, NW / 2 / KS) void attend_kernel(AttendArgs
 #pragma unroll
         for (int i = 0; i < NO; ++i) *reinterpret_cast<bf16x4*>(&pl[BEHIND ? c & 1 : 0][i][t * PP + 8 * g + 4 * si]) = parts[i];
       }
+      if constexpr (RB == 2) __builtin_amdgcn_s_setprio(1);
       // ---- c_t S q
 #pragma unroll
       for (int ks = 0; ks < DW / 32; ++ks) {
@@ -583,6 +607,11 @@ __global__ __launch_bounds__(64 * NW, NW / 2 / KS) void attend_kernel(AttendArgs
     }
     if constexpr (RB == 1)
       if (c + 1 < chunks) read_chunk(c + 1);
+    if constexpr (RB == 2) {                     // rows of c + 1 to LDS, of c + 2 from memory
+      put_chunk(c + 1, buf ^ 1);
+      read_chunk(c + 2);
+    }
+      if constexpr (RB == 2) __builtin_amdgcn_s_setprio(2);
     // ---- S = c_C S + k^T (w v)
     bf16x8 vs[CG][3];
 #pragma unroll
@@ -621,6 +650,7 @@ __global__ __launch_bounds__(64 * NW, NW / 2 / KS) void attend_kernel(AttendArgs
 #pragma unroll
             for (int cg = 0; cg < CG; ++cg) S[cg][I] = mfma(kp[i], vs[cg][j], S[cg][I]);
     }
+    if constexpr (RB == 2) __builtin_amdgcn_s_setprio(0);
     const bool round = at + C == ROUND;             // the next chunk opens a round of decays
     if constexpr (RB == 2) {
       if (round && c + 1 < chunks) put_decays((c + 1) * C, ((c + 1) / (ROUND / C)) & 1);
@@ -655,7 +685,7 @@ __global__ __launch_bounds__(64 * NW, NW / 2 / KS) void attend_kernel(AttendArgs
     __syncthreads();
     if (slice == 0 && tid == 0) {
       for (int w = 1; w < NW; ++w) total += sum[w];
-      args.ws_decay[seg * a.heads + h] = exp2_of(total);
+      args.ws_decay[sg.seg * a.heads + h] = exp2_of(total);
     }
   }
 }
@@ -672,8 +702,14 @@ __global__ __launch_bounds__(256) void combine_kernel(AttendArgs args, int block
   const int lane = threadIdx.x & 63, slot = slot_of(a.slots, i, a.nslots, lane);
   if (slot < 0) return;
   int64_t first = 0;                             // the sequence's first segment
-  for (int i0 = 0; i0 < i; i0 += 64)
-    first += __shfl(segments_upto(a, args.seg_len, i0, lane), i - i0 > 64 ? 63 : i - i0 - 1);
+  for (int i0 = 0;; i0 += 64) {
+    const Numbered m = number_segments(a, args.seg_len, i0, lane);
+    if (i < i0 + 64) {
+      first += __builtin_amdgcn_readlane(m.upto, __builtin_ctzll(__ballot(m.seq == i))) - n;
+      break;
+    }
+    first += __builtin_amdgcn_readlane(m.upto, 63);
+  }
   const int64_t per_head = quads / a.heads;
   const bool fresh = a.fresh && a.fresh[i];
   for (int64_t q = (int64_t)b * 256 + threadIdx.x; q < quads; q += (int64_t)blocks * 256) {
