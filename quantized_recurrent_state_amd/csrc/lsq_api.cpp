@@ -635,7 +635,6 @@ lsq_status lsq_attend(lsq_state* st, const lsq_token_batch* batch, void* workspa
   for (const int64_t x : {batch->q_stride, batch->k_stride, batch->v_stride, batch->o_stride})
     if (x * e > INT32_MAX / 64)                  // lanes address a chunk's rows with 32 bits
       return fail(LSQ_ERR_UNSUPPORTED, "a token stride of 32 MiB or more");
-  const size_t quad = 4 * (size_t)e;           // o is written four elements at a time
   lsq::AttendArgs a{};
   a.s = slot_args(st, batch);
   a.seg_len = p.seg_len;
@@ -643,8 +642,8 @@ lsq_status lsq_attend(lsq_state* st, const lsq_token_batch* batch, void* workspa
   a.ws = static_cast<float*>(workspace);
   a.ws_decay = p.workspace ? reinterpret_cast<float*>(static_cast<char*>(workspace) + p.state_bytes) : nullptr;
   a.slices = p.slices;
-  a.wide = aligned16(batch->v) && batch->v_stride * e % 16 == 0 && c.dv * e % 16 == 0 &&
-           aligned_to(batch->o, quad) && batch->o_stride % 4 == 0;
+  a.wide = e == 4 || (aligned4(batch->v) && aligned4(batch->o) && batch->v_stride % 2 == 0 &&
+                      batch->o_stride % 2 == 0 && c.dv % 2 == 0);
   return slot_status(lsq::launch_attend(a, batch->io, c.dk, hs), "attend launch");
 }
 

@@ -18,6 +18,7 @@
 // outputs (2^-16, against their own half step of 2^-8 or 2^-11).  One rounded
 // part instead would cost half a step of bf16 in the state at every chunk.
 #include <hip/hip_runtime.h>
+#include <math.h>
 #include <stdint.h>
 
 #include "lsq_slots.h"
@@ -43,6 +44,7 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_of(const void* p, int64_t
 }
 
 constexpr int kCUs = 256;
+constexpr int kWhole = 1024;                     // tokens that are not worth two more launches
 
 // A lane offset behind every buffer: chunks are below 2^31 bytes.
 constexpr uint32_t kNowhere = 0xFFFFFFF0u;
@@ -102,7 +104,7 @@ __device__ __forceinline__ f32x4 widen_bf16x4(bf16x4 p) {
 template <int IO>
 __device__ __forceinline__ uint32_t pair16(float x, float y) {
   if constexpr (IO == IO_BF16) return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{x, y}, bf16x2));
-  return to16<IO_F16>(x) | (uint32_t)to16<IO_F16>(y) << 16;
+  else return to16<IO_F16>(x) | (uint32_t)to16<IO_F16>(y) << 16;
 }
 
 __device__ __forceinline__ bf16x8 join(bf16x4 a, bf16x4 b) {
@@ -187,7 +189,7 @@ __device__ __forceinline__ u32x4 keep_elements(u32x4 x, int n) {
 
 // The segment a workgroup takes: sequence i, its j-th of n segments (n = 0:
 // none), number seg.  With a segment length L, a sequence of more than 2 L
-// tokens is cut into its length over L, rounded up.
+// tokens (and more than kWhole) is cut into its length over L, rounded up.
 struct Segment {
   int i, j, n;
   int64_t seg, t0, t1;
@@ -195,7 +197,7 @@ struct Segment {
 
 __device__ __forceinline__ int segments_of(const Span& sp, int64_t L) {
   const int64_t len = sp.t1 > sp.t0 ? sp.t1 - sp.t0 : 0;
-  return L == 0 || len <= 2 * L ? len > 0 : (int)((len + L - 1) / L);
+  return L == 0 || len <= 2 * L || len <= kWhole ? len > 0 : (int)((len + L - 1) / L);
 }
 
 // Segments are numbered without gaps (idle workgroups between busy ones would
@@ -286,8 +288,8 @@ __device__ __forceinline__ Item item_of(int64_t b, int rows) {
 // products are independent of each other: S q and the new S, P of the same
 // chunk, and (BEHIND) P v of the chunk before, with the next rows on their way
 // to LDS, all between two barriers.  OUT = false adds up a segment's writes alone
-// (no q, no output), for the segments behind it.  VEC: v and o by whole units
-// (else by element, for odd widths and addresses).
+// (no q, no output), for the segments behind it.  VEC: v and o by dwords and
+// more (else by element: 16-bit types of odd widths or addresses).
 template <int IO, int DK, int NW, int CG, int KS, bool VEC, bool OUT>
 __global__ __launch_bounds__(64 * NW, NW / 2 / KS) void attend_kernel(AttendArgs args) {
   using T = Tile<IO, DK, NW, CG, KS>;
@@ -367,9 +369,6 @@ __global__ __launch_bounds__(64 * NW, NW / 2 / KS) void attend_kernel(AttendArgs
     for (int n = 0; n < T::VU; ++n) {
       if constexpr (VEC) {
         rv[n] = __builtin_amdgcn_raw_buffer_load_b128(vb, vo, 0, 0);
-      } else if constexpr (IO == IO_F32) {
-#pragma unroll
-        for (int x = 0; x < EU; ++x) rv[n][x] = __builtin_amdgcn_raw_buffer_load_b32(vb, vo + x * B, 0, 0);
       } else {
         uint32_t w[EU];
 #pragma unroll
@@ -487,12 +486,17 @@ __global__ __launch_bounds__(64 * NW, NW / 2 / KS) void attend_kernel(AttendArgs
       for (int cg = 0; cg < CG; ++cg) {
         const f32x4 x = acc[cg][ti];
         const int left = vcols - (w0 + 16 * cg + 4 * g);               // columns to write, four per lane
-        if constexpr (VEC) {
+        if (VEC && vcols % 4 == 0) {
           const uint32_t e = left > 0 ? oo + 16 * cg * B : kNowhere;
           if constexpr (IO == IO_F32)
             __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, x), ob, e, 0, 0);
           else
             __builtin_amdgcn_raw_buffer_store_b64(u32x2{pair16<IO>(x[0], x[1]), pair16<IO>(x[2], x[3])}, ob, e, 0, 0);
+        } else if (VEC && IO != IO_F32) {
+#pragma unroll
+          for (int v = 0; v < 4; v += 2)
+            __builtin_amdgcn_raw_buffer_store_b32(pair16<IO>(x[v], x[v + 1]), ob,
+                                                  v < left ? oo + (16 * cg + v) * B : kNowhere, 0, 0);
         } else {
 #pragma unroll
           for (int v = 0; v < 4; ++v) {
@@ -717,14 +721,21 @@ __global__ __launch_bounds__(256) void combine_kernel(AttendArgs args, int block
     f32x4 S = {0.f, 0.f, 0.f, 0.f};
     if (!fresh) S = reinterpret_cast<const f32x4*>(a.S)[slot * quads + q];
     f32x4* ws = reinterpret_cast<f32x4*>(args.ws) + first * quads + q;
-    f32x4 x = ws[0];
-    for (int j = 0; j < n; ++j) {
-      ws[j * quads] = S;
-      if (j + 1 < n) {
-        const f32x4 next = j + 2 < n ? ws[(j + 1) * quads] : x;   // the last segment's writes are not needed
-        S = S * decay[(int64_t)j * a.heads] + x;
-        x = next;
+    for (int j0 = 0; j0 < n; j0 += 4) {          // four segments' writes in flight
+      f32x4 x[4];
+      float c[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int64_t k = j0 + j < n - 1 ? j0 + j : n - 2;   // the last segment's writes are not needed
+        x[j] = ws[k * quads];
+        c[j] = decay[k * a.heads];
       }
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (j0 + j < n) {
+          ws[(j0 + j) * quads] = S;
+          S = S * c[j] + x[j];
+        }
     }
   }
 }
@@ -754,8 +765,7 @@ hipError_t launch_instance(const AttendArgs& args, unsigned blocks, hipStream_t 
 template <int IO, int DK>
 hipError_t launch_width(const AttendArgs& args, unsigned blocks, hipStream_t s) {
   if constexpr (IO == IO_F32) {
-    return args.wide ? launch_instance<IO, DK, 8, 1, 2, true>(args, blocks, s)
-                     : launch_instance<IO, DK, 8, 1, 2, false>(args, blocks, s);
+    return launch_instance<IO, DK, 8, 1, 2, true>(args, blocks, s);
   } else {
     if (slice_width(IO, args.s.dv) == 128)
       return args.wide ? launch_instance<IO, DK, 8, 1, 1, true>(args, blocks, s)
@@ -772,13 +782,21 @@ AttendPlan attend_plan(int64_t tokens, int32_t seqs, int32_t heads, int32_t dk, 
   const int width = slice_width(io, dv);
   p.slices = (dv + width - 1) / width;
   p.segments = seqs;
-  // Segments of a 512th of the work (two workgroups on each of 256 CUs), 512
-  // tokens at least.  The host does not see the lengths: a batch of fewer than
-  // eight segments' tokens is taken whole, in a longer one the kernels cut the
-  // sequences of more than two segments.
-  int64_t L = (tokens * heads * p.slices / 512 + 63) / 64 * 64;
-  if (L < 512) L = 512;
-  if (tokens >= 8 * L) {
+  // A segment: a 512th of the work (two workgroups on each of 256 CUs), but 256
+  // tokens at least, and more where a long sequence has few rows, so that the
+  // combination's steps (0.5 us each) and a segment's chunks (3.5 us for both
+  // passes) take as long.  The host does not see the lengths: where the rows
+  // alone occupy the CUs, or the sequences are short on average, a batch of few
+  // tokens is taken whole; otherwise the kernels cut the sequences of more than
+  // two segments.
+  const int64_t rows = (int64_t)heads * p.slices;
+  int64_t L = tokens * rows / 512;
+  const int64_t root = (int64_t)(2.0 * sqrt((double)tokens));
+  if (L < root) L = root;
+  if (L < 256) L = 256;
+  L = (L + 63) / 64 * 64;
+  const bool alone = (int64_t)seqs * rows < dev::kCUs && tokens >= (int64_t)seqs * dev::kWhole;
+  if (tokens > dev::kWhole && (alone || tokens >= (8 * L > 4096 ? 8 * L : 4096))) {
     p.seg_len = L;
     p.segments = tokens / L + seqs;
     p.state_bytes = p.segments * heads * dv * dk * 4;

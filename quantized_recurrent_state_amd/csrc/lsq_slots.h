@@ -36,7 +36,7 @@ struct AttendArgs {
   float* ws;               // [segments][heads][dv][dk], then ws_decay (null without segments)
   float* ws_decay;         // [segments][heads]
   int32_t slices;          // workgroups over a head's value columns
-  int32_t wide;            // v and o allow 16-byte reads and four-element writes
+  int32_t wide;            // rows of v and o begin at dwords
 };
 
 struct AttendPlan {
