@@ -395,8 +395,8 @@ lsq_status lsq_attend_workspace(const lsq_state* st, const lsq_token_batch* batc
  * The step index does not move.  INVALID_ARG: null or misaligned pointers,
  * seqs < 0, tokens < 0, qk_heads not dividing heads, an o_stride below
  * heads * dv or a negative stride, a workspace of NULL where one is needed;
- * BUFFER_TOO_SMALL: a smaller workspace; UNSUPPORTED: a quantised handle, or
- * more than 2^31 - 1 workgroups. */
+ * BUFFER_TOO_SMALL: a smaller workspace; UNSUPPORTED: a quantised handle, a
+ * token stride of 32 MiB or more, or more than 2^31 - 1 workgroups. */
 lsq_status lsq_attend(lsq_state* st, const lsq_token_batch* batch, void* workspace,
                       size_t workspace_bytes, void* stream);
 

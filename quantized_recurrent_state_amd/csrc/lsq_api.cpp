@@ -639,6 +639,7 @@ lsq_status lsq_attend(lsq_state* st, const lsq_token_batch* batch, void* workspa
   a.s = slot_args(st, batch);
   a.seg_len = p.seg_len;
   a.segments = p.segments;
+  a.cut = p.cut;
   a.ws = static_cast<float*>(workspace);
   a.ws_decay = p.workspace ? reinterpret_cast<float*>(static_cast<char*>(workspace) + p.state_bytes) : nullptr;
   a.slices = p.slices;

@@ -188,11 +188,12 @@ __device__ __forceinline__ u32x4 keep_elements(u32x4 x, int n) {
 }
 
 // The segment a workgroup takes: sequence i, its j-th of n segments (n = 0:
-// none), number seg.  With a segment length L, a sequence of more than 2 L
-// tokens (and more than kWhole) is cut into its length over L, rounded up.
+// none).  With a segment length L, a sequence of more than 2 L tokens (and more
+// than kWhole) is cut into its length over L, rounded up; ws is the segment's
+// number among those of cut sequences, which alone use the workspace.
 struct Segment {
-  int i, j, n;
-  int64_t seg, t0, t1;
+  int i, j, n, ws;
+  int64_t t0, t1;
 };
 
 __device__ __forceinline__ int segments_of(const Span& sp, int64_t L) {
@@ -202,11 +203,11 @@ __device__ __forceinline__ int segments_of(const Span& sp, int64_t L) {
 
 // Segments are numbered without gaps (idle workgroups between busy ones would
 // leave whole shader engines idle), 64 sequences at a time: lane r has the
-// group's r-th sequence and the segments up to it.  Up to 64 sequences are
-// ordered by length, the longest first; with more of them the order matters
-// little, and a workgroup's search stays short.
+// group's r-th sequence, the segments up to it and those of cut sequences among
+// them.  Up to 64 sequences are ordered by length, the longest first; with more
+// of them the order matters little, and a workgroup's search stays short.
 struct Numbered {
-  int seq, upto;
+  int seq, n, upto, cut;
 };
 
 __device__ __forceinline__ Numbered number_segments(const SlotArgs& a, int64_t L, int i0, int lane) {
@@ -220,38 +221,48 @@ __device__ __forceinline__ Numbered number_segments(const SlotArgs& a, int64_t L
       const int x = __builtin_amdgcn_readlane(len, j);
       rank += in && (x > len || (x == len && j < lane));
     }
-  int n = __builtin_amdgcn_ds_permute(4 * rank, segments_of(sp, L));
-  const int seq = __builtin_amdgcn_ds_permute(4 * rank, i0 + lane);
+  Numbered m;
+  m.n = __builtin_amdgcn_ds_permute(4 * rank, segments_of(sp, L));
+  m.seq = __builtin_amdgcn_ds_permute(4 * rank, i0 + lane);
+  m.upto = m.n;
+  m.cut = m.n > 1 ? m.n : 0;
 #pragma unroll
   for (int o = 1; o < 64; o *= 2) {
-    const int up = __shfl_up(n, o);
-    if (lane >= o) n += up;
+    const int up = __shfl_up(m.upto, o), cut = __shfl_up(m.cut, o);
+    if (lane >= o) {
+      m.upto += up;
+      m.cut += cut;
+    }
   }
-  return {seq, n};
+  return m;
 }
 
+// Segment s of the batch, of the cut sequences alone where CUT.  rows:
+// workgroups per segment.
+template <bool CUT>
 __device__ __forceinline__ Segment segment_of(const SlotArgs& a, int64_t L, int64_t s, int rows, int lane) {
   Segment g{};
-  g.seg = s;
   g.i = (int)s;
   if (L || (int64_t)a.seqs * rows > kCUs) {
-    int64_t before = 0;
+    int before = 0;                              // cut segments of earlier groups
     for (int i0 = 0;; i0 += 64) {
       if (i0 >= a.seqs) return g;
       const Numbered m = number_segments(a, L, i0, lane);
-      const int all = __builtin_amdgcn_readlane(m.upto, 63);
+      const int upto = CUT ? m.cut : m.upto, all = __builtin_amdgcn_readlane(upto, 63);
       // Two workgroups share a CU: those of the second round in reverse, a long
       // sequence beside a short one.
       const int64_t round = kCUs / rows;
-      if (a.seqs <= 64 && s >= round && s < 2 * round && s < all)
-        g.seg = (all < 2 * round ? all : 2 * round) - 1 - (s - round);
-      if (g.seg < before + all) {
-        const int x = (int)(g.seg - before), at = __builtin_ctzll(__ballot(m.upto > x));
+      if (!CUT && a.seqs <= 64 && s >= round && s < 2 * round && s < all)
+        s = (all < 2 * round ? all : 2 * round) - 1 - (s - round);
+      if (s < all) {
+        const int at = __builtin_ctzll(__ballot(upto > (int)s));
         g.i = __builtin_amdgcn_readlane(m.seq, at);
-        g.j = x - (at ? __builtin_amdgcn_readlane(m.upto, at - 1) : 0);
+        g.j = (int)s - (__builtin_amdgcn_readlane(upto, at) - __builtin_amdgcn_readlane(m.n, at));
+        g.ws = before + __builtin_amdgcn_readlane(m.cut, at) - __builtin_amdgcn_readlane(m.n, at) + g.j;
         break;
       }
-      before += all;
+      s -= all;
+      before += __builtin_amdgcn_readlane(m.cut, 63);
     }
   }
   const Span sp = span_of(a, g.i);
@@ -310,8 +321,11 @@ __global__ __launch_bounds__(64 * NW, NW / 2 / KS) void attend_kernel(AttendArgs
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const Item item = item_of(blockIdx.x, args.slices * a.heads);
   const int h = item.row / args.slices, slice = item.row % args.slices;
-  const Segment sg = segment_of(a, args.seg_len, item.seg, args.slices * a.heads, lane);
+  const Segment sg = segment_of<!OUT>(a, args.seg_len, item.seg, args.slices * a.heads, lane);
   if (sg.n == 0 || (!OUT && sg.j == sg.n - 1)) return;
+  // Offsets that decrease can name a token in several sequences, more of them
+  // than the workspace was sized for.
+  if (sg.j < 0 || sg.j >= sg.n || (sg.n > 1 && (sg.ws < 0 || sg.ws >= args.cut))) return;
   const int slot = slot_of(a.slots, sg.i, a.nslots, lane);
   if (slot == kPadded) return;
   const int d0 = slice * T::DV, vcols = a.dv - d0 < T::DV ? a.dv - d0 : T::DV;   // the slice's columns
@@ -441,7 +455,7 @@ __global__ __launch_bounds__(64 * NW, NW / 2 / KS) void attend_kernel(AttendArgs
   f32x4 S[CG][KT];
   const int64_t state = ((int64_t)h * a.dv + d0 + w0 + li) * DK + kh * DW + 8 * g, per = (int64_t)a.heads * a.dv * DK;
   float* slot_S = a.S + slot * per + state;
-  float* seg_S = args.ws + sg.seg * per + state;
+  float* seg_S = args.ws + sg.ws * per + state;
   {
     const bool from_ws = OUT && sg.n > 1;
     const bool zero = !OUT || (!from_ws && a.fresh && a.fresh[sg.i]);
@@ -689,7 +703,7 @@ __global__ __launch_bounds__(64 * NW, NW / 2 / KS) void attend_kernel(AttendArgs
     __syncthreads();
     if (slice == 0 && tid == 0) {
       for (int w = 1; w < NW; ++w) total += sum[w];
-      args.ws_decay[sg.seg * a.heads + h] = exp2_of(total);
+      args.ws_decay[sg.ws * a.heads + h] = exp2_of(total);
     }
   }
 }
@@ -705,15 +719,16 @@ __global__ __launch_bounds__(256) void combine_kernel(AttendArgs args, int block
   if (n < 2) return;
   const int lane = threadIdx.x & 63, slot = slot_of(a.slots, i, a.nslots, lane);
   if (slot < 0) return;
-  int64_t first = 0;                             // the sequence's first segment
+  int64_t first = 0;                             // the sequence's first segment in the workspace
   for (int i0 = 0;; i0 += 64) {
     const Numbered m = number_segments(a, args.seg_len, i0, lane);
     if (i < i0 + 64) {
-      first += __builtin_amdgcn_readlane(m.upto, __builtin_ctzll(__ballot(m.seq == i))) - n;
+      first += __builtin_amdgcn_readlane(m.cut, __builtin_ctzll(__ballot(m.seq == i))) - n;
       break;
     }
-    first += __builtin_amdgcn_readlane(m.upto, 63);
+    first += __builtin_amdgcn_readlane(m.cut, 63);
   }
+  if (first < 0 || first + n > args.cut) return;   // decreasing offsets, as above
   const int64_t per_head = quads / a.heads;
   const bool fresh = a.fresh && a.fresh[i];
   for (int64_t q = (int64_t)b * 256 + threadIdx.x; q < quads; q += (int64_t)blocks * 256) {
@@ -752,7 +767,8 @@ template <int IO, int DK, int NW, int CG, int KS, bool VEC>
 hipError_t launch_instance(const AttendArgs& args, unsigned blocks, hipStream_t s) {
   const SlotArgs& a = args.s;
   if (args.seg_len) {
-    hipLaunchKernelGGL((dev::attend_kernel<IO, DK, NW, CG, KS, VEC, false>), dim3(blocks), dim3(64 * NW), 0, s, args);
+    const unsigned cut = (unsigned)(args.cut * args.slices * a.heads);
+    hipLaunchKernelGGL((dev::attend_kernel<IO, DK, NW, CG, KS, VEC, false>), dim3(cut), dim3(64 * NW), 0, s, args);
     const int64_t quads = (int64_t)a.heads * a.dv * DK / 4, most = 4096 / a.seqs + 1;
     const int64_t per = (quads + 255) / 256 < most ? (quads + 255) / 256 : most;
     hipLaunchKernelGGL(dev::combine_kernel, dim3((unsigned)(per * a.seqs)), dim3(256), 0, s, args,
@@ -799,8 +815,11 @@ AttendPlan attend_plan(int64_t tokens, int32_t seqs, int32_t heads, int32_t dk, 
   if (tokens > dev::kWhole && (alone || tokens >= (8 * L > 4096 ? 8 * L : 4096))) {
     p.seg_len = L;
     p.segments = tokens / L + seqs;
-    p.state_bytes = p.segments * heads * dv * dk * 4;
-    p.workspace = (size_t)(p.state_bytes + p.segments * heads * 4);
+    // a cut sequence has more than 2 L tokens and at most one segment that is
+    // not full: fewer than half as many again as there are full ones
+    p.cut = tokens / L + tokens / (2 * L) + 1;
+    p.state_bytes = p.cut * heads * dv * dk * 4;
+    p.workspace = (size_t)(p.state_bytes + p.cut * heads * 4);
   }
   return p;
 }

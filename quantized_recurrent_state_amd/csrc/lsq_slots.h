@@ -32,15 +32,15 @@ struct SlotArgs {
 struct AttendArgs {
   SlotArgs s;
   int64_t seg_len;         // tokens per segment, a multiple of 64; 0: whole sequences
-  int64_t segments;        // upper bound of their number
-  float* ws;               // [segments][heads][dv][dk], then ws_decay (null without segments)
-  float* ws_decay;         // [segments][heads]
+  int64_t segments, cut;   // upper bounds of their number, and of those of cut sequences
+  float* ws;               // [cut][heads][dv][dk], then ws_decay (null without segments)
+  float* ws_decay;         // [cut][heads]
   int32_t slices;          // workgroups over a head's value columns
   int32_t wide;            // rows of v and o begin at dwords
 };
 
 struct AttendPlan {
-  int64_t seg_len, segments, state_bytes;
+  int64_t seg_len, segments, cut, state_bytes;
   size_t workspace;        // bytes
   int32_t slices;
 };

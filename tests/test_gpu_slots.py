@@ -408,3 +408,159 @@ def test_attend_long_and_segments(io):
     run_attend([1500, 3, 700, 64], 1, 1, 64, 64, TYPES[io], slots=[1, 0, 3, 2],
                fresh=[False, False, True, False], seed=13)
     run_attend([2100], 1, 1, 128, 128, TYPES[io], seed=14, slow=True)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("seqs", [9, 70])
+def test_attend_cuts_only_the_long_ones(io, seqs):
+    """Few long sequences among many short ones: the long ones are cut, wherever they stand."""
+    lens = [(5 * i) % 37 for i in range(seqs)]
+    lens[2], lens[seqs - 3] = 1700, 2600
+    run_attend(lens, 1, 1, 64, 64, TYPES[io], slots=[(7 * i) % (seqs + 4) for i in range(seqs)] if seqs != 70
+               else [(7 * i) % 73 for i in range(seqs)], n_slots=seqs + 4, fresh=[i % 3 == 0 for i in range(seqs)],
+               seed=15)
+
+
+def test_attend_refuses_and_pads_cut_sequences():
+    st, S = state(4, 1, 64, 64)
+    q, k, v, alpha, beta = tokens(4 * 1500, 1, 1, 64, 64, torch.bfloat16, 16)
+    o = torch.full((6000, 1, 64), 7.0, dtype=torch.bfloat16, device=DEV)
+    cu = torch.tensor([0, 1500, 3000, 4500, 6000], dtype=torch.int32, device=DEV)
+    st.attend(*(x.to(DEV) for x in (q, k, v, alpha, beta)), cu,
+              slots=torch.tensor([3, -1, 3, 8], dtype=torch.int32, device=DEV), o=o)
+    want, pool, ao, mag = batch_ref(S, [3], None, [0, 1500], q, k, v, alpha, beta)
+    check_out(o[:1500], want[:1500], ao[:1500], 1500, 64, torch.bfloat16)
+    check_state(st, pool, mag, 1500)
+    assert bool((o[1500:3000] == 7).all()) and bool(o[3000:].isnan().all())
+
+
+def test_spoilt_offsets_of_long_sequences_stay_inside():
+    # the same tokens named twice: no slot but the named ones, no memory outside, is touched
+    st, S = state(6, 1, 64, 64)
+    q, k, v, alpha, beta = (x.to(DEV) for x in tokens(6000, 1, 1, 64, 64, torch.bfloat16, 17))
+    guard = torch.full((6002, 1, 64), 5.0, dtype=torch.bfloat16, device=DEV)
+    cu = torch.tensor([0, 6000, 0, 6000, 0, 6000], dtype=torch.int32, device=DEV)
+    st.attend(q, k, v, alpha, beta, cu, slots=torch.tensor([0, 1, 2, 3, 4], dtype=torch.int32, device=DEV),
+              o=guard[1:6001])
+    assert bool((guard[0] == 5).all()) and bool((guard[6001] == 5).all())
+    assert torch.equal(st.f32.view(6, 1, 64, 64)[5].cpu(), S[5])
+
+
+@pytest.mark.parametrize("io", TYPES)
+def test_attend_broadcast_inputs(io):
+    # one q, k or v row shared by all tokens (stride 0), with a last chunk that is not full
+    dtype, n, heads, dk, dv = TYPES[io], 75, 2, 64, 64
+    st, S = state(1, heads, dk, dv)
+    q, k, v, alpha, beta = tokens(n, heads, heads, dk, dv, dtype, 18)
+    q, k, v = (x[:1].expand(n, heads, 64) for x in (q, k, v))
+    dev = [x[:1].to(DEV).expand(n, heads, 64) for x in (q, k, v)]
+    o = st.attend(*dev, alpha.to(DEV), beta.to(DEV), torch.tensor([0, n], dtype=torch.int32, device=DEV))
+    want, pool, ao, mag = batch_ref(S, [0], None, [0, n], q, k, v, alpha, beta)
+    check_out(o, want, ao, n, dk, dtype)
+    check_state(st, pool, mag, n)
+    o = st.step_slots(*(x[:1] for x in dev), alpha[:1].to(DEV), beta[:1].to(DEV))
+    want, pool, ao, mag = batch_ref(pool, [0], None, [0, 1], q, k, v, alpha, beta)
+    check_out(o, want[:1], ao[:1], n + 1, dk, dtype)
+
+
+def test_attend_skips_rows_before_and_behind():
+    # NaN in rows that no sequence owns reaches nothing
+    st, S = state(2, 2, 64, 64)
+    q, k, v, alpha, beta = tokens(120, 2, 2, 64, 64, torch.bfloat16, 19)
+    for x in (q, k, v, alpha, beta):
+        x[:11] = float("nan")
+        x[61:64] = float("nan")
+        x[110:] = float("nan")
+    cu, slots = [11, 61, 64, 110], [0, -1, 1]
+    o = st.attend(*(x.to(DEV) for x in (q, k, v, alpha, beta)), torch.tensor(cu, dtype=torch.int32, device=DEV),
+                  slots=torch.tensor(slots, dtype=torch.int32, device=DEV),
+                  o=torch.full((120, 2, 64), float("nan"), dtype=torch.bfloat16, device=DEV))
+    want, pool, ao, mag = batch_ref(S, slots, None, cu, q, k, v, alpha, beta)
+    assert bool(o.cpu()[want.isnan()].isnan().all())
+    check_out(o, want, ao, 50, 64, torch.bfloat16)
+    check_state(st, pool, mag, 50)
+
+
+@pytest.mark.parametrize("io", TYPES)
+def test_nothing_written_leaves_the_state_bit_for_bit(io):
+    st, S = state(2, 2, 128, 128)
+    q, k, v, alpha, beta = tokens(1700, 2, 2, 128, 128, TYPES[io], 20)
+    alpha, beta = torch.ones_like(alpha), torch.zeros_like(beta)
+    st.attend(*(x.to(DEV) for x in (q, k, v, alpha, beta)), torch.tensor([0, 1600, 1700], dtype=torch.int32, device=DEV))
+    assert torch.equal(st.f32.cpu().view(S.shape), S)
+
+
+def test_pools_and_strides_beyond_32_bits():
+    """The last slots of a pool of more than 4 GiB, and rows more than 4 GiB apart."""
+    heads, dk, dv, dtype = 32, 128, 128, torch.bfloat16
+    n_slots = 2200                               # 2 MiB each
+    st = lsq.LsqState(lsq.LsqConfig(n_slots, heads, dk, dv, 32, 1, lsq.POLICY_NONE), device=DEV)
+    st.f32.zero_()
+    last = torch.randn((2, heads, dv, dk), generator=torch.Generator().manual_seed(21))
+    st.f32.view(n_slots, heads, dv, dk)[-2:] = last.to(DEV)
+    slots = torch.tensor([n_slots - 1, n_slots - 2], dtype=torch.int32, device=DEV)
+    cache = lsq.LsqState(lsq.LsqConfig(n_slots, heads, dk, dv, 8, 64, lsq.POLICY_DYNAMIC), device=DEV)
+    cache.store_slots(st, slots=slots, src_slots=slots)
+    want = lsq.LsqState(lsq.LsqConfig(2, heads, dk, dv, 8, 64, lsq.POLICY_DYNAMIC), device=DEV)
+    want.calibrate(last.view(-1, dv, dk).to(DEV))
+    assert torch.equal(cache.codes.view(n_slots, -1)[-2:], want.codes.view(2, -1))
+    cache.load_slots(st, slots=slots, dst_slots=slots)
+    base = want.dequantize().view(2, heads, dv, dk).cpu()
+    assert torch.equal(st.f32.view(n_slots, heads, dv, dk)[-2:].cpu(), base)
+    assert not bool(st.f32.view(n_slots, -1)[0].any())
+    # q and v as slices of rows of 8 MiB elements: token 300 lies 4.7 GiB behind token 0
+    n, row = 300, 8 << 20
+    q, k, v, alpha, beta = tokens(n, heads, 1, dk, dv, dtype, 22)
+    wide = torch.zeros((n, row), dtype=dtype, device=DEV)
+    wide[:, :dk] = q[:, 0].to(DEV)
+    wide[:, 1024:1024 + heads * dv] = v.flatten(1).to(DEV)
+    a, b = alpha.to(DEV), beta.to(DEV)
+    cu = torch.tensor([0, n - 1], dtype=torch.int32, device=DEV)
+    args = [wide[:, :dk].unflatten(1, (1, dk)), k.to(DEV), wide[:, 1024:1024 + heads * dv].unflatten(1, (heads, dv))]
+    o = st.attend(*args, a, b, cu, slots=slots[:1])
+    ref, pool, ao, mag = batch_ref(base[1:], [0], None, [0, n - 1], q, k, v, alpha, beta)
+    check_out(o[:n - 1], ref[:n - 1], ao[:n - 1], n, dk, dtype)
+    got = st.f32.view(n_slots, heads, dv, dk)[-1:].cpu()
+    assert rel(got, pool) <= 16 * U32
+    o = st.step_slots(*(x[n - 1:] for x in args), a[n - 1:], b[n - 1:], slots=slots[1:])
+    ref, pool, ao, mag = batch_ref(base[:1], [0], None, [0, 1], *(x[n - 1:] for x in (q, k, v, alpha, beta)))
+    check_out(o, ref, ao, 1, dk, dtype)
+    assert rel(st.f32.view(n_slots, heads, dv, dk)[-2:-1].cpu(), pool) <= 16 * U32
+
+
+def test_two_streams_and_two_graphs_with_cut_sequences():
+    """Two batches on two streams at once, then two captured graphs replayed in turn: each has a
+    workspace of its own, and every replay equals the eager run."""
+    heads, dk, dv, dtype = 2, 64, 64, torch.bfloat16
+    data = [[x.to(DEV) for x in tokens(3000, heads, heads, dk, dv, dtype, 23 + i)] for i in range(2)]
+    cu = torch.tensor([0, 1400, 3000], dtype=torch.int32, device=DEV)
+    slots = [torch.tensor(x, dtype=torch.int32, device=DEV) for x in ([0, 1], [3, 2])]
+
+    def eager(i):
+        st, _ = state(4, heads, dk, dv)
+        return st.attend(*data[i], cu, slots=slots[i]), st.f32.view(4, -1)[slots[i].long()]
+
+    want = [eager(0), eager(1)]
+    st, S = state(4, heads, dk, dv)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [st.attend(*data[i], cu, slots=slots[i], stream=streams[i]) for i in range(2)]
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert torch.equal(got[i], want[i][0])
+        assert torch.equal(st.f32.view(4, -1)[slots[i].long()], want[i][1])
+    S = S.to(DEV).view(st.f32.shape)
+    graphs, outs = [], []
+    for i in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(st.attend(*data[i], cu, slots=slots[i]))
+        graphs.append(g)
+    for _ in range(3):
+        st.f32.copy_(S)
+        for i in (1, 0):
+            graphs[i].replay()
+        torch.cuda.synchronize()
+        for i in range(2):
+            assert torch.equal(outs[i], want[i][0])
+            assert torch.equal(st.f32.view(4, -1)[slots[i].long()], want[i][1])

@@ -80,6 +80,31 @@ def test_other_refusals():
     lsq.lsq_state_free(d)
 
 
+def test_attend_workspace():
+    """Few tokens need none; many need a bounded one, which is checked."""
+    L = _lib.load()
+    h = handle()
+    n = ctypes.c_size_t(1)
+    need = lambda b: (L.lsq_attend_workspace(h, ctypes.byref(b), ctypes.byref(n)), n.value)[1]
+    assert need(batch(tokens=1000, seqs=1)) == 0
+    assert need(batch(tokens=0)) == 0
+    one = need(batch(tokens=100_000, seqs=1))
+    assert 0 < one <= need(batch(tokens=100_000, seqs=1000)) <= 64 << 20
+    b = batch(tokens=100_000, seqs=1)
+    assert L.lsq_attend(h, ctypes.byref(b), None, 0, None) == 1
+    assert L.lsq_attend(h, ctypes.byref(b), None, one, None) == 1
+    assert L.lsq_attend(h, ctypes.byref(b), FAKE + 4, one, None) == 1
+    assert L.lsq_attend(h, ctypes.byref(b), FAKE, one - 1, None) == 3
+    far = 16 << 20                                       # elements: 32 MiB between tokens
+    for name in ("q_stride", "k_stride", "v_stride", "o_stride"):
+        assert L.lsq_attend(h, ctypes.byref(batch(tokens=100, **{name: far})), None, 0, None) == 2
+    lsq.lsq_state_free(h)
+    for kw in (dict(delta=1), dict(decay=lsq.DECAY_DIAG)):   # token by token: none
+        h = handle(**kw)
+        assert need(batch(tokens=100_000, seqs=1)) == 0
+        lsq.lsq_state_free(h)
+
+
 def test_nothing_to_do_needs_no_pointers():
     L = _lib.load()
     h = handle()
