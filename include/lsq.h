@@ -368,7 +368,8 @@ typedef struct {
   const uint8_t* fresh;       /* [seqs], or NULL: none is fresh */
 } lsq_token_batch;
 
-/* Bytes of workspace lsq_attend needs for this batch (0 when it needs none).
+/* Bytes of workspace lsq_attend needs for this batch (0 when it needs none, as
+ * every batch of up to 1024 tokens).
  * Host only; depends on the handle's configuration, io, qk_heads, seqs and
  * tokens alone. */
 lsq_status lsq_attend_workspace(const lsq_state* st, const lsq_token_batch* batch, size_t* bytes);

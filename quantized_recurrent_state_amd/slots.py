@@ -15,6 +15,11 @@ from . import DECAY_DIAG, IO_BF16, IO_F16, IO_F32, LsqState, _lib
 _IO = {torch.float32: IO_F32, torch.float16: IO_F16, torch.bfloat16: IO_BF16}
 
 
+# The current stream's address without the Stream object around it, where torch has the call.
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                          lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _buffer(state):
     return state.f32 if state.codes is None else state.codes
 
@@ -28,9 +33,9 @@ def _on_device(index, stream, call):
         with torch.cuda.stream(stream):
             return call(stream.cuda_stream)
     if index == torch.cuda.current_device():
-        return call(torch.cuda.current_stream(index).cuda_stream)
+        return call(_current_stream(index))
     with torch.cuda.device(index):
-        return call(torch.cuda.current_stream(index).cuda_stream)
+        return call(_current_stream(index))
 
 
 def _plain(name, t, shape, dtype, index):
@@ -102,13 +107,14 @@ def attend(state, q, k, v, alpha, beta, cu_seqlens, slots, fresh, o, stream):
     def call(s):
         lib = _lib.load()
         b, out = token_batch(state, q, k, v, alpha, beta, cu_seqlens, slots, fresh, o)
-        b = ctypes.byref(b)
-        need = ctypes.c_size_t()
-        status = lib.lsq_attend_workspace(state.handle, b, ctypes.byref(need))
-        if status == 0:
+        nb, ws, status = 0, None, 0
+        if b.tokens > 1024:                  # smaller batches need none
+            need = ctypes.c_size_t()
+            status = lib.lsq_attend_workspace(state.handle, ctypes.byref(b), ctypes.byref(need))
             nb = need.value
             ws = torch.empty(nb, dtype=torch.uint8, device=out.device) if nb else None
-            status = lib.lsq_attend(state.handle, b, ws.data_ptr() if nb else None, nb, s)
+        if status == 0:
+            status = lib.lsq_attend(state.handle, ctypes.byref(b), ws.data_ptr() if nb else None, nb, s)
         if status:
             _lib.check(status, "lsq_attend")
         return out
