@@ -151,15 +151,43 @@ __device__ __forceinline__ double lane_of(double x, int lane) {
 // 2^x of a double, to fp32.
 __device__ __forceinline__ float exp2_of(double x) {
   const float h = (float)x;
-  return exp2f(h) * (1.f + 0.69314718f * (float)(x - (double)h));
+  return __builtin_amdgcn_exp2f(h) * (1.f + 0.69314718f * (float)(x - (double)h));
+}
+
+// log2(x) of 0 <= x, to 2^-26 of itself, also next to one; -160 for 0
+// and subnormals, NaN for negative x and NaN.  x = 2^e (1 + f) with 1 + f
+// from sqrt(1/2) to sqrt(2), log2(1 + f) = 2 / ln 2 atanh(s), s = f / (2 + f) in
+// |s| <= 0.1716: atanh(s) = s (1 + s^2/3 + s^4/5 + ...), the bracket's tail in
+// fp32 (its rounding is scaled by s^2), s and the product with 2 / ln 2 as sums
+// of two floats.  A library log2 in fp64 cost 2 us per round on the critical
+// path of a chunk.
+__device__ __forceinline__ double log2_of(float x) {
+  float m = __builtin_amdgcn_frexp_mantf(x);     // in [1/2, 1)
+  int e = __builtin_amdgcn_frexp_expf(x);
+  if (m < 0.70710678f) {
+    m *= 2.f;
+    --e;
+  }
+  const float f = m - 1.f;                       // exact
+  const float t = 2.f + f, tl = (2.f - t) + f;   // t + tl = 2 + f
+  const float r = __builtin_amdgcn_rcpf(t);
+  const float s = f * r;
+  const float sl = (fmaf(-s, t, f) - s * tl) * r;   // s + sl = f / (2 + f)
+  const float z = s * s;
+  const float tail = z * fmaf(z, fmaf(z, fmaf(z, fmaf(z, fmaf(z, 1.f / 13, 1.f / 11), 1.f / 9), 1.f / 7), 0.2f), 1.f / 3);
+  constexpr float C = 2.8853900817779268f, CL = (float)(2.8853900817779268 - (double)C);   // 2 / ln 2
+  const float h = C * s;
+  const float l = fmaf(C, s, -h) + (fmaf(CL, s, C * sl) + h * tail);
+  double y = (double)e + ((double)h + (double)l);
+  if (!(x >= 0x1p-126f)) y = x >= 0.f ? -160.0 : __builtin_nan("");   // 0 and subnormals count as 0
+  return y;
 }
 
 // One wave fills the decays of its 64 tokens (alpha 1 and beta 0 behind the
 // sequence) from at on; returns the lane's log2(alpha).
 template <int C, int N>
 __device__ __forceinline__ double fill_decays(Decays<N>& d, int at, float alpha, float beta, int lane) {
-  double l = log2((double)alpha);
-  l = l < -160.0 ? -160.0 : l;
+  double l = log2_of(alpha);
   const double own = l;
   l += dpp_or_zero<0x111, 0xF>(l);               // row_shr 1, 2, 4, 8: sums within 16 lanes
   l += dpp_or_zero<0x112, 0xF>(l);
@@ -342,7 +370,7 @@ __global__ __launch_bounds__(64 * NW, NW / 2 / KS) void attend_kernel(AttendArgs
   // ---- a chunk's rows, 16 bytes per unit, a unit's lane offset apart from its
   // neighbour's by a whole number of rows.  Rows behind the segment read as 0.
   u32x4 rq[OUT ? T::QU : 1], rk[T::QU], rv[T::VU];
-  float ra, rb;
+  float ra = 1.f, rb = 0.f;
   constexpr int KR = NT * EU / DK, VR = NT * EU / T::DV;               // rows per pass of the threads
   const uint32_t kstep = (uint32_t)a.k_stride * B, qstep = (uint32_t)a.q_stride * B;
   const uint32_t vstep = (uint32_t)a.v_stride * B, ostep = (uint32_t)a.o_stride * B;
@@ -351,10 +379,12 @@ __global__ __launch_bounds__(64 * NW, NW / 2 / KS) void attend_kernel(AttendArgs
     const int live = len - c * C < C ? len - c * C : C;
     return live > 0 ? (uint32_t)(live - 1) * step + row : 0u;
   };
-  // A round of decays: one token per thread of the last four waves.
+  // A round of decays: one token per thread of the last four waves, read a round
+  // ahead.
   const int dtok = tid - (NT - ROUND);
   auto read_decays = [&](int t) {
-    const int64_t x = (sg.t0 + (t + dtok < len ? (dtok < 0 ? 0 : t + dtok) : len - 1)) * a.heads + h;
+    if (dtok < 0) return;
+    const int64_t x = (sg.t0 + (t + dtok < len ? t + dtok : len - 1)) * a.heads + h;
     ra = a.alpha[x];
     rb = a.beta[x];
   };
@@ -363,7 +393,6 @@ __global__ __launch_bounds__(64 * NW, NW / 2 / KS) void attend_kernel(AttendArgs
     if (dtok >= 0) {
       const bool in = t + dtok < len;
       total += fill_decays<C>(dec[buf], dtok & ~63, in ? ra : 1.f, in ? rb : 0.f, lane);
-      if (t + ROUND < len) read_decays(t + ROUND);
     }
   };
   auto read_chunk = [&](int c) {
@@ -546,8 +575,9 @@ __global__ __launch_bounds__(64 * NW, NW / 2 / KS) void attend_kernel(AttendArgs
     __syncthreads();
     if constexpr (OUT && BEHIND) finish(c - 1, (c & 1) ^ 1);
     if constexpr (OUT) {
-      // ---- P^T tile of a wave: rows s, columns t (the tile above the diagonal is 0)
-      if (NW == 4 || wave < 4) {
+      // ---- P^T tile of a wave: rows s, columns t; the tile above the diagonal is 0
+      // and put once into each buffer
+      if ((NW == 4 || wave < 4) && (wave != 1 || c < 2)) {
         const int ti = wave >> 1, si = wave & 1;
         f32x4 x = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -625,11 +655,16 @@ __global__ __launch_bounds__(64 * NW, NW / 2 / KS) void attend_kernel(AttendArgs
     }
     if constexpr (RB == 1)
       if (c + 1 < chunks) read_chunk(c + 1);
-    if constexpr (RB == 2) {                     // rows of c + 1 to LDS, of c + 2 from memory
+    const bool round = at + C == ROUND;          // the next chunk opens a round of decays
+    if constexpr (RB == 2) {
+      // rows of c + 1 to LDS, of c + 2 from memory; the decays between them, where
+      // no younger load is in flight that their wait would include
       put_chunk(c + 1, buf ^ 1);
+      if (round && c + 1 < chunks) put_decays((c + 1) * C, ((c + 1) / (ROUND / C)) & 1);
+      if (at == 0) read_decays(c * C + ROUND);
       read_chunk(c + 2);
     }
-      if constexpr (RB == 2) __builtin_amdgcn_s_setprio(2);
+    if constexpr (RB == 2) __builtin_amdgcn_s_setprio(2);
     // ---- S = c_C S + k^T (w v)
     bf16x8 vs[CG][3];
 #pragma unroll
@@ -669,15 +704,13 @@ __global__ __launch_bounds__(64 * NW, NW / 2 / KS) void attend_kernel(AttendArgs
             for (int cg = 0; cg < CG; ++cg) S[cg][I] = mfma(kp[i], vs[cg][j], S[cg][I]);
     }
     if constexpr (RB == 2) __builtin_amdgcn_s_setprio(0);
-    const bool round = at + C == ROUND;             // the next chunk opens a round of decays
-    if constexpr (RB == 2) {
-      if (round && c + 1 < chunks) put_decays((c + 1) * C, ((c + 1) / (ROUND / C)) & 1);
-    } else {
+    if constexpr (RB == 1) {
       __syncthreads();
       if constexpr (OUT && !BEHIND) finish(c, 0);
       if (c + 1 < chunks) {
         put_chunk(c + 1, 0);
         if (round) put_decays((c + 1) * C, 0);
+        if (at == 0) read_decays(c * C + ROUND);
       }
     }
   }
