@@ -49,14 +49,13 @@ constexpr int kWhole = 1024;                     // tokens that are not worth tw
 // A lane offset behind every buffer: chunks are below 2^31 bytes.
 constexpr uint32_t kNowhere = 0xFFFFFFF0u;
 
-// Tiling of one instance: NW waves, KS of them to the same CG groups of 16 value
-// columns with a share of dk each; chunks of 32 tokens (one k-step of the MFMA
-// over tokens).
-template <int IO, int DK, int NW, int CG, int KS>
+// Tiling of one instance: NW waves, KS of them to the same 16 value columns with
+// a share of dk each; chunks of 32 tokens (one k-step of the MFMA over tokens).
+template <int IO, int DK, int NW, int KS>
 struct Tile {
   static constexpr int NP = IO == IO_BF16 ? 1 : IO == IO_F16 ? 2 : 3;   // parts of an input
   static constexpr int NO = IO == IO_F32 ? 3 : 2;                       // parts on the output's side
-  static constexpr int C = 32, NT = 64 * NW, DV = 16 * CG * NW / KS, ROUND = 256;
+  static constexpr int C = 32, NT = 64 * NW, DV = 16 * NW / KS, ROUND = 256;
   static constexpr int EU = IO == IO_F32 ? 4 : 8;                       // elements of a 16-byte unit
   // LDS row pitches in elements: rows 8 banks apart (P: 24), which keeps the
   // 16-byte reads of 16 rows (q, P) and the four-row reads by columns (v) free
@@ -123,7 +122,7 @@ __device__ __forceinline__ bf16x4 read_column4(const __bf16* p) {
                                         (__attribute__((address_space(3))) s16x4*)p));
 }
 
-// Decays of N tokens, by token; chunk borders are every C tokens.
+// Decays of N tokens, by token; chunk borders are every 32 tokens.
 template <int N>
 struct Decays {
   float hi[N], lo[N];      // L_t, the sum of log2(alpha) from the chunk's start
@@ -183,9 +182,9 @@ __device__ __forceinline__ double log2_of(float x) {
   return y;
 }
 
-// One wave fills the decays of its 64 tokens (alpha 1 and beta 0 behind the
-// sequence) from at on; returns the lane's log2(alpha).
-template <int C, int N>
+// One wave fills the decays of its 64 tokens, two chunks, from at on (alpha 1 and
+// beta 0 behind the sequence); returns the lane's log2(alpha).
+template <int N>
 __device__ __forceinline__ double fill_decays(Decays<N>& d, int at, float alpha, float beta, int lane) {
   double l = log2_of(alpha);
   const double own = l;
@@ -194,8 +193,7 @@ __device__ __forceinline__ double fill_decays(Decays<N>& d, int at, float alpha,
   l += dpp_or_zero<0x114, 0xF>(l);
   l += dpp_or_zero<0x118, 0xF>(l);
   l += dpp_or_zero<0x142, 0xA>(l);               // row_bcast 15 into rows 1 and 3: within 32
-  if constexpr (C == 64) l += dpp_or_zero<0x143, 0xC>(l);   // row_bcast 31 into rows 2 and 3
-  const double end = C == 64 || lane >= 32 ? lane_of(l, 63) : lane_of(l, 31);
+  const double end = lane >= 32 ? lane_of(l, 63) : lane_of(l, 31);
   const float hi = (float)l;
   d.hi[at + lane] = hi;
   d.lo[at + lane] = (float)(l - (double)hi);
@@ -317,8 +315,8 @@ __device__ __forceinline__ Item item_of(int64_t b, int rows) {
   return {p / own, (int)(b % 8) * own + (int)(p % own)};
 }
 
-// One workgroup walks the chunks of one segment of one head, 16 CG NW value
-// columns of it.  Four waves compute P's four tiles; every wave has its 16 CG
+// One workgroup walks the chunks of one segment of one head, 16 NW / KS
+// value columns of it.  Four waves compute P's tiles; every wave has its 16
 // columns of S in registers in the layout that the MFMA both writes (S^T[dk, dv]
 // accumulated from k^T and the scaled v) and reads (as the operand of S q): the
 // k index of an operand is only a labelling, so the tiles' rows are dealt to
@@ -329,9 +327,9 @@ __device__ __forceinline__ Item item_of(int64_t b, int rows) {
 // to LDS, all between two barriers.  OUT = false adds up a segment's writes alone
 // (no q, no output), for the segments behind it.  VEC: v and o by dwords and
 // more (else by element: 16-bit types of odd widths or addresses).
-template <int IO, int DK, int NW, int CG, int KS, bool VEC, bool OUT>
+template <int IO, int DK, int NW, int KS, bool VEC, bool OUT>
 __global__ __launch_bounds__(64 * NW, NW / 2 / KS) void attend_kernel(AttendArgs args) {
-  using T = Tile<IO, DK, NW, CG, KS>;
+  using T = Tile<IO, DK, NW, KS>;
   constexpr int NP = T::NP, NO = T::NO, C = T::C, PK = T::PK, PV = T::PV, PQ = T::PQ, PP = T::PP;
   constexpr int NT = T::NT, EU = T::EU, RB = T::RB, ROUND = T::ROUND, B = 16 / EU;   // B: bytes of an element
   constexpr bool BEHIND = T::BEHIND;
@@ -342,7 +340,7 @@ __global__ __launch_bounds__(64 * NW, NW / 2 / KS) void attend_kernel(AttendArgs
   __shared__ __align__(16) __bf16 vl[RB][NP][C * PV];
   __shared__ __align__(16) __bf16 ql[OUT ? RB : 1][OUT ? NP : 1][OUT ? C * PQ : 8];
   __shared__ __align__(16) __bf16 pl[OUT && BEHIND ? 2 : 1][OUT ? NO : 1][OUT ? C * PP : 8];
-  __shared__ __align__(16) f32x4 part[OUT && KS > 1 ? NW * CG * 64 : 1];
+  __shared__ __align__(16) f32x4 part[OUT && KS > 1 ? NW * 64 : 1];
   __shared__ __align__(16) Decays<ROUND> dec[RB];
 
   const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, li = lane & 15;
@@ -392,7 +390,7 @@ __global__ __launch_bounds__(64 * NW, NW / 2 / KS) void attend_kernel(AttendArgs
   auto put_decays = [&](int t, int buf) {
     if (dtok >= 0) {
       const bool in = t + dtok < len;
-      total += fill_decays<C>(dec[buf], dtok & ~63, in ? ra : 1.f, in ? rb : 0.f, lane);
+      total += fill_decays(dec[buf], dtok & ~63, in ? ra : 1.f, in ? rb : 0.f, lane);
     }
   };
   auto read_chunk = [&](int c) {
@@ -477,11 +475,11 @@ __global__ __launch_bounds__(64 * NW, NW / 2 / KS) void attend_kernel(AttendArgs
     for (int n = 0; n < T::VU; ++n) put(rv[n], vl[buf], n * VR + vrow, PV, vcol);
   };
 
-  // ---- the state's columns: lane li has columns 16 cg + li of the wave's, and of
+  // ---- the state's columns: lane li has column li of the wave's 16, and of
   // S^T the rows 32 (I / 2) + 8 g + 4 (I % 2) + v (tiles I = 2 m and 2 m + 1
   // together hold eight consecutive rows per lane, an operand's k-slots)
-  const int w0 = 16 * CG * (wave / KS), kh = wave % KS;   // the wave's first column in the slice; its part of dk
-  f32x4 S[CG][KT];
+  const int w0 = 16 * (wave / KS), kh = wave % KS;   // the wave's first column in the slice; its part of dk
+  f32x4 S[KT];
   const int64_t state = ((int64_t)h * a.dv + d0 + w0 + li) * DK + kh * DW + 8 * g, per = (int64_t)a.heads * a.dv * DK;
   float* slot_S = a.S + slot * per + state;
   float* seg_S = args.ws + sg.ws * per + state;
@@ -490,24 +488,19 @@ __global__ __launch_bounds__(64 * NW, NW / 2 / KS) void attend_kernel(AttendArgs
     const bool zero = !OUT || (!from_ws && a.fresh && a.fresh[sg.i]);
     const float* p = from_ws ? seg_S : slot_S;
 #pragma unroll
-    for (int cg = 0; cg < CG; ++cg)
-#pragma unroll
-      for (int I = 0; I < KT; ++I)
-        S[cg][I] = !zero && w0 + 16 * cg + li < vcols ? *reinterpret_cast<const f32x4*>(p + 16 * cg * DK + 32 * (I / 2) + 4 * (I % 2))
-                                                      : f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int I = 0; I < KT; ++I)
+      S[I] = !zero && w0 + li < vcols ? *reinterpret_cast<const f32x4*>(p + 32 * (I / 2) + 4 * (I % 2))
+                                      : f32x4{0.f, 0.f, 0.f, 0.f};
   }
 
-  bf16x4 vr[CG][2][NP];                          // the wave's columns of v, by columns
-  f32x4 acc[CG][OUT ? CT : 1];                   // o^T tiles: rows dv, columns t (KS = 2: only tile 0 from share() on)
+  bf16x4 vr[2][NP];                              // the wave's columns of v, by columns
+  f32x4 acc[OUT ? CT : 1];                       // o^T tiles: rows dv, columns t (KS = 2: only tile 0 once the halves are exchanged)
   // acc += P v of chunk c, and the output
   auto finish = [&](int c, int buf) {
     const auto ob = rows_of(a.o, ((sg.t0 + c * C) * a.o_stride + hv) * B, c < 0 ? 0u : bytes_of(c, ostep, vcols * B));
     const int t0 = KS > 1 ? 16 * kh : 0;         // the wave's first token
     uint32_t oo = (t0 + li) * ostep + (w0 + 4 * g) * B;
-    if constexpr (KS > 1) {
-#pragma unroll
-      for (int cg = 0; cg < CG; ++cg) acc[cg][0] = acc[cg][0] + part[(wave * CG + cg) * 64 + lane];
-    }
+    if constexpr (KS > 1) acc[0] = acc[0] + part[wave * 64 + lane];
 #pragma unroll
     for (int ti = 0; ti < OT; ++ti) {
       bf16x8 pp[NO];
@@ -519,36 +512,31 @@ __global__ __launch_bounds__(64 * NW, NW / 2 / KS) void attend_kernel(AttendArgs
       for (int i = NO - 1; i >= 0; --i)          // small products first
 #pragma unroll
         for (int j = NP - 1; j >= 0; --j)
-          if (i + j < NO)
-#pragma unroll
-            for (int cg = 0; cg < CG; ++cg) acc[cg][ti] = mfma(join(vr[cg][0][j], vr[cg][1][j]), pp[i], acc[cg][ti]);
+          if (i + j < NO) acc[ti] = mfma(join(vr[0][j], vr[1][j]), pp[i], acc[ti]);
     }
 #pragma unroll
     for (int ti = 0; ti < OT; ++ti) {
+      const f32x4 x = acc[ti];
+      const int left = vcols - (w0 + 4 * g);               // columns to write, four per lane
+      if (VEC && vcols % 4 == 0) {
+        const uint32_t e = left > 0 ? oo : kNowhere;
+        if constexpr (IO == IO_F32)
+          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, x), ob, e, 0, 0);
+        else
+          __builtin_amdgcn_raw_buffer_store_b64(u32x2{pair16<IO>(x[0], x[1]), pair16<IO>(x[2], x[3])}, ob, e, 0, 0);
+      } else if (VEC && IO != IO_F32) {
 #pragma unroll
-      for (int cg = 0; cg < CG; ++cg) {
-        const f32x4 x = acc[cg][ti];
-        const int left = vcols - (w0 + 16 * cg + 4 * g);               // columns to write, four per lane
-        if (VEC && vcols % 4 == 0) {
-          const uint32_t e = left > 0 ? oo + 16 * cg * B : kNowhere;
+        for (int v = 0; v < 4; v += 2)
+          __builtin_amdgcn_raw_buffer_store_b32(pair16<IO>(x[v], x[v + 1]), ob,
+                                                v < left ? oo + v * B : kNowhere, 0, 0);
+      } else {
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const uint32_t e = v < left ? oo + v * B : kNowhere;
           if constexpr (IO == IO_F32)
-            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, x), ob, e, 0, 0);
+            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x[v]), ob, e, 0, 0);
           else
-            __builtin_amdgcn_raw_buffer_store_b64(u32x2{pair16<IO>(x[0], x[1]), pair16<IO>(x[2], x[3])}, ob, e, 0, 0);
-        } else if (VEC && IO != IO_F32) {
-#pragma unroll
-          for (int v = 0; v < 4; v += 2)
-            __builtin_amdgcn_raw_buffer_store_b32(pair16<IO>(x[v], x[v + 1]), ob,
-                                                  v < left ? oo + (16 * cg + v) * B : kNowhere, 0, 0);
-        } else {
-#pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            const uint32_t e = v < left ? oo + (16 * cg + v) * B : kNowhere;
-            if constexpr (IO == IO_F32)
-              __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x[v]), ob, e, 0, 0);
-            else
-              __builtin_amdgcn_raw_buffer_store_b16(to16<IO>(x[v]), ob, e, 0, 0);
-          }
+            __builtin_amdgcn_raw_buffer_store_b16(to16<IO>(x[v]), ob, e, 0, 0);
         }
       }
       oo += 16 * ostep;
@@ -561,14 +549,11 @@ __global__ __launch_bounds__(64 * NW, NW / 2 / KS) void attend_kernel(AttendArgs
   put_chunk(0, 0);
   if constexpr (RB == 2) read_chunk(1);
 #pragma unroll
-  for (int cg = 0; cg < CG; ++cg) {
+  for (int ti = 0; ti < (OUT ? CT : 1); ++ti) acc[ti] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int ti = 0; ti < (OUT ? CT : 1); ++ti) acc[cg][ti] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int y = 0; y < 2; ++y)
 #pragma unroll
-    for (int y = 0; y < 2; ++y)
-#pragma unroll
-      for (int i = 0; i < NP; ++i) vr[cg][y][i] = bf16x4{};
-  }
+    for (int i = 0; i < NP; ++i) vr[y][i] = bf16x4{};
   for (int c = 0; c < chunks; ++c) {
     const int buf = RB == 2 ? c & 1 : 0, at = c * C % ROUND;
     const Decays<ROUND>& d = dec[RB == 2 ? c / (ROUND / C) & 1 : 0];
@@ -612,15 +597,12 @@ __global__ __launch_bounds__(64 * NW, NW / 2 / KS) void attend_kernel(AttendArgs
       // ---- c_t S q
 #pragma unroll
       for (int ks = 0; ks < DW / 32; ++ks) {
-        bf16x8 sp[CG][NO];
+        bf16x8 sp[NO];
+        bf16x4 s0[NO], s1[NO];
+        split4<NO>(S[2 * ks], s0);
+        split4<NO>(S[2 * ks + 1], s1);
 #pragma unroll
-        for (int cg = 0; cg < CG; ++cg) {
-          bf16x4 s0[NO], s1[NO];
-          split4<NO>(S[cg][2 * ks], s0);
-          split4<NO>(S[cg][2 * ks + 1], s1);
-#pragma unroll
-          for (int i = 0; i < NO; ++i) sp[cg][i] = join(s0[i], s1[i]);
-        }
+        for (int i = 0; i < NO; ++i) sp[i] = join(s0[i], s1[i]);
 #pragma unroll
         for (int ti = 0; ti < CT; ++ti) {
           bf16x8 qp[NP];
@@ -633,24 +615,17 @@ __global__ __launch_bounds__(64 * NW, NW / 2 / KS) void attend_kernel(AttendArgs
 #pragma unroll
             for (int j = NP - 1; j >= 0; --j)
               if (i + j < NO)
-#pragma unroll
-                for (int cg = 0; cg < CG; ++cg)
-                  acc[cg][ti] = mfma(sp[cg][i], qp[j], ks == 0 && i == NO - 1 && j == 0 ? f32x4{0.f, 0.f, 0.f, 0.f}
-                                                                                       : acc[cg][ti]);
+                acc[ti] = mfma(sp[i], qp[j], ks == 0 && i == NO - 1 && j == 0 ? f32x4{0.f, 0.f, 0.f, 0.f} : acc[ti]);
         }
       }
 #pragma unroll
       for (int ti = 0; ti < CT; ++ti) {
         const float ct = __builtin_amdgcn_exp2f(d.hi[at + 16 * ti + li]) * (1.f + 0.69314718f * d.lo[at + 16 * ti + li]);
-#pragma unroll
-        for (int cg = 0; cg < CG; ++cg) acc[cg][ti] = acc[cg][ti] * ct;
+        acc[ti] = acc[ti] * ct;
       }
       if constexpr (KS > 1) {                    // the other wave's tile to it, the own one to place 0
-#pragma unroll
-        for (int cg = 0; cg < CG; ++cg) {
-          part[((wave ^ 1) * CG + cg) * 64 + lane] = kh ? acc[cg][0] : acc[cg][1];
-          acc[cg][0] = kh ? acc[cg][1] : acc[cg][0];
-        }
+        part[(wave ^ 1) * 64 + lane] = kh ? acc[0] : acc[1];
+        acc[0] = kh ? acc[1] : acc[0];
       }
     }
     if constexpr (RB == 1)
@@ -666,24 +641,21 @@ __global__ __launch_bounds__(64 * NW, NW / 2 / KS) void attend_kernel(AttendArgs
     }
     if constexpr (RB == 2) __builtin_amdgcn_s_setprio(2);
     // ---- S = c_C S + k^T (w v)
-    bf16x8 vs[CG][3];
+    bf16x8 vs[3];
+    bf16x4 half[2][3];
 #pragma unroll
-    for (int cg = 0; cg < CG; ++cg) {
-      bf16x4 half[2][3];
+    for (int y = 0; y < 2; ++y) {
 #pragma unroll
-      for (int y = 0; y < 2; ++y) {
+      for (int i = 0; i < NP; ++i)
+        vr[y][i] = read_column4(&vl[buf][i][(16 * y + 4 * g + li / 4) * PV + w0 + 4 * (li % 4)]);
+      f32x4 x = widen_bf16x4(vr[y][0]);
 #pragma unroll
-        for (int i = 0; i < NP; ++i)
-          vr[cg][y][i] = read_column4(&vl[buf][i][(16 * y + 4 * g + li / 4) * PV + w0 + 16 * cg + 4 * (li % 4)]);
-        f32x4 x = widen_bf16x4(vr[cg][y][0]);
-#pragma unroll
-        for (int i = 1; i < NP; ++i) x = x + widen_bf16x4(vr[cg][y][i]);
-        x = x * *reinterpret_cast<const f32x4*>(&d.w[at + 16 * y + 4 * g]);
-        split4<3>(x, half[y]);
-      }
-#pragma unroll
-      for (int i = 0; i < 3; ++i) vs[cg][i] = join(half[0][i], half[1][i]);
+      for (int i = 1; i < NP; ++i) x = x + widen_bf16x4(vr[y][i]);
+      x = x * *reinterpret_cast<const f32x4*>(&d.w[at + 16 * y + 4 * g]);
+      split4<3>(x, half[y]);
     }
+#pragma unroll
+    for (int i = 0; i < 3; ++i) vs[i] = join(half[0][i], half[1][i]);
     const float gamma = __builtin_amdgcn_exp2f(d.hi[at + C - 1]) * (1.f + 0.69314718f * d.lo[at + C - 1]);   // c_C
 #pragma unroll
     for (int I = 0; I < KT; ++I) {
@@ -693,15 +665,12 @@ __global__ __launch_bounds__(64 * NW, NW / 2 / KS) void attend_kernel(AttendArgs
         const __bf16* p = &kl[buf][i][(4 * g + li / 4) * PK + kh * DW + 32 * (I / 2) + 8 * (li % 4) + 4 * (I % 2)];
         kp[i] = join(read_column4(p), read_column4(p + 16 * PK));
       }
-#pragma unroll
-      for (int cg = 0; cg < CG; ++cg) S[cg][I] = S[cg][I] * gamma;
+      S[I] = S[I] * gamma;
 #pragma unroll
       for (int i = NP - 1; i >= 0; --i)
 #pragma unroll
         for (int j = 2; j >= 0; --j)
-          if (i + j < 3)
-#pragma unroll
-            for (int cg = 0; cg < CG; ++cg) S[cg][I] = mfma(kp[i], vs[cg][j], S[cg][I]);
+          if (i + j < 3) S[I] = mfma(kp[i], vs[j], S[I]);
     }
     if constexpr (RB == 2) __builtin_amdgcn_s_setprio(0);
     if constexpr (RB == 1) {
@@ -721,12 +690,10 @@ __global__ __launch_bounds__(64 * NW, NW / 2 / KS) void attend_kernel(AttendArgs
 
   if (!OUT || sg.j == sg.n - 1) {
     float* p = OUT ? slot_S : seg_S;
+    if (w0 + li < vcols) {
 #pragma unroll
-    for (int cg = 0; cg < CG; ++cg)
-      if (w0 + 16 * cg + li < vcols) {
-#pragma unroll
-        for (int I = 0; I < KT; ++I) *reinterpret_cast<f32x4*>(p + 16 * cg * DK + 32 * (I / 2) + 4 * (I % 2)) = S[cg][I];
-      }
+      for (int I = 0; I < KT; ++I) *reinterpret_cast<f32x4*>(p + 32 * (I / 2) + 4 * (I % 2)) = S[I];
+    }
   }
   if constexpr (!OUT) {                          // the segment's own decay
     __shared__ double sum[NW];
@@ -796,31 +763,31 @@ namespace {
 // half a CU at 64.
 int slice_width(int io, int dv) { return io == IO_F32 || dv <= 64 ? 64 : 128; }
 
-template <int IO, int DK, int NW, int CG, int KS, bool VEC>
+template <int IO, int DK, int NW, int KS, bool VEC>
 hipError_t launch_instance(const AttendArgs& args, unsigned blocks, hipStream_t s) {
   const SlotArgs& a = args.s;
   if (args.seg_len) {
     const unsigned cut = (unsigned)(args.cut * args.slices * a.heads);
-    hipLaunchKernelGGL((dev::attend_kernel<IO, DK, NW, CG, KS, VEC, false>), dim3(cut), dim3(64 * NW), 0, s, args);
+    hipLaunchKernelGGL((dev::attend_kernel<IO, DK, NW, KS, VEC, false>), dim3(cut), dim3(64 * NW), 0, s, args);
     const int64_t quads = (int64_t)a.heads * a.dv * DK / 4, most = 4096 / a.seqs + 1;
     const int64_t per = (quads + 255) / 256 < most ? (quads + 255) / 256 : most;
     hipLaunchKernelGGL(dev::combine_kernel, dim3((unsigned)(per * a.seqs)), dim3(256), 0, s, args,
                        (int)per, quads);
   }
-  hipLaunchKernelGGL((dev::attend_kernel<IO, DK, NW, CG, KS, VEC, true>), dim3(blocks), dim3(64 * NW), 0, s, args);
+  hipLaunchKernelGGL((dev::attend_kernel<IO, DK, NW, KS, VEC, true>), dim3(blocks), dim3(64 * NW), 0, s, args);
   return hipGetLastError();
 }
 
 template <int IO, int DK>
 hipError_t launch_width(const AttendArgs& args, unsigned blocks, hipStream_t s) {
   if constexpr (IO == IO_F32) {
-    return launch_instance<IO, DK, 8, 1, 2, true>(args, blocks, s);
+    return launch_instance<IO, DK, 8, 2, true>(args, blocks, s);
   } else {
     if (slice_width(IO, args.s.dv) == 128)
-      return args.wide ? launch_instance<IO, DK, 8, 1, 1, true>(args, blocks, s)
-                       : launch_instance<IO, DK, 8, 1, 1, false>(args, blocks, s);
-    return args.wide ? launch_instance<IO, DK, 4, 1, 1, true>(args, blocks, s)
-                     : launch_instance<IO, DK, 4, 1, 1, false>(args, blocks, s);
+      return args.wide ? launch_instance<IO, DK, 8, 1, true>(args, blocks, s)
+                       : launch_instance<IO, DK, 8, 1, false>(args, blocks, s);
+    return args.wide ? launch_instance<IO, DK, 4, 1, true>(args, blocks, s)
+                     : launch_instance<IO, DK, 4, 1, false>(args, blocks, s);
   }
 }
 
