@@ -20,6 +20,7 @@
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
+#include <type_traits>
 
 #include "lsq_slots.h"
 #include "lsq_slots_dev.h"
@@ -332,8 +333,8 @@ __global__ __launch_bounds__(64 * NW, NW / 2 / KS) void attend_kernel(AttendArgs
   using T = Tile<IO, DK, NW, KS>;
   constexpr int NP = T::NP, NO = T::NO, C = T::C, PK = T::PK, PV = T::PV, PQ = T::PQ, PP = T::PP;
   constexpr int NT = T::NT, EU = T::EU, RB = T::RB, ROUND = T::ROUND, B = 16 / EU;   // B: bytes of an element
-  constexpr bool BEHIND = T::BEHIND;
-  constexpr int CT = C / 16, DW = DK / KS, KT = DW / 16;   // a wave's part of dk
+  constexpr bool BEHIND = T::BEHIND;  constexpr int CT = C / 16, DW = DK / KS, KT = DW / 16;   // a wave's part of dk
+  constexpr int PER = NP == 1 ? 2 : 1;           // tiles of S that a step of the state's products takes
   constexpr int OT = CT / KS;                    // tiles of 16 tokens whose output a wave finishes
   const SlotArgs& a = args.s;
   __shared__ __align__(16) __bf16 kl[RB][NP][C * PK];
@@ -495,11 +496,43 @@ __global__ __launch_bounds__(64 * NW, NW / 2 / KS) void attend_kernel(AttendArgs
 
   bf16x4 vr[2][NP];                              // the wave's columns of v, by columns
   f32x4 acc[OUT ? CT : 1];                       // o^T tiles: rows dv, columns t (KS = 2: only tile 0 once the halves are exchanged)
-  // acc += P v of chunk c, and the output
-  auto finish = [&](int c, int buf) {
-    const auto ob = rows_of(a.o, ((sg.t0 + c * C) * a.o_stride + hv) * B, c < 0 ? 0u : bytes_of(c, ostep, vcols * B));
-    const int t0 = KS > 1 ? 16 * kh : 0;         // the wave's first token
-    uint32_t oo = (t0 + li) * ostep + (w0 + 4 * g) * B;
+  // A v that is not finite may reach its own column from its token on, but P's
+  // zeros times it would be NaN for the chunk's earlier tokens too.  It has made
+  // its column of the new S NaN, so one register of S tells (a look at all of v
+  // would be ten instructions per chunk): such a v becomes 0 in P v, and the
+  // column's outputs NaN from it on.  While S is finite the branch costs 1%
+  // (16 x 2560 tokens of 32 heads 128x128 in bf16: 326 us without, 330 with).
+  auto keep_causal = [&]() __attribute__((always_inline)) {
+    int first = C;                               // of column li
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if ((__builtin_bit_cast(uint64_t, vr[y][0]) >> (16 * e) & 0x7F80) == 0x7F80) {
+          const int t = 16 * y + 4 * g + e;
+          first = t < first ? t : first;
+#pragma unroll
+          for (int i = 0; i < NP; ++i) vr[y][i][e] = (__bf16)0.f;
+        }
+    }
+    for (int o = 16; o < 64; o *= 2) {
+      const int other = __shfl_xor(first, o);
+      first = other < first ? other : first;
+    }
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      const int from = __shfl(first, 4 * g + v);
+#pragma unroll
+      for (int ti = 0; ti < OT; ++ti)
+        if ((KS > 1 ? 16 * kh : 16 * ti) + li >= from) acc[ti][v] = __uint_as_float(0x7FC00000u);
+    }
+  };
+  // acc += P v of a chunk, rounded
+  using Out = typename std::conditional<IO == IO_F32, f32x4, u32x2>::type;   // four columns of a token
+  Out out[OUT ? OT : 1];
+  const int t0 = KS > 1 ? 16 * kh : 0;           // the wave's first token
+  auto finish = [&](int buf) __attribute__((always_inline)) {
+    if (__builtin_expect(__any(S[0][0] != S[0][0]), 0)) keep_causal();
     if constexpr (KS > 1) acc[0] = acc[0] + part[wave * 64 + lane];
 #pragma unroll
     for (int ti = 0; ti < OT; ++ti) {
@@ -517,26 +550,38 @@ __global__ __launch_bounds__(64 * NW, NW / 2 / KS) void attend_kernel(AttendArgs
 #pragma unroll
     for (int ti = 0; ti < OT; ++ti) {
       const f32x4 x = acc[ti];
-      const int left = vcols - (w0 + 4 * g);               // columns to write, four per lane
+      if constexpr (IO == IO_F32) out[ti] = x;
+      else out[ti] = u32x2{pair16<IO>(x[0], x[1]), pair16<IO>(x[2], x[3])};
+    }
+  };
+  // Chunk c's outputs to memory.  A wait for loads counts the stores issued
+  // behind them too, so the one-copy instances store where no load is in flight
+  // that is waited for soon (4 prompts of 650-2500 tokens, 64 heads 128x64 in
+  // fp32: 211 us; 223 with the stores before the put of the next rows).  With
+  // two copies it makes no difference.
+  auto store_out = [&](int c) __attribute__((always_inline)) {
+    const auto ob = rows_of(a.o, ((sg.t0 + c * C) * a.o_stride + hv) * B, c < 0 ? 0u : bytes_of(c, ostep, vcols * B));
+    uint32_t oo = (t0 + li) * ostep + (w0 + 4 * g) * B;
+    const int left = vcols - (w0 + 4 * g);       // columns to write, four per lane
+#pragma unroll
+    for (int ti = 0; ti < OT; ++ti) {
+      const Out x = out[ti];
       if (VEC && vcols % 4 == 0) {
         const uint32_t e = left > 0 ? oo : kNowhere;
         if constexpr (IO == IO_F32)
           __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, x), ob, e, 0, 0);
         else
-          __builtin_amdgcn_raw_buffer_store_b64(u32x2{pair16<IO>(x[0], x[1]), pair16<IO>(x[2], x[3])}, ob, e, 0, 0);
-      } else if (VEC && IO != IO_F32) {
-#pragma unroll
-        for (int v = 0; v < 4; v += 2)
-          __builtin_amdgcn_raw_buffer_store_b32(pair16<IO>(x[v], x[v + 1]), ob,
-                                                v < left ? oo + v * B : kNowhere, 0, 0);
+          __builtin_amdgcn_raw_buffer_store_b64(x, ob, e, 0, 0);
       } else {
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
           const uint32_t e = v < left ? oo + v * B : kNowhere;
           if constexpr (IO == IO_F32)
             __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x[v]), ob, e, 0, 0);
-          else
-            __builtin_amdgcn_raw_buffer_store_b16(to16<IO>(x[v]), ob, e, 0, 0);
+          else if constexpr (!VEC)
+            __builtin_amdgcn_raw_buffer_store_b16((uint16_t)(x[v / 2] >> (16 * (v & 1))), ob, e, 0, 0);
+          else if (v % 2 == 0)
+            __builtin_amdgcn_raw_buffer_store_b32(x[v / 2], ob, e, 0, 0);
         }
       }
       oo += 16 * ostep;
@@ -558,7 +603,10 @@ __global__ __launch_bounds__(64 * NW, NW / 2 / KS) void attend_kernel(AttendArgs
     const int buf = RB == 2 ? c & 1 : 0, at = c * C % ROUND;
     const Decays<ROUND>& d = dec[RB == 2 ? c / (ROUND / C) & 1 : 0];
     __syncthreads();
-    if constexpr (OUT && BEHIND) finish(c - 1, (c & 1) ^ 1);
+    if constexpr (OUT && BEHIND) {
+      finish((c & 1) ^ 1);
+      if constexpr (RB == 2) store_out(c - 1);
+    }
     if constexpr (OUT) {
       // ---- P^T tile of a wave: rows s, columns t; the tile above the diagonal is 0
       // and put once into each buffer
@@ -628,8 +676,10 @@ __global__ __launch_bounds__(64 * NW, NW / 2 / KS) void attend_kernel(AttendArgs
         acc[0] = kh ? acc[1] : acc[0];
       }
     }
-    if constexpr (RB == 1)
+    if constexpr (RB == 1) {
+      if constexpr (OUT && BEHIND) store_out(c - 1);
       if (c + 1 < chunks) read_chunk(c + 1);
+    }
     const bool round = at + C == ROUND;          // the next chunk opens a round of decays
     if constexpr (RB == 2) {
       // rows of c + 1 to LDS, of c + 2 from memory; the decays between them, where
@@ -640,7 +690,10 @@ __global__ __launch_bounds__(64 * NW, NW / 2 / KS) void attend_kernel(AttendArgs
       read_chunk(c + 2);
     }
     if constexpr (RB == 2) __builtin_amdgcn_s_setprio(2);
-    // ---- S = c_C S + k^T (w v)
+    // ---- S = c_C S + k^T (w v); one part: PER tiles at a time, the next ones'
+    // operands read before their products (1000 tokens of 4 heads 128x128 in
+    // bf16: 65 us; 69 one by one).  More parts have products enough to wait
+    // behind, and no registers to spare (binary16: 90 us one by one, 119 so).
     bf16x8 vs[3];
     bf16x4 half[2][3];
 #pragma unroll
@@ -657,35 +710,52 @@ __global__ __launch_bounds__(64 * NW, NW / 2 / KS) void attend_kernel(AttendArgs
 #pragma unroll
     for (int i = 0; i < 3; ++i) vs[i] = join(half[0][i], half[1][i]);
     const float gamma = __builtin_amdgcn_exp2f(d.hi[at + C - 1]) * (1.f + 0.69314718f * d.lo[at + C - 1]);   // c_C
+    bf16x8 kp[2][PER][NP];
+    auto read_k = [&](int m) __attribute__((always_inline)) {
 #pragma unroll
-    for (int I = 0; I < KT; ++I) {
-      bf16x8 kp[NP];
+      for (int y = 0; y < PER; ++y)
 #pragma unroll
-      for (int i = 0; i < NP; ++i) {
-        const __bf16* p = &kl[buf][i][(4 * g + li / 4) * PK + kh * DW + 32 * (I / 2) + 8 * (li % 4) + 4 * (I % 2)];
-        kp[i] = join(read_column4(p), read_column4(p + 16 * PK));
+        for (int i = 0; i < NP; ++i) {
+          const int I = PER * m + y;
+          const __bf16* p = &kl[buf][i][(4 * g + li / 4) * PK + kh * DW + 32 * (I / 2) + 8 * (li % 4) + 4 * (I % 2)];
+          kp[m & 1][y][i] = join(read_column4(p), read_column4(p + 16 * PK));
+        }
+    };
+    if constexpr (PER > 1) read_k(0);
+#pragma unroll
+    for (int m = 0; m < KT / PER; ++m) {
+      if constexpr (PER == 1) {
+        read_k(m);
+      } else if (m + 1 < KT / PER) {
+        read_k(m + 1);
+        __builtin_amdgcn_sched_barrier(0);
       }
-      S[I] = S[I] * gamma;
+#pragma unroll
+      for (int y = 0; y < PER; ++y) S[PER * m + y] = S[PER * m + y] * gamma;
 #pragma unroll
       for (int i = NP - 1; i >= 0; --i)
 #pragma unroll
         for (int j = 2; j >= 0; --j)
-          if (i + j < 3) S[I] = mfma(kp[i], vs[j], S[I]);
+          if (i + j < 3)
+#pragma unroll
+            for (int y = 0; y < PER; ++y) S[PER * m + y] = mfma(kp[m & 1][y][i], vs[j], S[PER * m + y]);
     }
     if constexpr (RB == 2) __builtin_amdgcn_s_setprio(0);
     if constexpr (RB == 1) {
       __syncthreads();
-      if constexpr (OUT && !BEHIND) finish(c, 0);
+      if constexpr (OUT && !BEHIND) finish(0);
       if (c + 1 < chunks) {
         put_chunk(c + 1, 0);
         if (round) put_decays((c + 1) * C, 0);
         if (at == 0) read_decays(c * C + ROUND);
       }
+      if constexpr (OUT && !BEHIND) store_out(c);
     }
   }
   if constexpr (OUT && BEHIND) {
     __syncthreads();
-    finish(chunks - 1, (chunks - 1) & 1);
+    finish((chunks - 1) & 1);
+    store_out(chunks - 1);
   }
 
   if (!OUT || sg.j == sg.n - 1) {

@@ -564,3 +564,40 @@ def test_two_streams_and_two_graphs_with_cut_sequences():
         for i in range(2):
             assert torch.equal(outs[i], want[i][0])
             assert torch.equal(st.f32.view(4, -1)[slots[i].long()], want[i][1])
+
+
+@pytest.mark.parametrize("io", TYPES)
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")], ids=str)
+@pytest.mark.parametrize("n,at", [(40, 5), (70, 31), (70, 32), (100, 95), (1500, 700)])
+def test_a_value_that_is_not_finite_reaches_no_earlier_token(io, bad, n, at):
+    # one element of v or k of one token: the outputs before it, and of v the other columns, keep
+    # their bits; from it on the column (of k, the heads that share it) is not finite.  1500 tokens
+    # of one head are cut into segments.
+    heads = 2 if n < 1000 else 1
+    st, _ = state(1, heads, 64, 80)
+    start = st.f32.clone()
+    q, k, v, alpha, beta = (x.to(DEV) for x in tokens(n, heads, 1, 64, 80, TYPES[io], 40))
+    cu = torch.tensor([0, n], dtype=torch.int32, device=DEV)
+
+    def run(k, v):
+        st.f32.copy_(start)
+        return st.attend(q, k, v, alpha, beta, cu), st.f32.clone().view(heads, 80, 64)
+
+    o, S = run(k, v)
+    assert bool(o.isfinite().all())
+    for col in (0, 21, 79):
+        vb = v.clone()
+        vb[at, heads - 1, col] = bad
+        ob, Sb = run(k, vb)
+        assert torch.equal(ob[:at], o[:at])
+        assert not bool(ob[at:, heads - 1, col].isfinite().any())
+        assert not bool(Sb[heads - 1, col].isfinite().any())
+        ob[at:, heads - 1, col] = o[at:, heads - 1, col]
+        Sb[heads - 1, col] = S[heads - 1, col]
+        assert torch.equal(ob, o) and torch.equal(Sb, S)
+    kb = k.clone()
+    kb[at, 0, 17] = bad
+    ob, Sb = run(kb, v)
+    assert torch.equal(ob[:at], o[:at])
+    assert not bool(ob[at:].isfinite().any())
+    assert torch.equal(Sb[..., :17], S[..., :17]) and torch.equal(Sb[..., 18:], S[..., 18:])
