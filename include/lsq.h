@@ -400,7 +400,7 @@ lsq_status lsq_attend_workspace(const lsq_state* st, const lsq_token_batch* batc
  * seqs < 0, tokens < 0, qk_heads not dividing heads, an o_stride below
  * heads * dv or a negative stride, a workspace of NULL where one is needed;
  * BUFFER_TOO_SMALL: a smaller workspace; UNSUPPORTED: a quantised handle, a
- * token stride of 32 MiB or more, or more than 2^31 - 1 workgroups. */
+ * token stride of 32 MiB or more, or a launch of 2^32 threads or more. */
 lsq_status lsq_attend(lsq_state* st, const lsq_token_batch* batch, void* workspace,
                       size_t workspace_bytes, void* stream);
 

@@ -896,7 +896,7 @@ AttendPlan attend_plan(int64_t tokens, int32_t seqs, int32_t heads, int32_t dk, 
 
 hipError_t launch_attend(const AttendArgs& args, int io, int dk, hipStream_t s) {
   const int64_t blocks = args.segments * args.s.heads * args.slices;
-  if (blocks > INT32_MAX) return hipErrorInvalidConfiguration;
+  if (!fits_launch(blocks, 512)) return hipErrorInvalidConfiguration;
   const unsigned n = (unsigned)blocks;
   if (io == IO_F32) return dk == 128 ? launch_width<IO_F32, 128>(args, n, s) : launch_width<IO_F32, 64>(args, n, s);
   if (io == IO_F16) return dk == 128 ? launch_width<IO_F16, 128>(args, n, s) : launch_width<IO_F16, 64>(args, n, s);

@@ -10,6 +10,9 @@ namespace lsq {
 
 enum { IO_F32 = 0, IO_F16 = 1, IO_BF16 = 2 };
 
+// Whether a launch of so many workgroups is within a launch's 2^32 - 1 threads.
+inline bool fits_launch(int64_t blocks, int threads) { return blocks <= (int64_t)UINT32_MAX / threads; }
+
 // A packed token batch over the slots of one fp32 handle (include/lsq.h,
 // lsq_token_batch).
 struct SlotArgs {

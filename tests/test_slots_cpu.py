@@ -182,3 +182,20 @@ def test_python_checks():
     with pytest.raises(TypeError):
         st.store_slots(None)
     st.handle = None
+
+
+def test_launches_of_too_many_threads_are_refused():
+    """One launch holds fewer than 2^32 threads; nothing is launched."""
+    L = _lib.load()
+    h, q = handle(), handle(bits=4, group=32, policy=lsq.POLICY_DYNAMIC)
+    n = 1 << 23                                             # entries: 2^25 blocks and more
+    b = ctypes.byref(batch(seqs=n, tokens=n))
+    assert L.lsq_step_slots(h, b, None) == 2
+    assert L.lsq_attend(h, ctypes.byref(batch(seqs=n, tokens=100)), None, 0, None) == 2
+    assert L.lsq_state_store_slots(q, h, n, FAKE, FAKE, None) == 2
+    assert L.lsq_state_load_slots(h, q, n, FAKE, FAKE, None) == 2
+    lsq.lsq_state_free(q)
+    q = handle(bits=4, group=0, policy=lsq.POLICY_DYNAMIC)  # a block per head
+    assert L.lsq_state_store_slots(q, h, n, FAKE, FAKE, None) == 2
+    lsq.lsq_state_free(q)
+    lsq.lsq_state_free(h)
