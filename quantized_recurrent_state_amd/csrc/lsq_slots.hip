@@ -35,12 +35,12 @@ __device__ __forceinline__ void store_state(float* p, f32x4 x) {
 // cover a row (lane lc owns columns 4 lc .. 4 lc + 3 of each 64), so that a
 // wave's state loads are whole 256-byte runs and both dot products end in a
 // 16-lane DPP butterfly; a wave owns 4 R rows, all loaded before the first
-// token, and reads the next token's vectors during the current one's sums.
+// token, and reads the vectors of D tokens ahead during the current one's sums.
 // With one token it is the recurrent form: bound by the state's bytes, read and
 // written once (512 slots of 32 heads 128x128 in fp32 with a diagonal decay: 364
-// us, 6.0 TB/s; 64 slots in bf16 with the delta rule, a quarter of them fresh: 40 us,
-// 5.4 TB/s).  R = 1, 2 and 8 were slower.
-template <int IO, int DK, int DELTA, int DIAG, int R, bool NT>
+// us, 6.0 TB/s; 64 slots in bf16 with the delta rule, some of them fresh: 40 us,
+// 5.4 TB/s).  R = 1, 2 and 8 were slower for single tokens.
+template <int IO, int DK, int DELTA, int DIAG, int R, int D, bool NT>
 __global__ __launch_bounds__(256) void walk_kernel(SlotArgs a, int row_blocks) {
   constexpr int NJ = DK / 64, EPT = DK / 16;
   const int lane = threadIdx.x & 63, lr = lane >> 4, lc = lane & 15;
@@ -100,10 +100,15 @@ __global__ __launch_bounds__(256) void walk_kernel(SlotArgs a, int row_blocks) {
     }
     return x;
   };
-  Token next = read(sp.t0);
-  for (int64_t t = sp.t0; t < sp.t1; ++t) {
-    const Token x = next;
-    if (t + 1 < sp.t1) next = read(t + 1);
+  Token ring[D];
+#pragma unroll
+  for (int d = 0; d < D; ++d) ring[d] = read(D == 1 || sp.t0 + d < sp.t1 ? sp.t0 + d : sp.t1 - 1);
+  auto step = [&](int64_t t, Token& slot) __attribute__((always_inline)) {
+    const Token x = slot;
+    // no branch around the loads where several tokens are under way: with one the
+    // compiler cannot count them and waits for all
+    if (D > 1) slot = read(t + D < sp.t1 ? t + D : sp.t1 - 1);
+    else if (t + 1 < sp.t1) slot = read(t + 1);
     float kk[EPT], qq[EPT], aa[DIAG ? EPT : 1], vv[R];
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
@@ -136,6 +141,11 @@ __global__ __launch_bounds__(256) void walk_kernel(SlotArgs a, int row_blocks) {
       if (lc == r) out = o;
     }
     if (owrite) store1<IO>(a.o, t * a.o_stride + (int64_t)h * a.dv + orow, out);
+  };
+  for (int64_t t = sp.t0; t < sp.t1; t += D) {
+#pragma unroll
+    for (int d = 0; d < D; ++d)
+      if (t + d < sp.t1) step(t + d, ring[d]);
   }
 #pragma unroll
   for (int r = 0; r < R; ++r) {
@@ -283,26 +293,42 @@ __global__ __launch_bounds__(256) void load_slots_kernel(CopyArgs a, int64_t uni
 
 }  // namespace dev
 
+namespace {
+
+template <int IO, int DK, int DELTA, int DIAG>
+hipError_t launch_walk_instance(const SlotArgs& a, int nt, hipStream_t s) {
+  auto launch = [&](auto kernel, int R) {
+    const int row_blocks = (a.dv + 16 * R - 1) / (16 * R);
+    const int64_t blocks = (int64_t)a.seqs * a.heads * row_blocks;
+    if (!fits_launch(blocks, 256)) return hipErrorInvalidConfiguration;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(256), 0, s, a, row_blocks);
+    return hipGetLastError();
+  };
+  if (!a.cu)
+    return nt ? launch(dev::walk_kernel<IO, DK, DELTA, DIAG, 4, 1, true>, 4)
+              : launch(dev::walk_kernel<IO, DK, DELTA, DIAG, 4, 1, false>, 4);
+  // Prompts: a token's chain of sums is what takes the time, so rows are spread
+  // over waves while the workgroups do not share CUs (one prompt of 32 heads
+  // 128x128 in bf16 with the delta rule: 0.43 us per token with R = 2, 0.56 with
+  // 4; 16 prompts: 1.53 and 1.44), and two tokens are read ahead (0.56 and, with
+  // one, 0.60; of a diagonal decay 0.52 and 0.60).
+  const bool few = (int64_t)a.seqs * a.heads * ((a.dv + 31) / 32) <= 256;
+  return few ? launch(dev::walk_kernel<IO, DK, DELTA, DIAG, 2, 2, false>, 2)
+             : launch(dev::walk_kernel<IO, DK, DELTA, DIAG, 4, 2, false>, 4);
+}
+
+template <int IO, int DK>
+hipError_t launch_walk_rule(const SlotArgs& a, int delta, int diag, int nt, hipStream_t s) {
+  if (delta) return diag ? launch_walk_instance<IO, DK, 1, 1>(a, nt, s) : launch_walk_instance<IO, DK, 1, 0>(a, nt, s);
+  return diag ? launch_walk_instance<IO, DK, 0, 1>(a, nt, s) : launch_walk_instance<IO, DK, 0, 0>(a, nt, s);
+}
+
+}  // namespace
+
 hipError_t launch_walk(const SlotArgs& a, int io, int dk, int delta, int diag, int nt, hipStream_t s) {
-  constexpr int R = 4;
-  const int row_blocks = (a.dv + 16 * R - 1) / (16 * R);
-  const int64_t blocks = (int64_t)a.seqs * a.heads * row_blocks;
-  if (!fits_launch(blocks, 256)) return hipErrorInvalidConfiguration;
-#define LSQ_WALK(IO, DK, D, G, N)                                                                 \
-  if (io == IO && dk == DK && delta == D && diag == G && nt == N) {                               \
-    hipLaunchKernelGGL((dev::walk_kernel<IO, DK, D, G, R, N>), dim3((unsigned)blocks), dim3(256), \
-                       0, s, a, row_blocks);                                                      \
-    return hipGetLastError();                                                                     \
-  }
-#define LSQ_WALK_IO(IO, N)                                                                  \
-  LSQ_WALK(IO, 128, 0, 0, N) LSQ_WALK(IO, 128, 0, 1, N) LSQ_WALK(IO, 128, 1, 0, N)          \
-  LSQ_WALK(IO, 128, 1, 1, N) LSQ_WALK(IO, 64, 0, 0, N) LSQ_WALK(IO, 64, 0, 1, N)            \
-  LSQ_WALK(IO, 64, 1, 0, N) LSQ_WALK(IO, 64, 1, 1, N)
-  LSQ_WALK_IO(IO_F32, 0) LSQ_WALK_IO(IO_F16, 0) LSQ_WALK_IO(IO_BF16, 0)
-  LSQ_WALK_IO(IO_F32, 1) LSQ_WALK_IO(IO_F16, 1) LSQ_WALK_IO(IO_BF16, 1)
-#undef LSQ_WALK_IO
-#undef LSQ_WALK
-  return hipErrorInvalidValue;
+  if (io == IO_F32) return dk == 128 ? launch_walk_rule<IO_F32, 128>(a, delta, diag, nt, s) : launch_walk_rule<IO_F32, 64>(a, delta, diag, nt, s);
+  if (io == IO_F16) return dk == 128 ? launch_walk_rule<IO_F16, 128>(a, delta, diag, nt, s) : launch_walk_rule<IO_F16, 64>(a, delta, diag, nt, s);
+  return dk == 128 ? launch_walk_rule<IO_BF16, 128>(a, delta, diag, nt, s) : launch_walk_rule<IO_BF16, 64>(a, delta, diag, nt, s);
 }
 
 hipError_t launch_store_slots(const CopyArgs& a, int bits, int dk, hipStream_t s) {

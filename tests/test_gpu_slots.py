@@ -601,3 +601,22 @@ def test_a_value_that_is_not_finite_reaches_no_earlier_token(io, bad, n, at):
     assert torch.equal(ob[:at], o[:at])
     assert not bool(ob[at:].isfinite().any())
     assert torch.equal(Sb[..., :17], S[..., :17]) and torch.equal(Sb[..., 18:], S[..., 18:])
+
+
+@pytest.mark.parametrize("io", TYPES)
+@pytest.mark.parametrize("delta,diag", [(1, 0), (0, 1), (1, 1)])
+def test_a_walked_prompt_equals_its_single_tokens(io, delta, diag):
+    # prompts that walk (few of them and many) and the recurrent form: the same bits
+    for seqs, n in ((1, 1), (1, 2), (2, 5), (9, 4)):
+        heads, dk, dv = 32, 64, 40
+        st, _ = state(seqs, heads, dk, dv, delta, diag)
+        start = st.f32.clone()
+        x = [y.to(DEV) for y in tokens(seqs * n, heads, 4, dk, dv, TYPES[io], 50 + n, diag)]
+        cu = torch.arange(0, seqs * n + 1, n, dtype=torch.int32, device=DEV)
+        o = st.attend(*x, cu)
+        S = st.f32.clone()
+        st.f32.copy_(start)
+        for t in range(n):
+            one = st.step_slots(*(y[t::n].contiguous() for y in x))
+            assert torch.equal(one, o[t::n])
+        assert torch.equal(st.f32, S)
