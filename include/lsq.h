@@ -382,12 +382,14 @@ lsq_status lsq_attend_workspace(const lsq_state* st, const lsq_token_batch* batc
  * the linear write (delta 0) the tokens are taken in chunks on the matrix
  * cores, as in that page's chunkwise realisation (Methodology) without its
  * INT8 operands: states and sums are fp32, operands are split so that the
- * state keeps fp32 accuracy.  A diagonal decay or the delta rule walks the
- * tokens one by one with the state in registers.  alpha lies in [0, 1] (0
- * forgets everything before the token, and so does one below 2^-126); a
- * negative or NaN alpha gives NaN from its token on.  A v that is not finite
- * makes its value column NaN from its token on, a q its own output; nothing
- * reaches an earlier token, another column or, of alpha and beta, another head.
+ * state keeps fp32 accuracy (magnitudes from 2^-100 to 2^127; smaller ones
+ * lose their last bits, larger ones may count as infinite).  A diagonal decay
+ * or the delta rule walks the tokens one by one with the state in registers.
+ * alpha lies in [0, 1] (0 forgets everything before the token, and so does one
+ * below 2^-126); a negative or NaN alpha gives NaN from its token on.  A v that
+ * is not finite makes its value column NaN from its token on, a q its own
+ * output; nothing reaches an earlier token, another column or, of alpha and
+ * beta, another head.
  * A long sequence is taken in segments whose states pass through the
  * workspace; the same batch gives the same bits on every call.
  *

@@ -620,3 +620,41 @@ def test_a_walked_prompt_equals_its_single_tokens(io, delta, diag):
             one = st.step_slots(*(y[t::n].contiguous() for y in x))
             assert torch.equal(one, o[t::n])
         assert torch.equal(st.f32, S)
+
+
+@pytest.mark.parametrize("io,e", [("f32", -90), ("f32", 100), ("bf16", -90), ("bf16", 100)])
+def test_small_and_large_magnitudes_keep_the_accuracy(io, e):
+    # v and the state scaled by a power of two: the outputs and the state scale with them.  Each side
+    # is within 16 u of the definition in the 2-norm (outputs: and half a step of their type).
+    st, _ = state(1, 2, 64, 80)
+    start = st.f32.clone()
+    q, k, v, alpha, beta = (x.to(DEV) for x in tokens(150, 2, 1, 64, 80, TYPES[io], 60))
+    cu = torch.tensor([0, 150], dtype=torch.int32, device=DEV)
+    o = st.attend(q, k, v, alpha, beta, cu).double()
+    S = st.f32.double()
+    st.f32.copy_(start * 2.0 ** e)
+    oe = st.attend(q, k, v * 2.0 ** e, alpha, beta, cu).double() * 2.0 ** -e
+    assert rel(st.f32.double().cpu() * 2.0 ** -e, S.cpu()) <= 32 * U32
+    assert rel(oe.cpu(), o.cpu()) <= 2 * half_step(TYPES[io]) + 32 * U32
+
+
+def test_a_negative_or_nan_alpha_gives_nan_from_its_token_on():
+    st, _ = state(1, 3, 64, 64)
+    start = st.f32.clone()
+    q, k, v, alpha, beta = (x.to(DEV) for x in tokens(90, 3, 1, 64, 64, torch.bfloat16, 61))
+    cu = torch.tensor([0, 90], dtype=torch.int32, device=DEV)
+    o = st.attend(q, k, v, alpha, beta, cu)
+    for bad in (-0.5, float("nan")):
+        a = alpha.clone()
+        a[45, 1] = bad
+        st.f32.copy_(start)
+        ob = st.attend(q, k, v, a, beta, cu)
+        assert torch.equal(ob[:45], o[:45]) and torch.equal(ob[:, ::2], o[:, ::2])
+        assert bool(ob[45:, 1].isnan().all()) and bool(st.f32.view(3, -1)[1].isnan().all())
+    a = alpha.clone()
+    outs = []
+    for tiny in (0.0, 1e-39):                # both forget what was before
+        a[45, 1] = tiny
+        st.f32.copy_(start)
+        outs.append((st.attend(q, k, v, a, beta, cu), st.f32.clone()))
+    assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
