@@ -331,9 +331,11 @@ lsq_status lsq_prefill(lsq_state* st, int32_t T, const float* k, const float* v,
  *   - a negative slot marks a padded entry: nothing of it is read or written
  *     (its output rows stay as they were);
  *   - a slot >= batch, or one that an earlier entry of the same call already
- *     names, is refused on the device: no state is touched and the entry's
+ *     takes, is refused on the device: no state is touched and the entry's
  *     output rows are filled with NaN (a copy of slots leaves the destination
- *     as it was).  The first entry that names a slot is carried out.
+ *     as it was).  The first entry that has something to do with a slot takes
+ *     it: an empty sequence takes none, nor does a copy whose source is padded
+ *     or beyond its handle.
  * Token inputs use LSQ_IO_* types for q, k, v and o; alpha and beta are fp32.
  */
 typedef enum { LSQ_IO_F32 = 0, LSQ_IO_F16 = 1, LSQ_IO_BF16 = 2 } lsq_io_type;

@@ -356,7 +356,7 @@ __global__ __launch_bounds__(64 * NW, NW / 2 / KS) void attend_kernel(AttendArgs
   // Offsets that decrease can name a token in several sequences, more of them
   // than the workspace was sized for.
   if (sg.j < 0 || sg.j >= sg.n || (sg.n > 1 && (sg.ws < 0 || sg.ws >= args.cut))) return;
-  const int slot = slot_of(a.slots, sg.i, a.nslots, lane);
+  const int slot = slot_of(a, sg.i, lane);
   if (slot == kPadded) return;
   const int d0 = slice * T::DV, vcols = a.dv - d0 < T::DV ? a.dv - d0 : T::DV;   // the slice's columns
   const int64_t hk = (int64_t)(h / a.share) * DK, hv = (int64_t)h * a.dv + d0;
@@ -800,7 +800,7 @@ __global__ __launch_bounds__(256) void combine_kernel(AttendArgs args, int block
   const Span sp = span_of(a, i);
   const int n = segments_of(sp, args.seg_len);
   if (n < 2) return;
-  const int lane = threadIdx.x & 63, slot = slot_of(a.slots, i, a.nslots, lane);
+  const int lane = threadIdx.x & 63, slot = slot_of(a, i, lane);
   if (slot < 0) return;
   int64_t first = 0;                             // the sequence's first segment in the workspace
   for (int i0 = 0;; i0 += 64) {

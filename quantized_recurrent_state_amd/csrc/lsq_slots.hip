@@ -52,7 +52,7 @@ __global__ __launch_bounds__(256) void walk_kernel(SlotArgs a, int row_blocks) {
   if (row0 >= a.dv) return;
   const Span sp = span_of(a, i);
   if (sp.t1 <= sp.t0) return;
-  const int slot = slot_of(a.slots, i, a.nslots, lane);
+  const int slot = slot_of(a, i, lane);
   if (slot == kPadded) return;
   const int orow = row0 + 4 * lc + lr;          // the row whose output this lane stores
   const bool owrite = lc < R && orow < a.dv;
@@ -192,7 +192,7 @@ __global__ __launch_bounds__(256) void store_slots_kernel(CopyArgs a, int64_t un
   using F = Fmt<BITS>;
   const int i = blockIdx.x / blocks, b = blockIdx.x % blocks;
   const int lane = threadIdx.x & 63;
-  const int dst = slot_of(a.dst_slots, i, a.dst_n, lane);
+  const int dst = slot_of(a, i, lane);
   const int src = a.src_slots ? a.src_slots[i] : i;
   if (dst < 0 || src < 0 || src >= a.src_n) return;
   const f32x4* S = reinterpret_cast<const f32x4*>(a.S) + (int64_t)src * units;
@@ -236,7 +236,7 @@ __global__ __launch_bounds__(256) void store_head_kernel(CopyArgs a, int head_un
   using F = Fmt<BITS>;
   __shared__ float wmax[4];
   const int i = blockIdx.x / a.heads, h = blockIdx.x % a.heads;
-  const int dst = slot_of(a.dst_slots, i, a.dst_n, threadIdx.x & 63);
+  const int dst = slot_of(a, i, threadIdx.x & 63);
   const int src = a.src_slots ? a.src_slots[i] : i;
   if (dst < 0 || src < 0 || src >= a.src_n) return;
   const f32x4* S = reinterpret_cast<const f32x4*>(a.S) + ((int64_t)src * a.heads + h) * head_units;
@@ -264,7 +264,7 @@ __global__ __launch_bounds__(256) void load_slots_kernel(CopyArgs a, int64_t uni
                                                          int64_t group_units) {
   const int i = blockIdx.x / blocks, b = blockIdx.x % blocks;
   const int lane = threadIdx.x & 63;
-  const int dst = slot_of(a.dst_slots, i, a.dst_n, lane);
+  const int dst = slot_of(a, i, lane);
   const int src = a.src_slots ? a.src_slots[i] : i;
   if (dst < 0 || src < 0 || src >= a.src_n) return;
   f32x4* S = reinterpret_cast<f32x4*>(a.S) + (int64_t)dst * units;

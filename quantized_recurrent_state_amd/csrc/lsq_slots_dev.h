@@ -72,16 +72,19 @@ __device__ __forceinline__ void store1(void* p, int64_t e, float x) {
 constexpr int kPadded = -1, kRefused = -2;
 
 // Entry i's slot: the slot itself, kPadded for a negative one, kRefused for
-// one beyond the handle or already named by an earlier entry (the wave's lanes
-// compare 64 earlier entries at a time).  Called by whole waves.
-__device__ __forceinline__ int slot_of(const int32_t* slots, int i, int n, int lane) {
+// one beyond the handle or already taken by an earlier entry (the wave's lanes
+// compare 64 earlier entries at a time).  works(j) tells whether entry j does
+// anything; one that does not takes no slot.  Called by whole waves.
+template <typename Works>
+__device__ __forceinline__ int slot_of(const int32_t* slots, int i, int n, int lane, Works works) {
   if (!slots) return i < n ? i : kRefused;
   const int s = __builtin_amdgcn_readfirstlane(slots[i]);
   if (s < 0) return kPadded;
   if (s >= n) return kRefused;
-  bool seen = false;
-  for (int j = lane; j < i; j += 64) seen |= slots[j] == s;
-  return __any(seen) ? kRefused : s;
+  bool taken = false;
+  for (int j = lane; j < i; j += 64)
+    if (slots[j] == s) taken |= works(j);
+  return __any(taken) ? kRefused : s;
 }
 
 struct Span {
@@ -93,6 +96,23 @@ __device__ __forceinline__ Span span_of(const SlotArgs& a, int i) {
   if (!a.cu) return {i, i + 1};
   const int64_t t0 = a.cu[i], t1 = a.cu[i + 1];
   return {t0 < 0 ? 0 : t0 > a.tokens ? a.tokens : t0, t1 < 0 ? 0 : t1 > a.tokens ? a.tokens : t1};
+}
+
+// The slot of a batch's entry i; an empty sequence takes none.
+__device__ __forceinline__ int slot_of(const SlotArgs& a, int i, int lane) {
+  return slot_of(a.slots, i, a.nslots, lane, [&](int j) {
+    const Span sp = span_of(a, j);
+    return sp.t1 > sp.t0;
+  });
+}
+
+// The destination of a copy's entry i; one whose source is padded or beyond
+// its handle takes none.
+__device__ __forceinline__ int slot_of(const CopyArgs& a, int i, int lane) {
+  return slot_of(a.dst_slots, i, a.dst_n, lane, [&](int j) {
+    const int src = a.src_slots ? a.src_slots[j] : j;
+    return src >= 0 && src < a.src_n;
+  });
 }
 
 }  // namespace dev
