@@ -847,30 +847,33 @@ namespace {
 int slice_width(int io, int dv) { return io == IO_F32 || dv <= 64 ? 64 : 128; }
 
 template <int IO, int DK, int NW, int KS, bool VEC>
-hipError_t launch_instance(const AttendArgs& args, unsigned blocks, hipStream_t s) {
+hipError_t launch_instance(const AttendArgs& args, hipStream_t s) {
   const SlotArgs& a = args.s;
+  const int64_t rows = (int64_t)args.slices * a.heads, blocks = args.segments * rows, cut = args.cut * rows;
+  const int64_t quads = (int64_t)a.heads * a.dv * DK / 4, most = 4096 / a.seqs + 1;
+  const int64_t per = (quads + 255) / 256 < most ? (quads + 255) / 256 : most;
+  if (!fits_launch(blocks, 64 * NW) ||
+      (args.seg_len && (!fits_launch(cut, 64 * NW) || !fits_launch(per * a.seqs, 256))))
+    return hipErrorInvalidConfiguration;
   if (args.seg_len) {
-    const unsigned cut = (unsigned)(args.cut * args.slices * a.heads);
-    hipLaunchKernelGGL((dev::attend_kernel<IO, DK, NW, KS, VEC, false>), dim3(cut), dim3(64 * NW), 0, s, args);
-    const int64_t quads = (int64_t)a.heads * a.dv * DK / 4, most = 4096 / a.seqs + 1;
-    const int64_t per = (quads + 255) / 256 < most ? (quads + 255) / 256 : most;
+    hipLaunchKernelGGL((dev::attend_kernel<IO, DK, NW, KS, VEC, false>), dim3((unsigned)cut), dim3(64 * NW), 0, s, args);
     hipLaunchKernelGGL(dev::combine_kernel, dim3((unsigned)(per * a.seqs)), dim3(256), 0, s, args,
                        (int)per, quads);
   }
-  hipLaunchKernelGGL((dev::attend_kernel<IO, DK, NW, KS, VEC, true>), dim3(blocks), dim3(64 * NW), 0, s, args);
+  hipLaunchKernelGGL((dev::attend_kernel<IO, DK, NW, KS, VEC, true>), dim3((unsigned)blocks), dim3(64 * NW), 0, s, args);
   return hipGetLastError();
 }
 
 template <int IO, int DK>
-hipError_t launch_width(const AttendArgs& args, unsigned blocks, hipStream_t s) {
+hipError_t launch_width(const AttendArgs& args, hipStream_t s) {
   if constexpr (IO == IO_F32) {
-    return launch_instance<IO, DK, 8, 2, true>(args, blocks, s);
+    return launch_instance<IO, DK, 8, 2, true>(args, s);
   } else {
     if (slice_width(IO, args.s.dv) == 128)
-      return args.wide ? launch_instance<IO, DK, 8, 1, true>(args, blocks, s)
-                       : launch_instance<IO, DK, 8, 1, false>(args, blocks, s);
-    return args.wide ? launch_instance<IO, DK, 4, 1, true>(args, blocks, s)
-                     : launch_instance<IO, DK, 4, 1, false>(args, blocks, s);
+      return args.wide ? launch_instance<IO, DK, 8, 1, true>(args, s)
+                       : launch_instance<IO, DK, 8, 1, false>(args, s);
+    return args.wide ? launch_instance<IO, DK, 4, 1, true>(args, s)
+                     : launch_instance<IO, DK, 4, 1, false>(args, s);
   }
 }
 
@@ -908,12 +911,9 @@ AttendPlan attend_plan(int64_t tokens, int32_t seqs, int32_t heads, int32_t dk, 
 }
 
 hipError_t launch_attend(const AttendArgs& args, int io, int dk, hipStream_t s) {
-  const int64_t blocks = args.segments * args.s.heads * args.slices;
-  if (!fits_launch(blocks, 512)) return hipErrorInvalidConfiguration;
-  const unsigned n = (unsigned)blocks;
-  if (io == IO_F32) return dk == 128 ? launch_width<IO_F32, 128>(args, n, s) : launch_width<IO_F32, 64>(args, n, s);
-  if (io == IO_F16) return dk == 128 ? launch_width<IO_F16, 128>(args, n, s) : launch_width<IO_F16, 64>(args, n, s);
-  return dk == 128 ? launch_width<IO_BF16, 128>(args, n, s) : launch_width<IO_BF16, 64>(args, n, s);
+  if (io == IO_F32) return dk == 128 ? launch_width<IO_F32, 128>(args, s) : launch_width<IO_F32, 64>(args, s);
+  if (io == IO_F16) return dk == 128 ? launch_width<IO_F16, 128>(args, s) : launch_width<IO_F16, 64>(args, s);
+  return dk == 128 ? launch_width<IO_BF16, 128>(args, s) : launch_width<IO_BF16, 64>(args, s);
 }
 
 }  // namespace lsq
