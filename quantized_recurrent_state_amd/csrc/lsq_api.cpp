@@ -633,7 +633,7 @@ lsq_status lsq_attend(lsq_state* st, const lsq_token_batch* batch, void* workspa
   }
   const int64_t e = (int64_t)io_bytes(batch->io);
   for (const int64_t x : {batch->q_stride, batch->k_stride, batch->v_stride, batch->o_stride})
-    if (x * e > INT32_MAX / 64)                  // lanes address a chunk's rows with 32 bits
+    if (x > INT32_MAX / 64 / e)                  // lanes address a chunk's rows with 32 bits
       return fail(LSQ_ERR_UNSUPPORTED, "a token stride of 32 MiB or more");
   lsq::AttendArgs a{};
   a.s = slot_args(st, batch);

@@ -25,3 +25,15 @@ def test_a_launch_is_refused_by_its_own_threads():
         assert attend(h, seqs=seqs, tokens=100) == narrow, seqs
         assert attend(h, seqs=seqs, tokens=100, io=lsq.IO_F32) == wide, seqs
     lsq.lsq_state_free(h)
+
+
+@pytest.mark.parametrize("io", [lsq.IO_BF16, lsq.IO_F32])
+@pytest.mark.parametrize("name", ["q_stride", "k_stride", "v_stride", "o_stride"])
+def test_a_far_stride_is_refused_whatever_its_size(name, io):
+    h = handle()
+    e = 4 if io == lsq.IO_F32 else 2
+    far = (32 << 20) // e                                   # 32 MiB between tokens
+    for stride in (far, 1 << 40, 1 << 61, 1 << 62, (1 << 62) + 256, (1 << 63) - 256):
+        assert attend(h, tokens=100, io=io, **{name: stride}) == UNSUPPORTED, stride
+    assert attend(h, tokens=100, io=io, **{name: far - 8}) == HIP
+    lsq.lsq_state_free(h)
