@@ -30,6 +30,8 @@ def _on_device(index, stream, call):
     if stream is not None:
         if not isinstance(stream, torch.cuda.Stream):
             stream = torch.cuda.ExternalStream(int(stream), device=index)
+        if stream.device.index != index:
+            raise ValueError(f"stream is on device {stream.device.index}, the state on {index}")
         with torch.cuda.stream(stream):
             return call(stream.cuda_stream)
     if index == torch.cuda.current_device():
