@@ -387,11 +387,14 @@ lsq_status lsq_attend_workspace(const lsq_state* st, const lsq_token_batch* batc
  * state keeps fp32 accuracy (magnitudes from 2^-100 to 2^127; smaller ones
  * lose their last bits, larger ones may count as infinite).  A diagonal decay
  * or the delta rule walks the tokens one by one with the state in registers.
- * alpha lies in [0, 1] (0 forgets everything before the token, and so does one
- * below 2^-126); a negative or NaN alpha gives NaN from its token on.  A v that
- * is not finite makes its value column NaN from its token on, a q its own
- * output; nothing reaches an earlier token, another column or, of alpha and
- * beta, another head.
+ * alpha lies in [0, 1].  The chunk form works with its logarithm: an alpha
+ * below 2^-126 counts as 0 and forgets what was before (a product of several
+ * alphas below it may too); a negative one gives NaN from its token on.  The walk,
+ * like lsq_step_slots, multiplies the state by alpha as it stands, also by one
+ * that is negative or subnormal.  A NaN alpha gives NaN from its token on.  A v
+ * that is not finite makes its value column so from its token on (NaN in the
+ * chunk form), a q its own output; nothing reaches an earlier token, another
+ * column or, of alpha and beta, another head.
  * A long sequence is taken in segments whose states pass through the
  * workspace; the same batch gives the same bits on every call.
  *
@@ -404,7 +407,8 @@ lsq_status lsq_attend_workspace(const lsq_state* st, const lsq_token_batch* batc
  * seqs < 0, tokens < 0, qk_heads not dividing heads, an o_stride below
  * heads * dv or a negative stride, a workspace of NULL where one is needed;
  * BUFFER_TOO_SMALL: a smaller workspace; UNSUPPORTED: a quantised handle, a
- * token stride of 32 MiB or more, or a launch of 2^32 threads or more. */
+ * token stride of 32 MiB or more (chunk form), or a launch of 2^32 threads or
+ * more. */
 lsq_status lsq_attend(lsq_state* st, const lsq_token_batch* batch, void* workspace,
                       size_t workspace_bytes, void* stream);
 
