@@ -71,6 +71,13 @@ struct Tile {
   // P of two chunks (its product with v runs one chunk behind).
   static constexpr int RB = IO == IO_BF16 ? 2 : 1;
   static constexpr bool BEHIND = IO != IO_F32;
+  // LDS bytes of the kernel with outputs (rows, P, the sums exchanged by two
+  // waves, decays), and the workgroups of a CU, one or two at least, that its 160 KiB
+  // hold: one of fp32 at Dk 128 (90 KiB), two or three of the others.  The launch
+  // bounds ask for registers to match.
+  static constexpr int LDS = 2 * C * (RB * NP * (PK + PV + PQ) + (BEHIND ? 2 : 1) * NO * PP) +
+                             (KS > 1 ? 16 * NT : 16) + 16 * RB * ROUND;
+  static constexpr int RESIDENT = 2 * LDS <= 160 * 1024 ? 2 : 1;
   static_assert(KS == 1 || (KS == 2 && !BEHIND), "the shared sums are read between the same two barriers");
 };
 
@@ -267,8 +274,8 @@ __device__ __forceinline__ Numbered number_segments(const SlotArgs& a, int64_t L
 }
 
 // Segment s of the batch, of the cut sequences alone where CUT.  rows:
-// workgroups per segment.
-template <bool CUT>
+// workgroups per segment.  PAIRED: CUs hold two workgroups.
+template <bool CUT, bool PAIRED>
 __device__ __forceinline__ Segment segment_of(const SlotArgs& a, int64_t L, int64_t s, int rows, int lane) {
   Segment g{};
   g.i = (int)s;
@@ -278,10 +285,13 @@ __device__ __forceinline__ Segment segment_of(const SlotArgs& a, int64_t L, int6
       if (i0 >= a.seqs) return g;
       const Numbered m = number_segments(a, L, i0, lane);
       const int upto = CUT ? m.cut : m.upto, all = __builtin_amdgcn_readlane(upto, 63);
-      // Two workgroups share a CU: those of the second round in reverse, a long
-      // sequence beside a short one.
+      // Where two workgroups share a CU, those of the second round come in reverse,
+      // a long sequence beside a short one (16 prompts of 900-4096 tokens, 32 heads
+      // 128x128 in bf16: 351 us, 369 without; fp32, 64x64: 304 and 327).  Where a CU
+      // holds one, the next starts as CUs fall free, and the longest first is right
+      // (fp32, 128x64: 481 us, 555 in reverse; 8 of 300-2400, 64 heads: 267 and 305).
       const int64_t round = kCUs / rows;
-      if (!CUT && a.seqs <= 64 && s >= round && s < 2 * round && s < all)
+      if (!CUT && PAIRED && a.seqs <= 64 && s >= round && s < 2 * round && s < all)
         s = (all < 2 * round ? all : 2 * round) - 1 - (s - round);
       if (s < all) {
         const int at = __builtin_ctzll(__ballot(upto > (int)s));
@@ -331,7 +341,7 @@ __device__ __forceinline__ Item item_of(int64_t b, int rows) {
 // (no q, no output), for the segments behind it.  VEC: v and o by dwords and
 // more (else by element: 16-bit types of odd widths or addresses).
 template <int IO, int DK, int NW, int KS, bool VEC, bool OUT>
-__global__ __launch_bounds__(64 * NW, NW / 2 / KS) void attend_kernel(AttendArgs args) {
+__global__ __launch_bounds__(64 * NW, (NW * Tile<IO, DK, NW, KS>::RESIDENT / 4)) void attend_kernel(AttendArgs args) {
   using T = Tile<IO, DK, NW, KS>;
   constexpr int NP = T::NP, NO = T::NO, C = T::C, PK = T::PK, PV = T::PV, PQ = T::PQ, PP = T::PP;
   constexpr int NT = T::NT, EU = T::EU, RB = T::RB, ROUND = T::ROUND, B = 16 / EU;   // B: bytes of an element
@@ -346,12 +356,13 @@ __global__ __launch_bounds__(64 * NW, NW / 2 / KS) void attend_kernel(AttendArgs
   __shared__ __align__(16) __bf16 pl[OUT && BEHIND ? 2 : 1][OUT ? NO : 1][OUT ? C * PP : 8];
   __shared__ __align__(16) f32x4 part[OUT && KS > 1 ? NW * 64 : 1];
   __shared__ __align__(16) Decays<ROUND> dec[RB];
+  static_assert(!OUT || sizeof(kl) + sizeof(vl) + sizeof(ql) + sizeof(pl) + sizeof(part) + sizeof(dec) == T::LDS);
 
   const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, li = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const Item item = item_of(blockIdx.x, args.slices * a.heads);
   const int h = item.row / args.slices, slice = item.row % args.slices;
-  const Segment sg = segment_of<!OUT>(a, args.seg_len, item.seg, args.slices * a.heads, lane);
+  const Segment sg = segment_of<!OUT, (T::RESIDENT > 1)>(a, args.seg_len, item.seg, args.slices * a.heads, lane);
   if (sg.n == 0 || (!OUT && sg.j == sg.n - 1)) return;
   // Offsets that decrease can name a token in several sequences, more of them
   // than the workspace was sized for.
@@ -842,8 +853,8 @@ __global__ __launch_bounds__(256) void combine_kernel(AttendArgs args, int block
 
 namespace {
 
-// Value columns of a workgroup.  Three bf16 parts of fp32 rows fill the LDS of
-// half a CU at 64.
+// Value columns of a workgroup.  Three bf16 parts of fp32 rows take 66 KiB of LDS
+// at 64 columns of Dk 64, 90 at Dk 128.
 int slice_width(int io, int dv) { return io == IO_F32 || dv <= 64 ? 64 : 128; }
 
 template <int IO, int DK, int NW, int KS, bool VEC>
@@ -884,10 +895,10 @@ AttendPlan attend_plan(int64_t tokens, int32_t seqs, int32_t heads, int32_t dk, 
   const int width = slice_width(io, dv);
   p.slices = (dv + width - 1) / width;
   p.segments = seqs;
-  // A segment: a 512th of the work (two workgroups on each of 256 CUs), but 256
-  // tokens at least, and more where a long sequence has few rows, so that the
-  // combination's steps (0.5 us each) and a segment's chunks (3.5 us for both
-  // passes) take as long.  The host does not see the lengths: where the rows
+  // A segment: a 512th of the work (two workgroups on each of 256 CUs; for fp32 at
+  // Dk 128 one after the other), but 256 tokens at least, and more where a long
+  // sequence has few rows, so that the combination's steps (0.5 us each) and a
+  // segment's chunks (3.5 us for both passes) take as long.  The host does not see the lengths: where the rows
   // alone occupy the CUs, or the sequences are short on average, a batch of few
   // tokens is taken whole; otherwise the kernels cut the sequences of more than
   // two segments.
