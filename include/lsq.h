@@ -384,9 +384,12 @@ lsq_status lsq_attend_workspace(const lsq_state* st, const lsq_token_batch* batc
  * the linear write (delta 0) the tokens are taken in chunks on the matrix
  * cores, as in that page's chunkwise realisation (Methodology) without its
  * INT8 operands: states and sums are fp32, operands are split so that the
- * state keeps fp32 accuracy (magnitudes from 2^-100 to 2^127; smaller ones
- * lose their last bits, larger ones may count as infinite).  A diagonal decay
- * or the delta rule walks the tokens one by one with the state in registers.
+ * state and fp32 outputs keep fp32 accuracy (magnitudes from 2^-100 to 2^127;
+ * smaller ones lose their last bits, larger ones may count as infinite).  The
+ * operands of a 16-bit output are held to 16 bits: before its one rounding it
+ * is off by at most 2^-16 (bf16) or 3 2^-16 (binary16) of the sum of its terms'
+ * magnitudes, beside fp32's own rounding.  A diagonal decay or the delta rule
+ * walks the tokens one by one with the state in registers, all in fp32.
  * alpha lies in [0, 1].  The chunk form works with its logarithm: an alpha
  * below 2^-126 counts as 0 and forgets what was before (a product of several
  * alphas below it may too); a negative one gives NaN from its token on.  The walk,

@@ -248,8 +248,7 @@ size_t io_bytes(int32_t io) { return io == LSQ_IO_F32 ? 4 : 2; }
 
 bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
-// Checks of a token batch over an fp32 handle that need no device; `one` for
-// one token per entry (no offsets to read).
+// Checks of a token batch over an fp32 handle that need no device.
 lsq_status check_batch(const lsq_state* st, const lsq_token_batch* b) {
   if (!st) return fail(LSQ_ERR_INVALID_ARG, "state is null");
   if (!b) return fail(LSQ_ERR_INVALID_ARG, "batch is null");
