@@ -142,7 +142,8 @@ def lsq_prefill(handle: int, T: int, k, v, alpha, beta, stream=None) -> None:
 def token_batch(io: int, qk_heads: int, seqs: int, tokens: int, q, k, v, alpha, beta, o,
                 q_stride: int, k_stride: int, v_stride: int, o_stride: int, cu_seqlens=None,
                 slots=None, fresh=None) -> _lib.lsq_token_batch:
-    """``lsq_token_batch`` over device tensors (strides in elements between tokens)."""
+    """``lsq_token_batch`` over device tensors (strides in elements between tokens).  It holds their
+    addresses: the caller keeps the tensors alive while it is used."""
     return _lib.lsq_token_batch(io, qk_heads, seqs, tokens, q_stride, k_stride, v_stride, o_stride,
                                 _ptr(q), _ptr(k), _ptr(v), _ptr(alpha), _ptr(beta), _ptr(o),
                                 _ptr(cu_seqlens), _ptr(slots), _ptr(fresh))
@@ -352,8 +353,9 @@ class LsqState:
     def attend(self, q, k, v, alpha, beta, cu_seqlens, slots=None, fresh=None, o=None, stream=None):
         """Linear attention over a packed batch of prompts (``lsq_attend``), on an fp32 state.
 
-        q, k [tokens, qk_heads, dk] and v [tokens, heads, dv] in float32, float16 or bfloat16 (token
-        strides free, heads contiguous); alpha, beta as in ``step`` with a leading [tokens] axis;
+        q, k [tokens, qk_heads, dk] and v [tokens, heads, dv] in float32, float16 or bfloat16 (heads
+        contiguous, token strides below 32 MiB; q and k 16-byte aligned, their strides whole multiples
+        of 16 bytes); alpha, beta as in ``step`` with a leading [tokens] axis;
         cu_seqlens int32 [seqs + 1]; slots int32 [seqs] (default: sequence i is slot i); fresh bool
         [seqs] starts those sequences from S = 0.  Returns o [tokens, heads, dv] in q's type; the
         slots hold the sequences' final states.  Rows of o outside every sequence, and those of
@@ -362,7 +364,7 @@ class LsqState:
 
     def step_slots(self, q, k, v, alpha, beta, slots=None, fresh=None, o=None, stream=None):
         """One token for each listed slot (``lsq_step_slots``), on an fp32 state: the tensors of
-        ``attend`` with one token per entry.  Returns o [entries, heads, dv]."""
+        ``attend`` with one token per entry and strides of any length.  Returns o [entries, heads, dv]."""
         return _slots().step_slots(self, q, k, v, alpha, beta, slots, fresh, o, stream)
 
     def store_slots(self, src, slots=None, src_slots=None, stream=None):

@@ -230,7 +230,10 @@ __global__ __launch_bounds__(256) void store_slots_kernel(CopyArgs a, int64_t un
 }
 
 // One scale per head: a workgroup takes a head, its absmax first, then the
-// codes from a second read that the caches serve.
+// codes from a second read.  Counted, the state is fetched twice: the heads of a
+// round do not stay in L2, and the second read comes from the Infinity Cache (128
+// slots of 32 heads 128x128: 81 us to INT4, 3.8 TB/s of the bytes counted once, and
+// 90 to INT8; one slot 9.7 us).
 template <int BITS>
 __global__ __launch_bounds__(256) void store_head_kernel(CopyArgs a, int head_units) {
   using F = Fmt<BITS>;
