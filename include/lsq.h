@@ -443,6 +443,96 @@ lsq_status lsq_state_load_slots(lsq_state* dst, const lsq_state* src, int32_t co
                                 const int32_t* dst_slots, const int32_t* src_slots,
                                 void* stream);
 
+/* ---- Drafted tokens over the slots of an fp32 handle ----
+ *
+ * A program that drafts tokens holds, for each sequence, a tree of nodes: node j
+ * continues node parents[j] < j, or the slot's own state where parents[j] is
+ * -1 (node 0 is usually the last token of the sequence, which the slot does
+ * not hold yet).  lsq_step_tree gives the output of every node, lsq_verify_tree
+ * tests the drafted nodes against the target model's probabilities, and
+ * lsq_accept_path writes the nodes of the accepted path into the slot.  Trees
+ * have up to 64 nodes.  Node numbers count within their tree; node j of entry i
+ * is row cu[i] + j of the packed arrays.  As in the calls above, slots,
+ * offsets, parents and paths are device data, checked by the kernels, and the
+ * calls may be captured and replayed with other values in them.
+ */
+
+/* The recurrence along every path of the trees: for node j with parent p,
+ *   S_j = alpha_j S_p + beta_j (v_j - delta alpha_j S_p k_j) k_j^T,   o_j = S_j q_j,
+ * where S_-1 is the slot's state (0 for a fresh entry).  The batch is
+ * lsq_attend's, cu_seqlens [seqs + 1] being the nodes' offsets (clamped as there);
+ * max_nodes bounds the nodes of a tree.  The slots are read only, so several
+ * entries may name one slot.  Output rows outside every tree, and those of
+ * negative slots, are not written.  A slot >= batch, a tree of more than
+ * max_nodes nodes and one with a parent outside [-1, j) are refused on the
+ * device: their output rows are filled with NaN.  The step index does not
+ * move.  Alignment and errors as lsq_attend (no workspace); INVALID_ARG also:
+ * max_nodes < 1, null or misaligned parents; UNSUPPORTED also: max_nodes > 64. */
+lsq_status lsq_step_tree(const lsq_state* st, const lsq_token_batch* batch, const int32_t* parents,
+                         int32_t max_nodes, void* stream);
+
+/* Accepted paths into the state: entry i advances its slot (or 0 where fresh) by
+ * nodes path[i][0 .. lengths[i]), in this order, each as one token of the
+ * recurrence; path is [seqs][depth].  The batch is lsq_step_tree's; its q and o
+ * are not used and may be NULL.  An entry with a length of 0 or less does
+ * nothing, like one with a negative slot, and takes no slot.  A slot >= batch or
+ * taken by an earlier entry, a length above depth, and a node outside the
+ * entry's tree are refused on the device: the state stays as it was.  The
+ * arithmetic is lsq_step_slots', token by token in fp32, whatever the io type.
+ * depth = 0 does nothing.  Errors as lsq_step_tree; INVALID_ARG also: null or
+ * misaligned path or lengths, depth < 0; UNSUPPORTED also: depth > 64. */
+lsq_status lsq_accept_path(lsq_state* st, const lsq_token_batch* batch, const int32_t* path,
+                           const int32_t* lengths, int32_t depth, void* stream);
+
+/* Trees of drafted tokens and the probabilities they are tested against.  Row j
+ * of target (and draft) is the target (draft) model's distribution behind node
+ * j, that of its children; consecutive rows are target_stride (draft_stride)
+ * elements apart.  ids[j] is node j's token (node 0's is not read), uniform[j]
+ * the number in [0, 1) that decides on node j, uniform_next[i] the one that
+ * draws entry i's next token.  draft NULL: the drafts have no probabilities
+ * (each is certain to its model: a one-hot row).  replacement: siblings were
+ * drawn independently of each other (1), or without replacement (0; not used
+ * where draft is NULL). */
+typedef struct {
+  int32_t seqs, vocab;
+  int32_t depth;               /* most nodes of a path, columns of path */
+  int32_t replacement;
+  int64_t nodes;               /* rows */
+  int64_t target_stride, draft_stride;
+  const float* target;
+  const float* draft;          /* or NULL */
+  const int32_t* ids;          /* [nodes] */
+  const int32_t* parents;      /* [nodes] */
+  const int32_t* cu_nodes;     /* [seqs + 1] */
+  const float* uniform;        /* [nodes] */
+  const float* uniform_next;   /* [seqs] */
+  int32_t* path;               /* [seqs][depth], out */
+  int32_t* lengths;            /* [seqs], out */
+  int32_t* next;               /* [seqs], out */
+} lsq_draft_batch;
+
+/* Verification: entry i's walk starts at node 0, which is accepted as it
+ * stands, and tests the children x_1, x_2, ... of the node it is at, in order,
+ * with p and q the node's target and draft row.  P_1 = p, T_1 = Q_1 = 1, c_1 = 0:
+ *   x_i is accepted if uniform T_i q(x_i) < P_i(x_i) Q_i, and the walk goes on
+ *   there; otherwise c_i+1 = c_i + T_i / Q_i, P_i+1 = max(p - c_i+1 q, 0), T_i+1 is
+ *   its sum, and Q_i+1 is 1, or without replacement 1 - q(x_1) - ... - q(x_i).
+ * (P / T is what the residual rule of rejection sampling leaves for the next
+ * sibling, so that every accepted or drawn token has the target's distribution.)
+ * Without draft probabilities x_i is accepted if uniform T_i < P_i(x_i), else P_i+1
+ * is P_i without x_i and T_i+1 = T_i - P_i(x_i).  Where no child is accepted,
+ * or the path has depth nodes, the next token is the first y whose cumulative
+ * sum of P (of p where the path is full) exceeds uniform_next times its sum;
+ * where P is empty, of p; -1 where that is empty too.  All of it is fp64.
+ * A NaN counts as no probability, and a node whose token lies outside
+ * [0, vocab) is passed over.  Out: path, node 0 first, -1 behind its end; its
+ * length; next.  An empty tree, one of more than 64 nodes, and one with a
+ * parent outside [-1, j) get the length 0, next -1 and a path of -1; offsets
+ * are clamped to [0, nodes].  INVALID_ARG: null arrays, arrays not 4-byte
+ * aligned, seqs < 0, nodes < 0, vocab < 1, depth < 1, a negative stride,
+ * replacement not 0 or 1; UNSUPPORTED: vocab > 2^22, or 2^22 entries and more. */
+lsq_status lsq_verify_tree(const lsq_draft_batch* batch, void* stream);
+
 /* Static description of a status code. */
 const char* lsq_status_string(lsq_status s);
 

@@ -26,6 +26,7 @@ __all__ = ["LsqConfig", "LsqState", "LsqError", "lsq_state_sizes", "lsq_state_al
            "lsq_state_step_index", "lsq_state_set_step_index",
            "lsq_decode_step", "lsq_decode_run", "lsq_prefill", "token_batch", "lsq_attend_workspace",
            "lsq_attend", "lsq_step_slots", "lsq_state_store_slots", "lsq_state_load_slots",
+           "lsq_step_tree", "lsq_accept_path", "lsq_verify_tree", "verify_tree",
            "lsq_status_string", "lsq_version",
            "lsq_probe_stream", "lsq_probe_span",
            "lsq_probe_valu"]
@@ -166,6 +167,34 @@ def lsq_attend(handle: int, batch, workspace=None, stream=None) -> None:
 def lsq_step_slots(handle: int, batch, stream=None) -> None:
     _lib.check(_lib.load().lsq_step_slots(handle, ctypes.byref(batch), _stream_ptr(stream)),
                "lsq_step_slots")
+
+
+def lsq_step_tree(handle: int, batch, parents, max_nodes: int, stream=None) -> None:
+    _lib.check(_lib.load().lsq_step_tree(handle, ctypes.byref(batch), _ptr(parents), int(max_nodes),
+                                         _stream_ptr(stream)), "lsq_step_tree")
+
+
+def lsq_accept_path(handle: int, batch, path, lengths, depth: int, stream=None) -> None:
+    _lib.check(_lib.load().lsq_accept_path(handle, ctypes.byref(batch), _ptr(path), _ptr(lengths),
+                                           int(depth), _stream_ptr(stream)), "lsq_accept_path")
+
+
+def lsq_verify_tree(batch, stream=None) -> None:
+    _lib.check(_lib.load().lsq_verify_tree(ctypes.byref(batch), _stream_ptr(stream)), "lsq_verify_tree")
+
+
+def verify_tree(target, tokens, parents, cu_nodes, uniform, uniform_next, draft=None, replacement=True,
+                depth=64, stream=None):
+    """Trees of drafted tokens tested against the target's probabilities (``lsq_verify_tree``).
+
+    target (and draft) fp32 [nodes, vocab], rows contiguous, row j the distribution of node j's
+    children; tokens and parents int32 [nodes]; cu_nodes int32 [seqs + 1]; uniform fp32 [nodes] and
+    uniform_next fp32 [seqs], in [0, 1).  draft None: the drafts have no probabilities.
+    replacement False: siblings were drawn without replacement.  Returns (path [seqs, depth],
+    lengths [seqs], next [seqs]), int32: the accepted nodes, node 0 first and -1 behind the last,
+    their number, and the token drawn behind them; the first two are ``accept_path``'s arguments."""
+    return _drafts().verify_tree(target, tokens, parents, cu_nodes, uniform, uniform_next, draft,
+                                 replacement, depth, stream)
 
 
 def lsq_state_store_slots(dst: int, src: int, count: int, dst_slots=None, src_slots=None,
@@ -367,6 +396,24 @@ class LsqState:
         ``attend`` with one token per entry and strides of any length.  Returns o [entries, heads, dv]."""
         return _slots().step_slots(self, q, k, v, alpha, beta, slots, fresh, o, stream)
 
+    def step_tree(self, q, k, v, alpha, beta, cu_nodes, parents, slots=None, fresh=None, max_nodes=64,
+                  o=None, stream=None):
+        """The recurrence along every path of a tree of drafted tokens for each listed slot
+        (``lsq_step_tree``), on an fp32 state, which is left as it is.
+
+        The tensors of ``attend`` with one row per node (strides of any length); cu_nodes int32
+        [seqs + 1] the trees' offsets; parents int32 [nodes], within the tree: -1 or an earlier node;
+        max_nodes (at most 64) bounds a tree's nodes.  Returns o [nodes, heads, dv] in q's type."""
+        return _drafts().step_tree(self, q, k, v, alpha, beta, cu_nodes, parents, slots, fresh, max_nodes,
+                                   o, stream)
+
+    def accept_path(self, k, v, alpha, beta, cu_nodes, path, lengths, slots=None, fresh=None, stream=None):
+        """Advance each listed slot by the accepted nodes of its tree (``lsq_accept_path``):
+        path int32 [seqs, depth] with depth at most 64, of which lengths int32 [seqs] entries count;
+        the other tensors as in ``step_tree``."""
+        _drafts().accept_path(self, k, v, alpha, beta, cu_nodes, path, lengths, slots, fresh, stream)
+        return self
+
     def store_slots(self, src, slots=None, src_slots=None, stream=None):
         """Quantise slots of the fp32 state ``src`` into this quantised state
         (``lsq_state_store_slots``): entry i takes src_slots[i] to slots[i] (int32 device tensors;
@@ -381,7 +428,15 @@ class LsqState:
         return dst
 
 
-_slots_module = None
+_slots_module = _drafts_module = None
+
+
+def _drafts():
+    global _drafts_module
+    if _drafts_module is None:
+        from . import drafts
+        _drafts_module = drafts
+    return _drafts_module
 
 
 def _slots():

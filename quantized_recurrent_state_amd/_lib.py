@@ -41,6 +41,13 @@ class lsq_token_batch(ctypes.Structure):
                                                 "slots", "fresh")])
 
 
+class lsq_draft_batch(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("seqs", "vocab", "depth", "replacement")] +
+                [(n, ctypes.c_int64) for n in ("nodes", "target_stride", "draft_stride")] +
+                [(n, ctypes.c_void_p) for n in ("target", "draft", "ids", "parents", "cu_nodes", "uniform",
+                                                "uniform_next", "path", "lengths", "next")])
+
+
 class LsqError(RuntimeError):
     def __init__(self, status: int, where: str, detail: str):
         self.status = status
@@ -80,6 +87,9 @@ def load() -> ctypes.CDLL:
         "lsq_attend_workspace": [P, batchp, ctypes.POINTER(S)],
         "lsq_attend": [P, batchp, P, S, P],
         "lsq_step_slots": [P, batchp, P],
+        "lsq_step_tree": [P, batchp, P, ctypes.c_int32, P],
+        "lsq_accept_path": [P, batchp, P, P, ctypes.c_int32, P],
+        "lsq_verify_tree": [ctypes.POINTER(lsq_draft_batch), P],
         "lsq_state_store_slots": [P, P, ctypes.c_int32, P, P, P],
         "lsq_state_load_slots": [P, P, ctypes.c_int32, P, P, P],
         "lsq_status_string": [ctypes.c_int],

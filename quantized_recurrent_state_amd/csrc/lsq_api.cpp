@@ -248,8 +248,9 @@ size_t io_bytes(int32_t io) { return io == LSQ_IO_F32 ? 4 : 2; }
 
 bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
-// Checks of a token batch over an fp32 handle that need no device.
-lsq_status check_batch(const lsq_state* st, const lsq_token_batch* b) {
+// Checks of a token batch over an fp32 handle that need no device; outputs: q
+// and o are used.
+lsq_status check_batch(const lsq_state* st, const lsq_token_batch* b, bool outputs = true) {
   if (!st) return fail(LSQ_ERR_INVALID_ARG, "state is null");
   if (!b) return fail(LSQ_ERR_INVALID_ARG, "batch is null");
   if (st->cfg.bits != 32)
@@ -260,9 +261,9 @@ lsq_status check_batch(const lsq_state* st, const lsq_token_batch* b) {
   if (b->qk_heads < 0 || (b->qk_heads == 0 && st->cfg.heads > 0) ||
       (b->qk_heads > 0 && st->cfg.heads % b->qk_heads != 0))
     return fail(LSQ_ERR_INVALID_ARG, "qk_heads %d must divide heads %d", b->qk_heads, st->cfg.heads);
-  if (b->q_stride < 0 || b->k_stride < 0 || b->v_stride < 0)
+  if ((outputs && b->q_stride < 0) || b->k_stride < 0 || b->v_stride < 0)
     return fail(LSQ_ERR_INVALID_ARG, "negative token stride");
-  if (b->o_stride < (int64_t)st->cfg.heads * st->cfg.dv)
+  if (outputs && b->o_stride < (int64_t)st->cfg.heads * st->cfg.dv)
     return fail(LSQ_ERR_INVALID_ARG, "o_stride must be at least heads * dv");
   return ok();
 }
@@ -271,13 +272,13 @@ bool empty_batch(const lsq_state* st, const lsq_token_batch* b) {
   return n_heads(st->cfg) == 0 || b->seqs == 0 || b->tokens == 0;
 }
 
-lsq_status check_batch_ptrs(const lsq_state* st, const lsq_token_batch* b) {
+lsq_status check_batch_ptrs(const lsq_state* st, const lsq_token_batch* b, bool outputs = true) {
   const size_t e = io_bytes(b->io);
-  if (!b->q || !b->k || !b->v || !b->alpha || !b->beta || !b->o)
+  if ((outputs && (!b->q || !b->o)) || !b->k || !b->v || !b->alpha || !b->beta)
     return fail(LSQ_ERR_INVALID_ARG, "q, k, v, alpha, beta and o must be non-null");
-  if (!aligned16(b->q) || !aligned16(b->k) || (b->q_stride * e) % 16 || (b->k_stride * e) % 16)
+  if ((outputs && (!aligned16(b->q) || (b->q_stride * e) % 16)) || !aligned16(b->k) || (b->k_stride * e) % 16)
     return fail(LSQ_ERR_INVALID_ARG, "q and k must be 16-byte aligned, their token strides a multiple of 16 bytes");
-  if (!aligned_to(b->v, e) || !aligned_to(b->o, e) || !aligned4(b->beta) || !aligned4(b->alpha))
+  if (!aligned_to(b->v, e) || (outputs && !aligned_to(b->o, e)) || !aligned4(b->beta) || !aligned4(b->alpha))
     return fail(LSQ_ERR_INVALID_ARG, "v, o, alpha and beta must be aligned to their elements");
   if (st->cfg.decay == LSQ_DECAY_DIAG && !aligned16(b->alpha))
     return fail(LSQ_ERR_INVALID_ARG, "a diagonal alpha must be 16-byte aligned");
@@ -663,6 +664,74 @@ lsq_status lsq_step_slots(lsq_state* st, const lsq_token_batch* batch, void* str
                      "step_slots launch");
 }
 
+lsq_status lsq_step_tree(const lsq_state* st, const lsq_token_batch* batch, const int32_t* parents,
+                         int32_t max_nodes, void* stream) {
+  lsq_status s = check_batch(st, batch);
+  if (s != LSQ_OK) return s;
+  if (max_nodes < 1) return fail(LSQ_ERR_INVALID_ARG, "max_nodes must be at least 1");
+  if (max_nodes > lsq::kMaxNodes)
+    return fail(LSQ_ERR_UNSUPPORTED, "trees of more than %d nodes", lsq::kMaxNodes);
+  if (empty_batch(st, batch)) return ok();
+  if (!batch->cu_seqlens) return fail(LSQ_ERR_INVALID_ARG, "cu_seqlens is null");
+  if (!parents || !aligned4(parents))
+    return fail(LSQ_ERR_INVALID_ARG, "parents must be non-null and 4-byte aligned");
+  s = check_batch_ptrs(st, batch);
+  if (s != LSQ_OK) return s;
+  const lsq_config& c = st->cfg;
+  const lsq::TreeArgs a{slot_args(st, batch), parents, max_nodes, past_cache(c, batch->seqs)};
+  return slot_status(lsq::launch_tree(a, batch->io, c.dk, c.delta, c.decay == LSQ_DECAY_DIAG,
+                                      static_cast<hipStream_t>(stream)), "step_tree launch");
+}
+
+lsq_status lsq_accept_path(lsq_state* st, const lsq_token_batch* batch, const int32_t* path,
+                           const int32_t* lengths, int32_t depth, void* stream) {
+  lsq_status s = check_batch(st, batch, false);
+  if (s != LSQ_OK) return s;
+  if (depth < 0) return fail(LSQ_ERR_INVALID_ARG, "negative depth");
+  if (depth > lsq::kMaxNodes)
+    return fail(LSQ_ERR_UNSUPPORTED, "paths of more than %d nodes", lsq::kMaxNodes);
+  if (empty_batch(st, batch) || depth == 0) return ok();
+  if (!batch->cu_seqlens) return fail(LSQ_ERR_INVALID_ARG, "cu_seqlens is null");
+  if (!path || !lengths || !aligned4(path) || !aligned4(lengths))
+    return fail(LSQ_ERR_INVALID_ARG, "path and lengths must be non-null and 4-byte aligned");
+  s = check_batch_ptrs(st, batch, false);
+  if (s != LSQ_OK) return s;
+  const lsq_config& c = st->cfg;
+  const lsq::PathArgs a{slot_args(st, batch), path, lengths, depth, past_cache(c, batch->seqs)};
+  return slot_status(lsq::launch_path(a, batch->io, c.dk, c.delta, c.decay == LSQ_DECAY_DIAG,
+                                      static_cast<hipStream_t>(stream)), "accept_path launch");
+}
+
+lsq_status lsq_verify_tree(const lsq_draft_batch* b, void* stream) {
+  if (!b) return fail(LSQ_ERR_INVALID_ARG, "batch is null");
+  if (b->seqs < 0 || b->nodes < 0) return fail(LSQ_ERR_INVALID_ARG, "negative seqs or nodes");
+  if (b->vocab < 1) return fail(LSQ_ERR_INVALID_ARG, "vocab must be at least 1");
+  if (b->depth < 1) return fail(LSQ_ERR_INVALID_ARG, "depth must be at least 1");
+  if (b->replacement != 0 && b->replacement != 1)
+    return fail(LSQ_ERR_INVALID_ARG, "replacement must be 0 or 1");
+  if (b->vocab > lsq::kMaxVocab)
+    return fail(LSQ_ERR_UNSUPPORTED, "a vocabulary of more than %d tokens", lsq::kMaxVocab);
+  if (b->target_stride < 0 || (b->draft && b->draft_stride < 0))
+    return fail(LSQ_ERR_INVALID_ARG, "negative row stride");
+  if (b->seqs == 0) return ok();
+  if (!b->cu_nodes || !b->path || !b->lengths || !b->next ||
+      (b->nodes > 0 && (!b->target || !b->ids || !b->parents || !b->uniform || !b->uniform_next)))
+    return fail(LSQ_ERR_INVALID_ARG, "all arrays but draft must be non-null");
+  for (const void* p : {(const void*)b->target, (const void*)b->draft, (const void*)b->ids, (const void*)b->parents,
+                        (const void*)b->cu_nodes, (const void*)b->uniform, (const void*)b->uniform_next,
+                        (const void*)b->path, (const void*)b->lengths, (const void*)b->next})
+    if (!aligned4(p)) return fail(LSQ_ERR_INVALID_ARG, "arrays must be 4-byte aligned");
+  lsq::VerifyArgs a{};
+  a.target = b->target; a.draft = b->draft;
+  a.ids = b->ids; a.parents = b->parents; a.cu = b->cu_nodes;
+  a.uniform = b->uniform; a.uniform_next = b->uniform_next;
+  a.path = b->path; a.lengths = b->lengths; a.next = b->next;
+  a.target_stride = b->target_stride; a.draft_stride = b->draft_stride;
+  a.nodes = b->nodes;
+  a.seqs = b->seqs; a.vocab = b->vocab; a.depth = b->depth; a.replacement = b->replacement;
+  return slot_status(lsq::launch_verify(a, static_cast<hipStream_t>(stream)), "verify_tree launch");
+}
+
 lsq_status lsq_state_store_slots(lsq_state* dst, const lsq_state* src, int32_t count,
                                  const int32_t* dst_slots, const int32_t* src_slots, void* stream) {
   return copy_slots(src, dst, true, count, dst_slots, src_slots, stream);
@@ -744,6 +813,6 @@ const char* lsq_status_string(lsq_status s) {
 
 const char* lsq_last_error(void) { return g_last_error.c_str(); }
 
-int32_t lsq_version(void) { return 103; }
+int32_t lsq_version(void) { return 104; }
 
 }  // extern "C"

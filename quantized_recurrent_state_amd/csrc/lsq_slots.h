@@ -1,5 +1,5 @@
 // Interface between the host API (lsq_api.cpp) and the slot kernels
-// (lsq_slots.hip, lsq_attend.hip).  Not installed.
+// (lsq_slots.hip, lsq_attend.hip, lsq_tree.hip, lsq_verify.hip).  Not installed.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -63,6 +63,44 @@ struct CopyArgs {
   int32_t nt;              // the read-back states take the non-temporal hint
 };
 
+// Drafted tokens: trees of up to kMaxNodes nodes, one wave's lanes.
+constexpr int kMaxNodes = 64;
+
+struct TreeArgs {
+  SlotArgs s;              // cu: the trees' nodes
+  const int32_t* parents;  // [tokens], within the tree; -1: the slot's state
+  int32_t max_nodes;       // a tree of more nodes is refused
+  int32_t nt;              // the states take the non-temporal hint
+};
+
+struct PathArgs {
+  SlotArgs s;              // q and o are not used
+  const int32_t* path;     // [seqs][depth], nodes within the tree
+  const int32_t* lengths;  // [seqs]
+  int32_t depth;
+  int32_t nt;
+};
+
+constexpr int kMaxVocab = 1 << 22;
+
+struct VerifyArgs {
+  const float* target;     // [nodes] rows target_stride elements apart
+  const float* draft;      // rows draft_stride apart, or null: one-hot drafts
+  const int32_t* ids;      // [nodes]
+  const int32_t* parents;  // [nodes]
+  const int32_t* cu;       // [seqs + 1]
+  const float* uniform;    // [nodes]
+  const float* uniform_next;   // [seqs]
+  int32_t* path;           // [seqs][depth]
+  int32_t* lengths;        // [seqs]
+  int32_t* next;           // [seqs]
+  int64_t target_stride, draft_stride, nodes;
+  int32_t seqs, vocab, depth, replacement;
+};
+
+hipError_t launch_tree(const TreeArgs& a, int io, int dk, int delta, int diag, hipStream_t s);
+hipError_t launch_path(const PathArgs& a, int io, int dk, int delta, int diag, hipStream_t s);
+hipError_t launch_verify(const VerifyArgs& a, hipStream_t s);
 hipError_t launch_walk(const SlotArgs& a, int io, int dk, int delta, int diag, int nt, hipStream_t s);
 hipError_t launch_attend(const AttendArgs& a, int io, int dk, hipStream_t s);
 hipError_t launch_store_slots(const CopyArgs& a, int bits, int dk, hipStream_t s);

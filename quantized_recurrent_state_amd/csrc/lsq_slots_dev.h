@@ -69,6 +69,24 @@ __device__ __forceinline__ void store1(void* p, int64_t e, float x) {
     static_cast<uint16_t*>(p)[e] = to16<IO>(x);
 }
 
+// The state's rows.  NT: with the non-temporal hint, for a state that does not
+// stay in the last-level cache between steps.
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+template <bool NT>
+__device__ __forceinline__ f32x4 load_state(const float* p) {
+  if constexpr (NT) return __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(p));
+  return *reinterpret_cast<const f32x4*>(p);
+}
+
+template <bool NT>
+__device__ __forceinline__ void store_state(float* p, f32x4 x) {
+  if constexpr (NT)
+    __builtin_nontemporal_store(x, reinterpret_cast<f32x4*>(p));
+  else
+    *reinterpret_cast<f32x4*>(p) = x;
+}
+
 constexpr int kPadded = -1, kRefused = -2;
 
 // Entry i's slot: the slot itself, kPadded for a negative one, kRefused for

@@ -64,22 +64,23 @@ def _rows(name, t, shape, dtype, index):
     return t.data_ptr(), row
 
 
-def token_batch(state, q, k, v, alpha, beta, cu_seqlens, slots, fresh, o):
-    """Checks a token batch's tensors; returns (lsq_token_batch, o)."""
+def token_batch(state, q, k, v, alpha, beta, cu_seqlens, slots, fresh, o, outputs=True):
+    """Checks a token batch's tensors; returns (lsq_token_batch, o).  outputs False: without q and o."""
     c = state.cfg
     if c.bits != 32:
         raise ValueError("token batches run on an fp32 state (bits 32)")
-    dev, dtype = state.f32.get_device(), q.dtype
+    first, name = (q, "q") if outputs else (k, "k")
+    dev, dtype = state.f32.get_device(), first.dtype
     io = _IO.get(dtype)
     if io is None:
-        raise ValueError(f"q has type {dtype}, expected float32, float16 or bfloat16")
-    if q.dim() != 3:
-        raise ValueError(f"q has shape {tuple(q.shape)}, expected (tokens, qk_heads, {c.dk})")
-    n, hk, _ = q.shape
+        raise ValueError(f"{name} has type {dtype}, expected float32, float16 or bfloat16")
+    if first.dim() != 3:
+        raise ValueError(f"{name} has shape {tuple(first.shape)}, expected (tokens, qk_heads, {c.dk})")
+    n, hk, _ = first.shape
     heads, dk, dv = c.heads, c.dk, c.dv
     if hk == 0 or heads % hk:
-        raise ValueError(f"q has {hk} heads, which must divide the state's {heads}")
-    qp, sq = _rows("q", q, (n, hk, dk), dtype, dev)
+        raise ValueError(f"{name} has {hk} heads, which must divide the state's {heads}")
+    qp, sq = _rows("q", q, (n, hk, dk), dtype, dev) if outputs else (None, 0)
     kp, sk = _rows("k", k, (n, hk, dk), dtype, dev)
     vp, sv = _rows("v", v, (n, heads, dv), dtype, dev)
     ap = _plain("alpha", alpha, (n, heads, dk) if c.decay == DECAY_DIAG else (n, heads), torch.float32, dev)
@@ -94,7 +95,9 @@ def token_batch(state, q, k, v, alpha, beta, cu_seqlens, slots, fresh, o):
         sp = _plain("slots", slots, (m,), torch.int32, dev)
     if fresh is not None:
         fp = _plain("fresh", fresh, (m,), torch.bool if fresh.dtype is torch.bool else torch.uint8, dev)
-    if o is None:
+    if not outputs:
+        op, so = None, 0
+    elif o is None:
         o = torch.empty((n, heads, dv), dtype=dtype, device=state.f32.device)
         op, so = o.data_ptr(), heads * dv
     else:
