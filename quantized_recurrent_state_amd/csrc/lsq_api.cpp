@@ -679,8 +679,11 @@ lsq_status lsq_step_tree(const lsq_state* st, const lsq_token_batch* batch, cons
   if (s != LSQ_OK) return s;
   const lsq_config& c = st->cfg;
   const lsq::TreeArgs a{slot_args(st, batch), parents, max_nodes, past_cache(c, batch->seqs)};
-  return slot_status(lsq::launch_tree(a, batch->io, c.dk, c.delta, c.decay == LSQ_DECAY_DIAG,
-                                      static_cast<hipStream_t>(stream)), "step_tree launch");
+  const auto launch = batch->io == LSQ_IO_F32   ? lsq::launch_tree_f32
+                      : batch->io == LSQ_IO_F16 ? lsq::launch_tree_f16
+                                                : lsq::launch_tree_bf16;
+  return slot_status(launch(a, c.dk, c.delta, c.decay == LSQ_DECAY_DIAG, static_cast<hipStream_t>(stream)),
+                     "step_tree launch");
 }
 
 lsq_status lsq_accept_path(lsq_state* st, const lsq_token_batch* batch, const int32_t* path,

@@ -1,5 +1,4 @@
-// Drafted tokens over the slots of an fp32 handle: the recurrence along every
-// path of a tree, and an accepted path written into the state.
+// Accepted paths of drafted tokens written into the slots of an fp32 handle.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -80,85 +79,6 @@ __device__ __forceinline__ void load_rows(float (&s)[R][DK / 16], const float* S
   }
 }
 
-// Nodes on the way from each lane's node to its root, itself included, as a bit
-// mask, from the lanes' parents (-1 above a root): by pointer doubling, six
-// rounds for any tree of 64 nodes.
-__device__ __forceinline__ uint64_t path_mask(int parent, int lane) {
-  uint64_t mask = (uint64_t)1 << lane;
-  int up = parent;
-#pragma unroll
-  for (int r = 0; r < 6; ++r) {
-    const int at = up < 0 ? lane : up;
-    const uint32_t lo = __shfl((int)(uint32_t)mask, at), hi = __shfl((int)(uint32_t)(mask >> 32), at);
-    const int next = __shfl(up, at);
-    mask |= (uint64_t)hi << 32 | lo;
-    if (up >= 0) up = next;
-  }
-  return mask;
-}
-
-// Tree of one entry.  A wave holds its rows of the slot's state and walks every
-// node's path from it.
-template <int IO, int DK, int DELTA, int DIAG, int R>
-__global__ __launch_bounds__(256) void tree_kernel(TreeArgs a, int row_blocks) {
-  constexpr int NJ = DK / 64, EPT = DK / 16;
-  const int lane = threadIdx.x & 63, lr = lane >> 4, lc = lane & 15;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const SlotArgs& b = a.s;
-  const int rb = blockIdx.x % row_blocks;
-  const int64_t ih = blockIdx.x / row_blocks;
-  const int h = (int)(ih % b.heads), i = (int)(ih / b.heads);
-  const int row0 = (rb * 4 + wave) * 4 * R;
-  if (row0 >= b.dv) return;
-  const Span sp = span_of(b, i);
-  if (sp.t1 <= sp.t0) return;
-  const int slot = b.slots ? __builtin_amdgcn_readfirstlane(b.slots[i]) : i;
-  if (slot < 0) return;
-  const int64_t n = sp.t1 - sp.t0;
-  const int parent = lane < n ? a.parents[sp.t0 + lane] : -1;
-  const int orow = row0 + 4 * lc + lr;          // the row whose output this lane stores
-  const bool owrite = lc < R && orow < b.dv;
-  if (slot >= b.nslots || n > a.max_nodes || __any(parent < -1 || parent >= lane)) {
-    if (owrite)
-      for (int64_t t = sp.t0; t < sp.t1; ++t)
-        store1<IO>(b.o, t * b.o_stride + (int64_t)h * b.dv + orow, __uint_as_float(0x7FC00000u));
-    return;
-  }
-  const uint64_t mask = path_mask(parent, lane);
-  float s0[R][EPT];
-  load_rows<DK, R, false>(s0, b.S + ((int64_t)slot * b.heads + h) * b.dv * DK, row0, b.dv,
-                          b.fresh && b.fresh[i], lr, lc);
-  for (int j = 0; j < n; ++j) {
-    uint64_t on = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)mask, j) |
-                  (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(mask >> 32), j) << 32;
-    float s[R][EPT];
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-#pragma unroll
-      for (int e = 0; e < EPT; ++e) s[r][e] = s0[r][e];
-    while (on) {
-      const int at = __builtin_ctzll(on);
-      on &= on - 1;
-      Node<IO, DK, DIAG, R> x;
-      x.read(b, sp.t0 + at, h, row0, lr, lc);
-      x.template advance<DELTA>(s);
-    }
-    float qq[EPT], out = 0.f;
-#pragma unroll
-    for (int c = 0; c < NJ; ++c)
-      widen4<IO>(&qq[4 * c], raw4<IO>(b.q, (sp.t0 + j) * b.q_stride + (int64_t)(h / b.share) * DK + 64 * c + 4 * lc));
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      float o = 0.f;
-#pragma unroll
-      for (int e = 0; e < EPT; ++e) o = fmaf(s[r][e], qq[e], o);
-      o = row_sum<16>(o);
-      if (lc == r) out = o;
-    }
-    if (owrite) store1<IO>(b.o, (sp.t0 + j) * b.o_stride + (int64_t)h * b.dv + orow, out);
-  }
-}
-
 // An entry's path: node numbers in the lanes, the slot it takes (kPadded for an
 // entry with nothing to do).  One with a length of zero or less does nothing and takes no
 // slot; one with more nodes than depth or a node outside its tree is refused.
@@ -234,16 +154,6 @@ namespace {
 constexpr int kRows = 4;                         // rows a lane
 
 template <int IO, int DK, int DELTA, int DIAG>
-hipError_t launch_tree_instance(const TreeArgs& a, hipStream_t s) {
-  const int row_blocks = (a.s.dv + 16 * kRows - 1) / (16 * kRows);
-  const int64_t blocks = (int64_t)a.s.seqs * a.s.heads * row_blocks;
-  if (!fits_launch(blocks, 256)) return hipErrorInvalidConfiguration;
-  hipLaunchKernelGGL((dev::tree_kernel<IO, DK, DELTA, DIAG, kRows>), dim3((unsigned)blocks), dim3(256), 0, s, a,
-                     row_blocks);
-  return hipGetLastError();
-}
-
-template <int IO, int DK, int DELTA, int DIAG>
 hipError_t launch_path_instance(const PathArgs& a, hipStream_t s) {
   const int row_blocks = (a.s.dv + 16 * kRows - 1) / (16 * kRows);
   const int64_t blocks = (int64_t)a.s.seqs * a.s.heads * row_blocks;
@@ -254,42 +164,18 @@ hipError_t launch_path_instance(const PathArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-// f.template operator()<IO, DK, DELTA, DIAG>() of the run-time choice.
-template <int IO, int DK, typename F>
-hipError_t by_rule(int delta, int diag, F f) {
-  if (delta) return diag ? f.template operator()<IO, DK, 1, 1>() : f.template operator()<IO, DK, 1, 0>();
-  return diag ? f.template operator()<IO, DK, 0, 1>() : f.template operator()<IO, DK, 0, 0>();
+template <int IO, int DK>
+hipError_t launch_path_rule(const PathArgs& a, int delta, int diag, hipStream_t s) {
+  if (delta) return diag ? launch_path_instance<IO, DK, 1, 1>(a, s) : launch_path_instance<IO, DK, 1, 0>(a, s);
+  return diag ? launch_path_instance<IO, DK, 0, 1>(a, s) : launch_path_instance<IO, DK, 0, 0>(a, s);
 }
-
-template <typename F>
-hipError_t by_type(int io, int dk, int delta, int diag, F f) {
-  if (io == IO_F32) return dk == 128 ? by_rule<IO_F32, 128>(delta, diag, f) : by_rule<IO_F32, 64>(delta, diag, f);
-  if (io == IO_F16) return dk == 128 ? by_rule<IO_F16, 128>(delta, diag, f) : by_rule<IO_F16, 64>(delta, diag, f);
-  return dk == 128 ? by_rule<IO_BF16, 128>(delta, diag, f) : by_rule<IO_BF16, 64>(delta, diag, f);
-}
-
-struct TreeLaunch {
-  const TreeArgs& a;
-  hipStream_t s;
-  template <int IO, int DK, int DELTA, int DIAG>
-  hipError_t operator()() const { return launch_tree_instance<IO, DK, DELTA, DIAG>(a, s); }
-};
-
-struct PathLaunch {
-  const PathArgs& a;
-  hipStream_t s;
-  template <int IO, int DK, int DELTA, int DIAG>
-  hipError_t operator()() const { return launch_path_instance<IO, DK, DELTA, DIAG>(a, s); }
-};
 
 }  // namespace
 
-hipError_t launch_tree(const TreeArgs& a, int io, int dk, int delta, int diag, hipStream_t s) {
-  return by_type(io, dk, delta, diag, TreeLaunch{a, s});
-}
-
 hipError_t launch_path(const PathArgs& a, int io, int dk, int delta, int diag, hipStream_t s) {
-  return by_type(io, dk, delta, diag, PathLaunch{a, s});
+  if (io == IO_F32) return dk == 128 ? launch_path_rule<IO_F32, 128>(a, delta, diag, s) : launch_path_rule<IO_F32, 64>(a, delta, diag, s);
+  if (io == IO_F16) return dk == 128 ? launch_path_rule<IO_F16, 128>(a, delta, diag, s) : launch_path_rule<IO_F16, 64>(a, delta, diag, s);
+  return dk == 128 ? launch_path_rule<IO_BF16, 128>(a, delta, diag, s) : launch_path_rule<IO_BF16, 64>(a, delta, diag, s);
 }
 
 }  // namespace lsq

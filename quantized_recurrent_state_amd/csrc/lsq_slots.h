@@ -1,5 +1,5 @@
 // Interface between the host API (lsq_api.cpp) and the slot kernels
-// (lsq_slots.hip, lsq_attend.hip, lsq_tree.hip, lsq_verify.hip).  Not installed.
+// (lsq_slots.hip, lsq_attend.hip, lsq_tree_*.hip, lsq_path.hip, lsq_verify.hip).  Not installed.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -98,7 +98,9 @@ struct VerifyArgs {
   int32_t seqs, vocab, depth, replacement;
 };
 
-hipError_t launch_tree(const TreeArgs& a, int io, int dk, int delta, int diag, hipStream_t s);
+hipError_t launch_tree_f32(const TreeArgs& a, int dk, int delta, int diag, hipStream_t s);
+hipError_t launch_tree_f16(const TreeArgs& a, int dk, int delta, int diag, hipStream_t s);
+hipError_t launch_tree_bf16(const TreeArgs& a, int dk, int delta, int diag, hipStream_t s);
 hipError_t launch_path(const PathArgs& a, int io, int dk, int delta, int diag, hipStream_t s);
 hipError_t launch_verify(const VerifyArgs& a, hipStream_t s);
 hipError_t launch_walk(const SlotArgs& a, int io, int dk, int delta, int diag, int nt, hipStream_t s);

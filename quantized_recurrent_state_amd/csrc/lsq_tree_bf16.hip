@@ -1,0 +1,10 @@
+// Instances of the tree kernel for bfloat16 inputs.
+#include "lsq_tree_impl.h"
+
+namespace lsq {
+
+hipError_t launch_tree_bf16(const TreeArgs& a, int dk, int delta, int diag, hipStream_t s) {
+  return launch_tree_type<IO_BF16>(a, dk, delta, diag, s);
+}
+
+}  // namespace lsq
