@@ -678,7 +678,13 @@ lsq_status lsq_step_tree(const lsq_state* st, const lsq_token_batch* batch, cons
   s = check_batch_ptrs(st, batch);
   if (s != LSQ_OK) return s;
   const lsq_config& c = st->cfg;
-  const lsq::TreeArgs a{slot_args(st, batch), parents, max_nodes, past_cache(c, batch->seqs)};
+  const size_t e = io_bytes(batch->io);
+  for (const int64_t x : {batch->q_stride, batch->k_stride, batch->v_stride, batch->o_stride})
+    if (x > INT32_MAX)                           // offsets within a tree are products of 32 bits
+      return fail(LSQ_ERR_UNSUPPORTED, "a token stride of 2^31 elements or more");
+  const bool wide = aligned16(batch->v) && aligned16(batch->o) && batch->v_stride * e % 16 == 0 &&
+                    batch->o_stride * e % 16 == 0 && c.dv * e % 16 == 0;
+  const lsq::TreeArgs a{slot_args(st, batch), parents, max_nodes, past_cache(c, batch->seqs), wide};
   const auto launch = batch->io == LSQ_IO_F32   ? lsq::launch_tree_f32
                       : batch->io == LSQ_IO_F16 ? lsq::launch_tree_f16
                                                 : lsq::launch_tree_bf16;

@@ -71,6 +71,7 @@ struct TreeArgs {
   const int32_t* parents;  // [tokens], within the tree; -1: the slot's state
   int32_t max_nodes;       // a tree of more nodes is refused
   int32_t nt;              // the states take the non-temporal hint
+  int32_t wide;            // rows of v and o are whole 16-byte units
 };
 
 struct PathArgs {
