@@ -66,27 +66,42 @@ struct TreeTile {
   static constexpr int IN = IO == IO_BF16 ? 1 : IO == IO_F16 ? 2 : 3;   // parts of an input
   static constexpr int NO = IO == IO_F32 ? 3 : 2;                       // parts of what is computed
   static constexpr int NR = DIAG ? NO : IN;                             // parts of the node rows
-  static constexpr int N = 16 * NT, W = NT == 1 ? 32 : N;               // nodes; columns of P and M as parts
+  static constexpr int N = 16 * NT, W = (N + 31) / 32 * 32;             // nodes; columns of P and M as parts
   // Pitches in elements: node rows, P and M as parts and as fp32, T, rows of the walk.
   static constexpr int PK = DK + 16, PW = W + 16, PP = N + 4, PT = 20, PR = DK + 4;
   static constexpr int EU = IO == IO_F32 ? 4 : 8;                       // elements of a 16-byte unit
   static constexpr int UNITS = (N * DK / EU + 64 * NW - 1) / (64 * NW); // units of q (k) per thread
+  static constexpr int ROUNDS = (4 * NT + NW - 1) / NW;                 // nodes a lane group walks up from
+  // Tiles of P, with the zeros behind the diagonal in a pair of them, and of M behind
+  // the first row of tiles.
+  static constexpr int PTILES = NT == 1 ? 2 : NT == 2 ? 4 : NT == 3 ? 8 : 12;
+  static constexpr int MTILES = !DELTA || NT == 1 ? 0 : NT == 2 ? 2 : NT == 3 ? 4 : 8;
+  static constexpr int TASKS = (PTILES + MTILES + NW - 1) / NW;
   // 16-bit rows of v come, and of o go, through LDS: value columns of all waves, whole
   // 128-byte lines instead of 32-byte pieces.
   static constexpr bool STAGED = IO != IO_F32;
   static constexpr int C = 16 * NW, PC = C + 8, VUNITS = (N * C / 8 + 64 * NW - 1) / (64 * NW);
-  static constexpr int ROUNDS = (4 * NT + NW - 1) / NW;                 // nodes a lane group walks up from
-  static constexpr int PTILES = NT == 1 ? 2 : NT == 2 ? 4 : 12;         // tiles of P, with the zeros of a pair
-  static constexpr int MTILES = !DELTA || NT == 1 ? 0 : NT == 2 ? 2 : 8;   // of M behind the first row of tiles
-  static constexpr int TASKS = (PTILES + MTILES + NW - 1) / NW;
-  // P and M as parts take the place of the node rows once the products with S are done.
-  static constexpr bool OVERLAY = NT > 1;
-  static constexpr int ROWS = 2 * NR * N * PK * (DIAG && !DELTA ? 1 : 2);   // bytes
-  static constexpr int PARTS = DIAG ? 0 : 2 * NO * N * PW * (MTILES ? 2 : 1);
-  static constexpr int RAW = DIAG ? 8 * N * PR : 0;
+  // LDS, in bytes.  P and M as parts, and the rows of v, take the place of the node
+  // rows once the products with S are done; one tile's have room beside them.
+  static constexpr bool OVERLAY = NT > 1 && !DIAG;
   static constexpr int max2(int x, int y) { return x > y ? x : y; }
-  static constexpr int SHARED = max2(max2(ROWS + (OVERLAY ? 0 : PARTS), PARTS), RAW);
-  static constexpr int BLOCKS = DIAG ? 4 * N * PP : 64 * NT * PT;       // bytes of M's (and P's) fp32 values
+  static constexpr int ROWS = 2 * NR * N * PK * (DIAG && !DELTA ? 1 : 2);
+  static constexpr int PARTS = DIAG ? 0 : 2 * NO * N * PW * (MTILES ? 2 : 1);
+  static constexpr int VROWS = STAGED ? 2 * N * PC : 0;
+  static constexpr int RAW = DIAG ? 8 * N * PR : 0;
+  static constexpr int PARTS_AT = OVERLAY ? 0 : ROWS, VROWS_AT = PARTS_AT + (DIAG ? max2(0, RAW - ROWS) : PARTS);
+  static constexpr int P_AT = max2(max2(ROWS, RAW), VROWS_AT + VROWS);  // P in fp32
+  static constexpr int M_AT = P_AT + (DIAG ? 4 * N * PP : 0);           // M in fp32, or its diagonal blocks
+  static constexpr int T_AT = M_AT + (!DELTA ? 0 : DIAG ? 4 * N * PP : 64 * NT * PT);
+  static constexpr int BYTES = T_AT + (DELTA ? 2 * NO * N * PT : 0);
+};
+
+// What all waves of a workgroup know of the nodes.
+struct TreeNodes {
+  float hi[64], lo[64], g[64], beta[64];         // L, 2^L with its sign, beta
+  uint32_t on[2][64];                            // the paths, by 32 nodes
+  uint64_t neg;                                  // nodes with a negative decay
+  unsigned long long spoilt;                     // whose row of T is not finite
 };
 
 template <int N, int NA, int NB>
@@ -119,55 +134,29 @@ __device__ __forceinline__ void get8(const __bf16* src, int plane, bf16x8 (&out)
   for (int y = 0; y < P; ++y) out[y] = *reinterpret_cast<const bf16x8*>(src + y * plane);
 }
 
+// One head of a tree of up to 16 NT nodes, more than 16 (NT - 1).
 template <int IO, int DK, int DELTA, int DIAG, int NT, int NW>
-__global__ __launch_bounds__(64 * NW, 2) void tree_kernel(TreeArgs a, int row_blocks) {
+__device__ __forceinline__ void tree_head(const TreeArgs& a, char* lds, TreeNodes& nl, int i, int h, int rb, int slot,
+                                          int64_t t0, int n) {
   using T = TreeTile<IO, DK, DELTA, DIAG, NT, NW>;
   constexpr int N = T::N, PK = T::PK, PP = T::PP, PW = T::PW, PT = T::PT, PR = T::PR, KS = DK / 32, NO = T::NO, NR = T::NR;
-  constexpr int kRow = N * PK, kPart = N * PW, kT = NT * 16 * PT;      // planes
-  __shared__ __align__(16) char shared[T::SHARED];
-  __shared__ __align__(16) float pl[DIAG ? N * PP : 4];                // P in fp32
-  __shared__ __align__(16) float ml[DELTA ? T::BLOCKS / 4 : 4];        // M in fp32, or its diagonal blocks
-  __shared__ __align__(16) __bf16 tl[DELTA ? NO * kT : 8];
-  __shared__ __align__(16) float hil[64], lol[64], gl[64], bl[64];
-  __shared__ __align__(16) uint32_t onl[2][64];                        // the paths, by 32 nodes
-  __shared__ uint64_t negl;
-  __shared__ __align__(16) uint16_t vl[T::STAGED ? N * T::PC : 8];
-  __shared__ unsigned long long spoiltl;
-  __bf16* const ql = reinterpret_cast<__bf16*>(shared);
+  constexpr int kRow = N * PK, kPart = N * PW, kT = N * PT;            // planes
+  __bf16* const ql = reinterpret_cast<__bf16*>(lds);
   __bf16* const kl = ql + NR * kRow;
-  __bf16* const pp = T::OVERLAY ? ql : kl + NR * kRow;                 // P, then M, as parts
+  __bf16* const pp = reinterpret_cast<__bf16*>(lds + T::PARTS_AT);     // P, then M, as parts
   __bf16* const mp = pp + NO * kPart;
+  uint16_t* const vl = reinterpret_cast<uint16_t*>(lds + T::VROWS_AT);
+  float* const pl = reinterpret_cast<float*>(lds + T::P_AT);
+  float* const ml = reinterpret_cast<float*>(lds + T::M_AT);
+  __bf16* const tl = reinterpret_cast<__bf16*>(lds + T::T_AT);
 
   const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, lc = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const SlotArgs& b = a.s;
-  // Blocks go to the eight XCDs in turn; where a tree's blocks divide by eight, an
-  // XCD takes neighbouring heads, which share rows of q and k in its L2.
-  const int blocks = b.heads * row_blocks;
-  int i, part;
-  if (blocks % 8 == 0) {
-    const int own = blocks / 8, x = blockIdx.x / 8;
-    i = x / own;
-    part = (int)(blockIdx.x % 8) * own + x % own;
-  } else {
-    i = blockIdx.x / blocks;
-    part = blockIdx.x % blocks;
-  }
-  const int h = part / row_blocks, rb = part % row_blocks;
-  const Span sp = span_of(b, i);
-  if (sp.t1 <= sp.t0) return;
-  const int slot = b.slots ? __builtin_amdgcn_readfirstlane(b.slots[i]) : i;
-  if (slot < 0) return;
-  const int64_t t0 = sp.t0, nodes = sp.t1 - sp.t0;
   const int row0 = (rb * NW + wave) * 16, row = row0 + lc;   // the lane's value column
   const int rowc = row < b.dv ? row : b.dv - 1;
-  const int64_t hv = (int64_t)h * b.dv, hk = (int64_t)(h / b.share) * DK;
-  if (slot >= b.nslots || nodes > a.max_nodes) {
-    if (row < b.dv)
-      for (int64_t t = t0 + g; t < sp.t1; t += 4) store1<IO>(b.o, t * b.o_stride + hv + row, __uint_as_float(0x7FC00000u));
-    return;
-  }
-  const int n = (int)nodes, tiles = (n + 15) / 16;
+  const int hk = h / b.share * DK;
+  const int64_t hv = (int64_t)h * b.dv;
   // Element offset of node j's row; rows behind the last repeat it.
   auto at_node = [&](int j, int64_t stride) { return (uint64_t)(uint32_t)(j < n ? j : n - 1) * (uint32_t)stride; };
   auto behind = [](const void* p, int64_t e) { return static_cast<const typename Raw<IO>::One*>(p) + e; };
@@ -179,7 +168,7 @@ __global__ __launch_bounds__(64 * NW, 2) void tree_kernel(TreeArgs a, int row_bl
   // ---- loads: node rows first, as they are used first
   int parent = lane < n ? a.parents[t0 + lane] : -1;
   constexpr int EU = T::EU, ROWU = DK / EU;      // units of a row
-  auto unit_in = [&](int x) { return x * 64 * NW / ROWU < 16 * tiles && (N * ROWU % (64 * NW) == 0 || x * 64 * NW + tid < N * ROWU); };
+  auto unit_in = [&](int x) { return (x + 1) * 64 * NW <= N * ROWU || x * 64 * NW + tid < N * ROWU; };
   u32x4 rq[DIAG ? 1 : T::UNITS], rk[T::UNITS];
   float4 rd[DIAG ? T::UNITS : 1][EU / 4];
 #pragma unroll
@@ -220,24 +209,29 @@ __global__ __launch_bounds__(64 * NW, 2) void tree_kernel(TreeArgs a, int row_bl
       for (int y = 0; y < 2; ++y)
         s[kk][y] = a.nt ? load_state<true>(S + 32 * kk + 16 * y) : load_state<false>(S + 32 * kk + 16 * y);
   }
-  typename Raw<IO>::One rv[NT][4];               // this lane's, or units of all columns
-  u32x4 ru[T::STAGED ? T::VUNITS : 1];
-  const bool staged = T::STAGED && a.wide;
+  typename Raw<IO>::One rv[T::STAGED ? 1 : NT][4];           // this lane's, or units of all columns
+  u32x4 rvu[T::STAGED ? T::VUNITS : 1];
   const int col0 = rb * T::C;                    // the workgroup's first value column
-  if (staged) {
+  auto v_in = [&](int x) { return (x + 1) * 64 * NW <= N * (T::C / 8) || x * 64 * NW + tid < N * (T::C / 8); };
+  if constexpr (T::STAGED) {
 #pragma unroll
-    for (int x = 0; x < (T::STAGED ? T::VUNITS : 0); ++x) {
+    for (int x = 0; x < T::VUNITS; ++x) {
       const int u = x * 64 * NW + tid, j = u / (T::C / 8), c = col0 + u % (T::C / 8) * 8;
-      if (j < 16 * tiles)
-        ru[x] = *reinterpret_cast<const u32x4*>(vb + at_node(j, b.v_stride) + (c < b.dv ? c : 0));
+      if (!v_in(x)) continue;
+      const auto* from = vb + at_node(j, b.v_stride);
+      if (a.wide) {
+        rvu[x] = *reinterpret_cast<const u32x4*>(from + (c < b.dv ? c : 0));
+      } else {
+#pragma unroll
+        for (int y = 0; y < 4; ++y)
+          rvu[x][y] = from[min(c + 2 * y, b.dv - 1)] | (uint32_t)from[min(c + 2 * y + 1, b.dv - 1)] << 16;
+      }
     }
   } else {
 #pragma unroll
     for (int t = 0; t < NT; ++t)
-      if (t < tiles) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) rv[t][r] = vb[at_node(16 * t + 4 * g + r, b.v_stride) + rowc];
-      }
+      for (int r = 0; r < 4; ++r) rv[t][r] = vb[at_node(16 * t + 4 * g + r, b.v_stride) + rowc];
   }
 
   // ---- paths and decays.  A tree with a parent that is no earlier node is worked
@@ -251,15 +245,15 @@ __global__ __launch_bounds__(64 * NW, 2) void tree_kernel(TreeArgs a, int row_bl
     if constexpr (!DIAG) {
       const uint64_t neg = __ballot(lane < n && ra < 0.f);
       const float hi = (float)l;
-      hil[lane] = hi;
-      lol[lane] = (float)(l - (double)hi);
-      gl[lane] = exp2_of(l) * (__popcll(neg & mask) & 1 ? -1.f : 1.f);
-      if (lane == 0) negl = neg;
+      nl.hi[lane] = hi;
+      nl.lo[lane] = (float)(l - (double)hi);
+      nl.g[lane] = exp2_of(l) * (__popcll(neg & mask) & 1 ? -1.f : 1.f);
+      if (lane == 0) nl.neg = neg;
     }
-    bl[lane] = lane < n ? rbeta : 0.f;
-    onl[0][lane] = (uint32_t)mask;
-    onl[1][lane] = (uint32_t)(mask >> 32);
-    if (lane == 0) spoiltl = 0;
+    nl.beta[lane] = lane < n ? rbeta : 0.f;
+    nl.on[0][lane] = (uint32_t)mask;
+    nl.on[1][lane] = (uint32_t)(mask >> 32);
+    if (lane == 0) nl.spoilt = 0;
   }
 
   // A tile of S's products' decayed cousins: rows tj of P (or M) at columns ti.
@@ -273,16 +267,16 @@ __global__ __launch_bounds__(64 * NW, 2) void tree_kernel(TreeArgs a, int row_bl
       d = mfma_parts<NO>(x, y, d);
     }
     const int col = 16 * ti + lc, j0 = 16 * tj + 4 * g;
-    const float hc = hil[col], lo = lol[col];
-    const f32x4 hj = *reinterpret_cast<const f32x4*>(&hil[j0]), lj = *reinterpret_cast<const f32x4*>(&lol[j0]);
-    const u32x4 on = *reinterpret_cast<const u32x4*>(&onl[ti >> 1][j0]);
-    const uint64_t neg = negl;
+    const float hc = nl.hi[col], lo = nl.lo[col];
+    const f32x4 hj = *reinterpret_cast<const f32x4*>(&nl.hi[j0]), lj = *reinterpret_cast<const f32x4*>(&nl.lo[j0]);
+    const u32x4 on = *reinterpret_cast<const u32x4*>(&nl.on[ti >> 1][j0]);
+    const uint64_t neg = nl.neg;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       float x = __builtin_amdgcn_exp2f((hj[r] - hc) + (lj[r] - lo)) * d[r];
       if (neg) {
-        const uint32_t n0 = (uint32_t)neg & (onl[0][j0 + r] ^ onl[0][col]);
-        const uint32_t n1 = (uint32_t)(neg >> 32) & (onl[1][j0 + r] ^ onl[1][col]);
+        const uint32_t n0 = (uint32_t)neg & (nl.on[0][j0 + r] ^ nl.on[0][col]);
+        const uint32_t n1 = (uint32_t)(neg >> 32) & (nl.on[1][j0 + r] ^ nl.on[1][col]);
         x = (__popc(n0) + __popc(n1)) & 1 ? -x : x;
       }
       d[r] = on[r] >> (col & 31) & 1 ? x : 0.f;
@@ -290,14 +284,15 @@ __global__ __launch_bounds__(64 * NW, 2) void tree_kernel(TreeArgs a, int row_bl
     return d;
   };
   // T of tile t from M's block there: column lc by forward substitution in every
-  // lane group, which writes its four rows.
+  // lane group, which writes its four rows.  Rows behind the last node stay the
+  // identity's; the second half is left out where it holds none.
   auto invert = [&](int t, const float* m, int pitch) {
     float x[16];
     uint32_t odd = 0;
+    auto rows = [&](auto from) {
 #pragma unroll
-    for (int r = 0; r < 16; ++r) {
-      x[r] = lc == r ? 1.f : 0.f;
-      if (16 * t + r < n && r > 0) {
+      for (int r = decltype(from)::value; r < decltype(from)::value + 8; ++r) {
+        x[r] = lc == r ? 1.f : 0.f;
         float d = 0.f;
 #pragma unroll
         for (int c = 0; c < r; c += 4) {
@@ -306,16 +301,23 @@ __global__ __launch_bounds__(64 * NW, 2) void tree_kernel(TreeArgs a, int row_bl
           for (int e = 0; e < 4; ++e)
             if (c + e < r) d = fmaf(y[e], x[c + e], d);
         }
-        x[r] = fmaf(-bl[16 * t + r], d, x[r]);
+        if (r > 0) x[r] = fmaf(-nl.beta[16 * t + r], d, x[r]);
         const bool fine = fabsf(x[r]) <= 0x1.fffffep127f;
         odd |= fine ? 0u : 1u << r;
         x[r] = fine ? x[r] : 0.f;
       }
+    };
+    rows(std::integral_constant<int, 0>());
+    if (n > 16 * t + 8) {
+      rows(std::integral_constant<int, 8>());
+    } else {
+#pragma unroll
+      for (int r = 8; r < 16; ++r) x[r] = lc == r ? 1.f : 0.f;
     }
     if (__any(odd != 0)) {
 #pragma unroll
       for (int o = 1; o < 16; o *= 2) odd |= __shfl_xor((int)odd, o);
-      if (lane == 0) atomicOr(&spoiltl, (unsigned long long)odd << 16 * t);
+      if (lane == 0) atomicOr(&nl.spoilt, (unsigned long long)odd << 16 * t);
     }
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
@@ -329,7 +331,6 @@ __global__ __launch_bounds__(64 * NW, 2) void tree_kernel(TreeArgs a, int row_bl
       }
     }
   };
-
   // Four of a unit's elements as parts of a node row; as they are for the walk.
   auto four_of = [](u32x4 x, int y) {
     f32x4 z;
@@ -346,11 +347,11 @@ __global__ __launch_bounds__(64 * NW, 2) void tree_kernel(TreeArgs a, int row_bl
     else put4<NR>(to, kRow, four_of(x, y));
   };
   auto put_v = [&] {
-    if (staged) {
+    if constexpr (T::STAGED) {
 #pragma unroll
-      for (int x = 0; x < (T::STAGED ? T::VUNITS : 0); ++x) {
+      for (int x = 0; x < T::VUNITS; ++x) {
         const int u = x * 64 * NW + tid, j = u / (T::C / 8);
-        if (j < 16 * tiles) *reinterpret_cast<u32x4*>(&vl[j * T::PC + u % (T::C / 8) * 8]) = ru[x];
+        if (v_in(x)) *reinterpret_cast<u32x4*>(&vl[j * T::PC + u % (T::C / 8) * 8]) = rvu[x];
       }
     }
   };
@@ -358,13 +359,12 @@ __global__ __launch_bounds__(64 * NW, 2) void tree_kernel(TreeArgs a, int row_bl
   f32x4 done[DIAG ? 1 : T::TASKS];
   // Task x of the tiles of P and M that are kept as parts; false behind the last.
   auto task = [&](int x, int& tj, int& ti, bool& m) {
-    const int np = tiles == 1 ? 2 : tiles == 2 ? 4 : tiles == 3 ? 8 : 12, nm = !DELTA ? 0 : tiles == 1 ? 0 : tiles == 2 ? 2 : tiles == 3 ? 4 : 8;
-    m = x >= np;
+    m = x >= T::PTILES;
     if (m) {
-      x -= np;
+      x -= T::PTILES;
       tj = x < 2 ? 1 : x < 4 ? 2 : 3;
       ti = x - (tj == 1 ? 0 : tj == 2 ? 2 : 4);
-      return x < nm;
+      return x < T::MTILES;
     }
     tj = x < 2 ? 0 : x < 4 ? 1 : x < 8 ? 2 : 3;
     ti = x - (tj == 0 ? 0 : tj == 1 ? 2 : tj == 2 ? 4 : 8);
@@ -407,10 +407,10 @@ __global__ __launch_bounds__(64 * NW, 2) void tree_kernel(TreeArgs a, int row_bl
         }
       }
     }
-    put_v();
+    if constexpr (!T::OVERLAY) put_v();
     __syncthreads();
     if constexpr (DELTA) {
-      if (wave < tiles) {
+      if (wave < NT) {
         const f32x4 d = gram(kl, wave, wave);
         float* m = ml + wave * 16 * PT;
 #pragma unroll
@@ -431,7 +431,7 @@ __global__ __launch_bounds__(64 * NW, 2) void tree_kernel(TreeArgs a, int row_bl
     // what is left of q (and alpha k) on the way is multiplied by the decays passed,
     // and with the k's met makes P and M.
     constexpr int NJ = DK / 64, EPT = DK / 16, R = T::ROUNDS;
-    float* const kw = reinterpret_cast<float*>(shared);
+    float* const kw = reinterpret_cast<float*>(lds);
     float* const aw = kw + N * PR;
 #pragma unroll
     for (int x = 0; x < T::UNITS; ++x) {
@@ -453,7 +453,7 @@ __global__ __launch_bounds__(64 * NW, 2) void tree_kernel(TreeArgs a, int row_bl
       at[t] = j < n ? j : -1;
 #pragma unroll
       for (int c = 0; c < NJ; ++c) widen4<IO>(&q[t][4 * c], wq[t][c]);
-      if (j < 16 * tiles)
+      if (j < N)
         for (int c = 4 * lc; c < 16 * (j / 16 + 1); c += 64) {
           *reinterpret_cast<f32x4*>(&pl[j * PP + c]) = f32x4{0.f, 0.f, 0.f, 0.f};
           if constexpr (DELTA) *reinterpret_cast<f32x4*>(&ml[j * PP + c]) = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -509,7 +509,7 @@ __global__ __launch_bounds__(64 * NW, 2) void tree_kernel(TreeArgs a, int row_bl
 #pragma unroll
     for (int t = 0; t < R; ++t) {
       const int j = 4 * (NW * t + wave) + g;
-      if (j < 16 * tiles) {
+      if (j < N) {
 #pragma unroll
         for (int c = 0; c < NJ; ++c) {
           const int to = j * PK + slot_order(64 * c + 4 * lc);
@@ -520,7 +520,7 @@ __global__ __launch_bounds__(64 * NW, 2) void tree_kernel(TreeArgs a, int row_bl
     }
     __syncthreads();
     if constexpr (DELTA)
-      if (wave < tiles) invert(wave, ml + 16 * wave * PP + 16 * wave, PP);
+      if (wave < NT) invert(wave, ml + 16 * wave * PP + 16 * wave, PP);
   }
 
   // ---- S q and S k
@@ -539,28 +539,28 @@ __global__ __launch_bounds__(64 * NW, 2) void tree_kernel(TreeArgs a, int row_bl
 #pragma unroll
     for (int y = 0; y < NO; ++y) sp8[y] = join(lo[y], hi[y]);
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
-      if (t < tiles) {
-        const int at = (16 * t + lc) * PK + 32 * kk + 8 * g;
-        bf16x8 x[NR];
-        get8<NR>(ql + at, kRow, x);
-        xq[t] = mfma_parts<NO>(x, sp8, xq[t]);
-        if constexpr (DELTA) {
-          get8<NR>(kl + at, kRow, x);
-          xk[t] = mfma_parts<NO>(x, sp8, xk[t]);
-        }
+    for (int t = 0; t < NT; ++t) {
+      const int at = (16 * t + lc) * PK + 32 * kk + 8 * g;
+      bf16x8 x[NR];
+      get8<NR>(ql + at, kRow, x);
+      xq[t] = mfma_parts<NO>(x, sp8, xq[t]);
+      if constexpr (DELTA) {
+        get8<NR>(kl + at, kRow, x);
+        xk[t] = mfma_parts<NO>(x, sp8, xk[t]);
       }
+    }
   }
   if constexpr (!DIAG) {
     if constexpr (T::OVERLAY) {
       __syncthreads();                           // the node rows are done with
       put_done();
+      put_v();
     }
     __syncthreads();
   } else if constexpr (DELTA) {
     __syncthreads();
   }
-  if (!staged && row0 >= b.dv) return;
+  if (!T::STAGED && row0 >= b.dv) return;
 
   // Four values of two tiles (u and u + 1) of a row of P or M as an operand; with
   // fp32 values the second tile counts as 0 where it is not asked for.
@@ -578,107 +578,170 @@ __global__ __launch_bounds__(64 * NW, 2) void tree_kernel(TreeArgs a, int row_bl
   };
 
   // ---- w
-  uint32_t bad = 0;                              // bit 4 t + r: node 16 t + 4 g + r
+  uint32_t bad[2] = {};                          // bit 16 (t % 2) + r of word t / 2: w of node 16 t + 4 g + r is not finite
   bf16x4 w[NT][NO];
 #pragma unroll
-  for (int t = 0; t < NT; ++t)
-    if (t < tiles) {
-      const f32x4 beta = *reinterpret_cast<const f32x4*>(&bl[16 * t + 4 * g]);
-      f32x4 x;
+  for (int t = 0; t < NT; ++t) {
+    const f32x4 beta = *reinterpret_cast<const f32x4*>(&nl.beta[16 * t + 4 * g]);
+    f32x4 x;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        if (staged) rv[t][r] = vl[(16 * t + 4 * g + r) * T::PC + 16 * wave + lc];
-        x[r] = widen<IO>(rv[t][r]);
-      }
-      if constexpr (DELTA) {
-        f32x4 y = xk[t];
-        if constexpr (!DIAG) y *= *reinterpret_cast<const f32x4*>(&gl[16 * t + 4 * g]);
-#pragma unroll
-        for (int u = 0; u < t; u += 2) {
-          bf16x8 m[NO], o[NO];
-          operand(ml, mp, t, u, u + 1 < t, m);
-#pragma unroll
-          for (int p = 0; p < NO; ++p) o[p] = join(w[u][p], u + 1 < t ? w[u + 1 < NT ? u + 1 : u][p] : bf16x4{});
-          y = mfma_parts<NO>(m, o, y);
-        }
-        x -= y;
-      }
-      x *= beta;
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const bool fine = fabsf(x[r]) <= 0x1.fffffep127f;
-        bad |= fine ? 0u : 1u << (4 * t + r);
-        x[r] = fine ? x[r] : 0.f;
-      }
-      split4<NO>(x, w[t]);
-      if constexpr (DELTA) {
-        f32x4 y = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int p = NO - 1; p >= 0; --p) {
-          const bf16x4 m = *reinterpret_cast<const bf16x4*>(tl + p * kT + (16 * t + lc) * PT + 4 * g);
-#pragma unroll
-          for (int o = NO - 1 - p; o >= 0; --o)
-            y = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(__builtin_bit_cast(s16x4, m), __builtin_bit_cast(s16x4, w[t][o]), y, 0, 0, 0);
-        }
-        split4<NO>(y, w[t]);
-      }
+    for (int r = 0; r < 4; ++r) {
+      if constexpr (T::STAGED) x[r] = widen<IO>(vl[(16 * t + 4 * g + r) * T::PC + 16 * wave + lc]);
+      else x[r] = widen<IO>(rv[t][r]);
     }
-
-  // ---- o
-  uint64_t spoilt = 0;                           // nodes of the column whose w is not finite
-  if (__any(bad != 0)) {
+    if constexpr (DELTA) {
+      f32x4 y = xk[t];
+      if constexpr (!DIAG) y *= *reinterpret_cast<const f32x4*>(&nl.g[16 * t + 4 * g]);
 #pragma unroll
-    for (int t = 0; t < NT; ++t) spoilt |= (uint64_t)(bad >> 4 * t & 15) << (16 * t + 4 * g);
+      for (int u = 0; u < t; u += 2) {
+        bf16x8 m[NO], o[NO];
+        operand(ml, mp, t, u, u + 1 < t, m);
 #pragma unroll
-    for (int o = 16; o < 64; o *= 2) {
-      const uint32_t lo = __shfl_xor((int)(uint32_t)spoilt, o), hi = __shfl_xor((int)(uint32_t)(spoilt >> 32), o);
-      spoilt |= (uint64_t)hi << 32 | lo;
+        for (int p = 0; p < NO; ++p) o[p] = join(w[u][p], u + 1 < t ? w[u + 1 < NT ? u + 1 : u][p] : bf16x4{});
+        y = mfma_parts<NO>(m, o, y);
+      }
+      x -= y;
+    }
+    x *= beta;
+    uint32_t odd = 0;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const bool fine = fabsf(x[r]) <= 0x1.fffffep127f;
+      odd |= fine ? 0u : 1u << r;
+      x[r] = fine ? x[r] : 0.f;
+    }
+    bad[t / 2] |= odd << 16 * (t % 2);
+    split4<NO>(x, w[t]);
+    if constexpr (DELTA) {
+      f32x4 y = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int p = NO - 1; p >= 0; --p) {
+        const bf16x4 m = *reinterpret_cast<const bf16x4*>(tl + p * kT + (16 * t + lc) * PT + 4 * g);
+#pragma unroll
+        for (int o = NO - 1 - p; o >= 0; --o)
+          y = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(__builtin_bit_cast(s16x4, m), __builtin_bit_cast(s16x4, w[t][o]), y, 0, 0, 0);
+      }
+      split4<NO>(y, w[t]);
     }
   }
-  if constexpr (DELTA) spoilt |= spoiltl;
-  const bool nans = refused || __any(spoilt != 0);
-  auto* const ob = static_cast<typename Raw<IO>::One*>(b.o) + t0 * b.o_stride + hv;
+
+  // ---- o
 #pragma unroll
-  for (int t = 0; t < NT; ++t)
-    if (t < tiles) {
-      f32x4 o = xq[t];
-      if constexpr (!DIAG) o *= *reinterpret_cast<const f32x4*>(&gl[16 * t + 4 * g]);
+  for (int t = 0; t < NT; ++t) {
+    if constexpr (!DIAG) xq[t] *= *reinterpret_cast<const f32x4*>(&nl.g[16 * t + 4 * g]);
 #pragma unroll
-      for (int u = 0; u <= t; u += 2) {
-        bf16x8 p[NO], x[NO];
-        operand(pl, pp, t, u, u + 1 <= t, p);
+    for (int u = 0; u <= t; u += 2) {
+      bf16x8 p[NO], x[NO];
+      operand(pl, pp, t, u, u + 1 <= t, p);
 #pragma unroll
-        for (int y = 0; y < NO; ++y) x[y] = join(w[u][y], u + 1 <= t ? w[u + 1 < NT ? u + 1 : u][y] : bf16x4{});
-        o = mfma_parts<NO>(p, x, o);
-      }
-      if (nans) {
+      for (int y = 0; y < NO; ++y) x[y] = join(w[u][y], u + 1 <= t ? w[u + 1 < NT ? u + 1 : u][y] : bf16x4{});
+      xq[t] = mfma_parts<NO>(p, x, xq[t]);
+    }
+  }
+  const unsigned long long rows = DELTA ? nl.spoilt : 0;
+  if (refused || rows || __any((bad[0] | bad[1]) != 0)) {      // nodes behind one that is not finite
+    uint32_t lo = bad[0] << 4 * g, hi = bad[1] << 4 * g;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int j = 16 * t + 4 * g + r;
-          const bool hit = refused || ((uint32_t)spoilt & onl[0][j]) != 0 || ((uint32_t)(spoilt >> 32) & onl[1][j]) != 0;
-          o[r] = hit ? __uint_as_float(0x7FC00000u) : o[r];
-        }
-      }
+    for (int o = 16; o < 64; o *= 2) {
+      lo |= __shfl_xor((int)lo, o);
+      hi |= __shfl_xor((int)hi, o);
+    }
+    lo |= (uint32_t)rows;
+    hi |= (uint32_t)(rows >> 32);
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const int j = 16 * t + 4 * g + r;
-        if constexpr (T::STAGED)
-          if (staged) {                          // in v's place: no other wave reads these columns
-            vl[j * T::PC + 16 * wave + lc] = to16<IO>(o[r]);
-            continue;
-          }
-        if (j < n && row < b.dv) store1<IO>(ob, (uint64_t)(uint32_t)j * (uint32_t)b.o_stride + row, o[r]);
+        if (refused || (lo & nl.on[0][j]) != 0 || (hi & nl.on[1][j]) != 0) xq[t][r] = __uint_as_float(0x7FC00000u);
       }
+  }
+  auto* const ob = static_cast<typename Raw<IO>::One*>(b.o) + t0 * b.o_stride + hv;
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int j = 16 * t + 4 * g + r;
+      if constexpr (T::STAGED) vl[j * T::PC + 16 * wave + lc] = to16<IO>(xq[t][r]);   // v's: no other wave reads them
+      else if (j < n && row < b.dv) store1<IO>(ob, (uint64_t)(uint32_t)j * (uint32_t)b.o_stride + row, xq[t][r]);
     }
-  if (staged) {
+  if constexpr (T::STAGED) {
     __syncthreads();
 #pragma unroll
-    for (int x = 0; x < (T::STAGED ? T::VUNITS : 0); ++x) {
+    for (int x = 0; x < T::VUNITS; ++x) {
       const int u = x * 64 * NW + tid, j = u / (T::C / 8), c = u % (T::C / 8) * 8;
-      if (j < n && col0 + c < b.dv)
-        *reinterpret_cast<u32x4*>(ob + (uint64_t)(uint32_t)j * (uint32_t)b.o_stride + col0 + c) =
-            *reinterpret_cast<const u32x4*>(&vl[j * T::PC + c]);
+      if (!v_in(x) || j >= n || col0 + c >= b.dv) continue;
+      auto* to = ob + (uint64_t)(uint32_t)j * (uint32_t)b.o_stride + col0 + c;
+      const u32x4 y = *reinterpret_cast<const u32x4*>(&vl[j * T::PC + c]);
+      if (a.wide) {
+        *reinterpret_cast<u32x4*>(to) = y;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (col0 + c + e < b.dv) to[e] = (uint16_t)(y[e / 2] >> 16 * (e & 1));
+      }
     }
+  }
+}
+
+// Bytes of LDS and the workgroups a CU holds of it, for up to MT tiles of nodes.
+template <int IO, int DK, int DELTA, int DIAG, int MT, int NW>
+struct TreeLds {
+  template <int NT>
+  using T = TreeTile<IO, DK, DELTA, DIAG, NT, NW>;
+  static constexpr int BYTES = T<1>::max2(T<1>::max2(T<1>::BYTES, T<MT >= 2 ? 2 : 1>::BYTES),
+                                          T<1>::max2(T<MT >= 3 ? 3 : 1>::BYTES, T<MT >= 4 ? 4 : 1>::BYTES));
+  // Waves of a SIMD: as many workgroups as LDS holds, and no more than leave the
+  // registers that a wave needs (measured on 256 trees of 8 nodes, 32 heads of
+  // 128x128 in bf16: six waves 108 us, five, which is two workgroups, 130).
+  static constexpr int HELD = 160 * 1024 / (BYTES + (int)sizeof(TreeNodes)) * NW / 4;
+  static constexpr int FEWER = IO == IO_BF16 ? 0 : 1;    // parts take registers too
+  static constexpr int MOST = DK == 128 ? (MT == 1 ? 6 : 5) - FEWER : (MT == 1 ? 7 : 6) - FEWER;
+  static constexpr int WAVES = MT == 4 && MOST > 4 ? (HELD < 4 ? HELD : 4) : HELD < MOST ? HELD : MOST;
+  static_assert(HELD > 0, "one workgroup fits");
+};
+
+template <int IO, int DK, int DELTA, int DIAG, int MT, int NW>
+__global__ __launch_bounds__(64 * NW, (TreeLds<IO, DK, DELTA, DIAG, MT, NW>::WAVES)) void tree_kernel(TreeArgs a, int row_blocks) {
+  __shared__ __align__(16) char lds[TreeLds<IO, DK, DELTA, DIAG, MT, NW>::BYTES];
+  __shared__ __align__(16) TreeNodes nl;
+  const SlotArgs& b = a.s;
+  // Blocks go to the eight XCDs in turn; where a tree's blocks divide by eight, an
+  // XCD takes neighbouring heads, which share rows of q and k in its L2.
+  const int blocks = b.heads * row_blocks;
+  int i, part;
+  if (blocks % 8 == 0) {
+    const int own = blocks / 8, x = blockIdx.x / 8;
+    i = x / own;
+    part = (int)(blockIdx.x % 8) * own + x % own;
+  } else {
+    i = blockIdx.x / blocks;
+    part = blockIdx.x % blocks;
+  }
+  const int h = part / row_blocks, rb = part % row_blocks;
+  const Span sp = span_of(b, i);
+  if (sp.t1 <= sp.t0) return;
+  const int slot = b.slots ? __builtin_amdgcn_readfirstlane(b.slots[i]) : i;
+  if (slot < 0) return;
+  const int64_t nodes = sp.t1 - sp.t0;
+  if (slot >= b.nslots || nodes > a.max_nodes) {
+    const int c = threadIdx.x % (16 * NW), row = rb * 16 * NW + c;
+    if (row < b.dv)
+      for (int64_t t = sp.t0 + threadIdx.x / (16 * NW); t < sp.t1; t += 4)
+        store1<IO>(b.o, t * b.o_stride + (int64_t)h * b.dv + row, __uint_as_float(0x7FC00000u));
+    return;
+  }
+  const int n = (int)nodes;
+  // The tiles are a constant of each branch: with a condition on each of them the
+  // registers of the tiles are copied at every one.
+  auto head = [&](auto t) { tree_head<IO, DK, DELTA, DIAG, decltype(t)::value, NW>(a, lds, nl, i, h, rb, slot, sp.t0, n); };
+  if (MT == 1 || n <= 16) return head(std::integral_constant<int, 1>());
+  if constexpr (MT >= 2) {
+    if (MT == 2 || n <= 32) return head(std::integral_constant<int, 2>());
+  }
+  if constexpr (MT >= 4) {
+    if (n <= 48) return head(std::integral_constant<int, 3>());
+    head(std::integral_constant<int, 4>());
   }
 }
 
