@@ -511,6 +511,11 @@ typedef struct {
   int32_t* next;               /* [seqs], out */
 } lsq_draft_batch;
 
+/* Bytes of workspace lsq_verify_tree needs for this batch (0 for vocabularies of
+ * up to 8192 tokens).  Host only; depends on seqs, nodes, vocab and whether draft
+ * is NULL alone. */
+lsq_status lsq_verify_workspace(const lsq_draft_batch* batch, size_t* bytes);
+
 /* Verification: entry i's walk starts at node 0, which is accepted as it
  * stands, and tests the children x_1, x_2, ... of the node it is at, in order,
  * with p and q the node's target and draft row.  P_1 = p, T_1 = Q_1 = 1, c_1 = 0:
@@ -528,10 +533,14 @@ typedef struct {
  * [0, vocab) is passed over.  Out: path, node 0 first, -1 behind its end; its
  * length; next.  An empty tree, one of more than 64 nodes, and one with a
  * parent outside [-1, j) get the length 0, next -1 and a path of -1; offsets
- * are clamped to [0, nodes].  INVALID_ARG: null arrays, arrays not 4-byte
- * aligned, seqs < 0, nodes < 0, vocab < 1, depth < 1, a negative stride,
- * replacement not 0 or 1; UNSUPPORTED: vocab > 2^22, or 2^22 entries and more. */
-lsq_status lsq_verify_tree(const lsq_draft_batch* batch, void* stream);
+ * are clamped to [0, nodes].  The workspace is device memory, 16-byte aligned,
+ * used by this call alone until the stream has passed it.  INVALID_ARG: null
+ * arrays, arrays not 4-byte aligned, seqs < 0, nodes < 0, vocab < 1, depth < 1,
+ * a negative stride, replacement not 0 or 1, a workspace of NULL where one is
+ * needed; BUFFER_TOO_SMALL: a smaller workspace; UNSUPPORTED: vocab > 2^22, or
+ * a launch of 2^32 threads or more. */
+lsq_status lsq_verify_tree(const lsq_draft_batch* batch, void* workspace, size_t workspace_bytes,
+                           void* stream);
 
 /* Static description of a status code. */
 const char* lsq_status_string(lsq_status s);

@@ -26,7 +26,8 @@ __all__ = ["LsqConfig", "LsqState", "LsqError", "lsq_state_sizes", "lsq_state_al
            "lsq_state_step_index", "lsq_state_set_step_index",
            "lsq_decode_step", "lsq_decode_run", "lsq_prefill", "token_batch", "lsq_attend_workspace",
            "lsq_attend", "lsq_step_slots", "lsq_state_store_slots", "lsq_state_load_slots",
-           "lsq_step_tree", "lsq_accept_path", "lsq_verify_tree", "verify_tree",
+           "lsq_step_tree", "lsq_accept_path", "lsq_verify_workspace",
+           "lsq_verify_tree", "verify_tree",
            "lsq_status_string", "lsq_version",
            "lsq_probe_stream", "lsq_probe_span",
            "lsq_probe_valu"]
@@ -179,8 +180,17 @@ def lsq_accept_path(handle: int, batch, path, lengths, depth: int, stream=None) 
                                            int(depth), _stream_ptr(stream)), "lsq_accept_path")
 
 
-def lsq_verify_tree(batch, stream=None) -> None:
-    _lib.check(_lib.load().lsq_verify_tree(ctypes.byref(batch), _stream_ptr(stream)), "lsq_verify_tree")
+def lsq_verify_workspace(batch) -> int:
+    """Bytes of workspace ``lsq_verify_tree`` needs for this batch."""
+    n = ctypes.c_size_t(0)
+    _lib.check(_lib.load().lsq_verify_workspace(ctypes.byref(batch), ctypes.byref(n)), "lsq_verify_workspace")
+    return int(n.value)
+
+
+def lsq_verify_tree(batch, workspace=None, stream=None) -> None:
+    nb = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _lib.check(_lib.load().lsq_verify_tree(ctypes.byref(batch), _ptr(workspace), nb, _stream_ptr(stream)),
+               "lsq_verify_tree")
 
 
 def verify_tree(target, tokens, parents, cu_nodes, uniform, uniform_next, draft=None, replacement=True,

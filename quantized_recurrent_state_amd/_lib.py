@@ -89,7 +89,8 @@ def load() -> ctypes.CDLL:
         "lsq_step_slots": [P, batchp, P],
         "lsq_step_tree": [P, batchp, P, ctypes.c_int32, P],
         "lsq_accept_path": [P, batchp, P, P, ctypes.c_int32, P],
-        "lsq_verify_tree": [ctypes.POINTER(lsq_draft_batch), P],
+        "lsq_verify_workspace": [ctypes.POINTER(lsq_draft_batch), ctypes.POINTER(S)],
+        "lsq_verify_tree": [ctypes.POINTER(lsq_draft_batch), P, S, P],
         "lsq_state_store_slots": [P, P, ctypes.c_int32, P, P, P],
         "lsq_state_load_slots": [P, P, ctypes.c_int32, P, P, P],
         "lsq_status_string": [ctypes.c_int],

@@ -322,6 +322,27 @@ lsq_status slot_status(hipError_t e, const char* what) {
 // A scalar decay and the linear write run in chunks; the rest token by token.
 bool chunked(const lsq_config& c) { return c.decay == LSQ_DECAY_SCALAR && c.delta == 0; }
 
+// Checks of a batch of drafts that need no device.
+lsq_status check_drafts(const lsq_draft_batch* b) {
+  if (!b) return fail(LSQ_ERR_INVALID_ARG, "batch is null");
+  if (b->seqs < 0 || b->nodes < 0) return fail(LSQ_ERR_INVALID_ARG, "negative seqs or nodes");
+  if (b->vocab < 1) return fail(LSQ_ERR_INVALID_ARG, "vocab must be at least 1");
+  if (b->depth < 1) return fail(LSQ_ERR_INVALID_ARG, "depth must be at least 1");
+  if (b->replacement != 0 && b->replacement != 1)
+    return fail(LSQ_ERR_INVALID_ARG, "replacement must be 0 or 1");
+  if (b->vocab > lsq::kMaxVocab)
+    return fail(LSQ_ERR_UNSUPPORTED, "a vocabulary of more than %d tokens", lsq::kMaxVocab);
+  if (b->target_stride < 0 || (b->draft && b->draft_stride < 0))
+    return fail(LSQ_ERR_INVALID_ARG, "negative row stride");
+  return LSQ_OK;
+}
+
+size_t drafts_workspace(const lsq_draft_batch* b) {
+  const size_t runs = ((size_t)b->vocab + lsq::kRun - 1) / lsq::kRun;
+  const size_t rounds = lsq::verify_rounds(b->seqs, b->nodes, b->vocab, b->draft != nullptr);
+  return rounds ? (8 * runs * rounds + lsq::kEnded) * b->seqs : 0;
+}
+
 // Store (fp32 -> quantised) and load (quantised -> fp32) of slots.
 lsq_status copy_slots(const lsq_state* f, const lsq_state* q, bool store, int32_t count,
                       const int32_t* dst_slots, const int32_t* src_slots, void* stream) {
@@ -711,17 +732,17 @@ lsq_status lsq_accept_path(lsq_state* st, const lsq_token_batch* batch, const in
                                       static_cast<hipStream_t>(stream)), "accept_path launch");
 }
 
-lsq_status lsq_verify_tree(const lsq_draft_batch* b, void* stream) {
-  if (!b) return fail(LSQ_ERR_INVALID_ARG, "batch is null");
-  if (b->seqs < 0 || b->nodes < 0) return fail(LSQ_ERR_INVALID_ARG, "negative seqs or nodes");
-  if (b->vocab < 1) return fail(LSQ_ERR_INVALID_ARG, "vocab must be at least 1");
-  if (b->depth < 1) return fail(LSQ_ERR_INVALID_ARG, "depth must be at least 1");
-  if (b->replacement != 0 && b->replacement != 1)
-    return fail(LSQ_ERR_INVALID_ARG, "replacement must be 0 or 1");
-  if (b->vocab > lsq::kMaxVocab)
-    return fail(LSQ_ERR_UNSUPPORTED, "a vocabulary of more than %d tokens", lsq::kMaxVocab);
-  if (b->target_stride < 0 || (b->draft && b->draft_stride < 0))
-    return fail(LSQ_ERR_INVALID_ARG, "negative row stride");
+lsq_status lsq_verify_workspace(const lsq_draft_batch* batch, size_t* bytes) {
+  lsq_status s = check_drafts(batch);
+  if (s != LSQ_OK) return s;
+  if (!bytes) return fail(LSQ_ERR_INVALID_ARG, "bytes is null");
+  *bytes = drafts_workspace(batch);
+  return ok();
+}
+
+lsq_status lsq_verify_tree(const lsq_draft_batch* b, void* workspace, size_t workspace_bytes, void* stream) {
+  lsq_status s = check_drafts(b);
+  if (s != LSQ_OK) return s;
   if (b->seqs == 0) return ok();
   if (!b->cu_nodes || !b->path || !b->lengths || !b->next ||
       (b->nodes > 0 && (!b->target || !b->ids || !b->parents || !b->uniform || !b->uniform_next)))
@@ -730,6 +751,13 @@ lsq_status lsq_verify_tree(const lsq_draft_batch* b, void* stream) {
                         (const void*)b->cu_nodes, (const void*)b->uniform, (const void*)b->uniform_next,
                         (const void*)b->path, (const void*)b->lengths, (const void*)b->next})
     if (!aligned4(p)) return fail(LSQ_ERR_INVALID_ARG, "arrays must be 4-byte aligned");
+  const size_t need = drafts_workspace(b);
+  if (need) {
+    if (!workspace || !aligned16(workspace))
+      return fail(LSQ_ERR_INVALID_ARG, "the workspace must be non-null and 16-byte aligned");
+    if (workspace_bytes < need)
+      return fail(LSQ_ERR_BUFFER_TOO_SMALL, "the workspace holds %zu bytes, needs %zu", workspace_bytes, need);
+  }
   lsq::VerifyArgs a{};
   a.target = b->target; a.draft = b->draft;
   a.ids = b->ids; a.parents = b->parents; a.cu = b->cu_nodes;
@@ -738,6 +766,8 @@ lsq_status lsq_verify_tree(const lsq_draft_batch* b, void* stream) {
   a.target_stride = b->target_stride; a.draft_stride = b->draft_stride;
   a.nodes = b->nodes;
   a.seqs = b->seqs; a.vocab = b->vocab; a.depth = b->depth; a.replacement = b->replacement;
+  a.rounds = lsq::verify_rounds(b->seqs, b->nodes, b->vocab, b->draft != nullptr);
+  a.ws = static_cast<double*>(workspace);
   return slot_status(lsq::launch_verify(a, static_cast<hipStream_t>(stream)), "verify_tree launch");
 }
 

@@ -83,6 +83,7 @@ struct PathArgs {
 };
 
 constexpr int kMaxVocab = 1 << 22;
+constexpr int kRun = 2048;   // elements of a row that are summed together
 
 struct VerifyArgs {
   const float* target;     // [nodes] rows target_stride elements apart
@@ -97,7 +98,13 @@ struct VerifyArgs {
   int32_t* next;           // [seqs]
   int64_t target_stride, draft_stride, nodes;
   int32_t seqs, vocab, depth, replacement;
+  int32_t rounds;          // sums made by launches of their own
+  double* ws;              // [seqs][rounds][runs], then where each entry's walk ended (kEnded bytes)
 };
+constexpr int kEnded = 16 + 4 * kMaxNodes;
+
+// Sums of rows that are split over the chip, by a launch each, before the walk's own.
+int verify_rounds(int32_t seqs, int64_t nodes, int32_t vocab, bool draft);
 
 hipError_t launch_tree_f32(const TreeArgs& a, int dk, int delta, int diag, hipStream_t s);
 hipError_t launch_tree_f16(const TreeArgs& a, int dk, int delta, int diag, hipStream_t s);

@@ -55,7 +55,8 @@ def _probabilities(name, t, shape, dev):
 
 
 def draft_batch(target, tokens, parents, cu_nodes, uniform, uniform_next, draft, replacement, depth):
-    """Checks the tensors of ``verify_tree``; returns (lsq_draft_batch, path, lengths, next)."""
+    """Checks the tensors of ``verify_tree``; returns (lsq_draft_batch, its workspace's address and
+    bytes, path, lengths, next)."""
     if target.dim() != 2:
         raise ValueError(f"target has shape {tuple(target.shape)}, expected (nodes, vocab)")
     if cu_nodes.dim() != 1 or cu_nodes.shape[0] < 1:
@@ -70,12 +71,21 @@ def draft_batch(target, tokens, parents, cu_nodes, uniform, uniform_next, draft,
     cp = _plain("cu_nodes", cu_nodes, (m + 1,), torch.int32, dev)
     up = _plain("uniform", uniform, (n,), torch.float32, dev)
     np = _plain("uniform_next", uniform_next, (m,), torch.float32, dev)
-    out = torch.empty(m * (depth + 2), dtype=torch.int32, device=target.device)
-    at = out.data_ptr()
     b = _lib.lsq_draft_batch(m, vocab, depth, 1 if replacement else 0, n, ts, ds, tp, dp, ip, pp, cp, up, np,
-                             at, at + 4 * m * depth, at + 4 * m * (depth + 1))
-    path, lengths, token = out.split_with_sizes((m * depth, m, m))
-    return b, path.view(m, depth), lengths, token
+                             None, None, None)
+    nb = 0
+    if vocab > 8192:                         # smaller rows need no workspace
+        need = ctypes.c_size_t()
+        status = _lib.load().lsq_verify_workspace(ctypes.byref(b), ctypes.byref(need))
+        if status:
+            _lib.check(status, "lsq_verify_workspace")
+        nb = need.value // 4                 # whole 8-byte numbers
+    # the workspace, then the outputs
+    buf = torch.empty(nb + m * (depth + 2), dtype=torch.int32, device=target.device)
+    at = buf.data_ptr()
+    b.path, b.lengths, b.next = at + 4 * nb, at + 4 * (nb + m * depth), at + 4 * (nb + m * (depth + 1))
+    _, path, lengths, token = buf.split_with_sizes((nb, m * depth, m, m))
+    return b, at, 4 * nb, path.view(m, depth), lengths, token
 
 
 def verify_tree(target, tokens, parents, cu_nodes, uniform, uniform_next, draft, replacement, depth, stream):
@@ -83,9 +93,9 @@ def verify_tree(target, tokens, parents, cu_nodes, uniform, uniform_next, draft,
         raise ValueError("target must be a device tensor")
 
     def call(s):
-        b, path, lengths, token = draft_batch(target, tokens, parents, cu_nodes, uniform, uniform_next, draft,
-                                              replacement, depth)
-        status = _lib.load().lsq_verify_tree(ctypes.byref(b), s)
+        b, ws, nb, path, lengths, token = draft_batch(target, tokens, parents, cu_nodes, uniform, uniform_next,
+                                                      draft, replacement, depth)
+        status = _lib.load().lsq_verify_tree(ctypes.byref(b), ws if nb else None, nb, s)
         if status:
             _lib.check(status, "lsq_verify_tree")
         return path, lengths, token

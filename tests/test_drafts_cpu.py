@@ -89,16 +89,33 @@ def draft(**kw):
                                    "lengths", "next")]], ids=lambda x: str(x))
 def test_draft_batches_are_refused(change, status):
     L = _lib.load()
-    assert L.lsq_verify_tree(ctypes.byref(draft(**change)), None) == status
+    assert L.lsq_verify_tree(ctypes.byref(draft(**change)), FAKE, 1 << 40, None) == status
     assert L.lsq_last_error() != b""
 
 
 def test_no_entries_to_verify():
     L = _lib.load()
-    assert L.lsq_verify_tree(None, None) == 1
+    assert L.lsq_verify_tree(None, None, 0, None) == 1
+    n = ctypes.c_size_t()
+    assert L.lsq_verify_workspace(None, ctypes.byref(n)) == 1
+    assert L.lsq_verify_workspace(ctypes.byref(draft()), None) == 1
     none = {x: None for x in ("target", "draft", "ids", "parents", "cu_nodes", "uniform", "uniform_next", "path",
                               "lengths", "next")}
-    assert L.lsq_verify_tree(ctypes.byref(draft(seqs=0, **none)), None) == 0
+    assert L.lsq_verify_tree(ctypes.byref(draft(seqs=0, **none)), None, 0, None) == 0
+
+
+def test_verify_workspace():
+    """Small vocabularies need none; larger ones a bounded one, which is checked."""
+    L, n = _lib.load(), ctypes.c_size_t(1)
+    need = lambda **kw: (L.lsq_verify_workspace(ctypes.byref(draft(**kw)), ctypes.byref(n)), n.value)[1]
+    assert need(vocab=8192) == 0 and need(seqs=0, vocab=100_000) == 0
+    for kw in (dict(vocab=8193), dict(vocab=131_072), dict(vocab=131_072, draft=None), dict(vocab=1 << 22, nodes=99)):
+        size = need(**kw)
+        assert 0 < size <= 3 * (4 * kw["vocab"] // 256 + 4096)
+        b = ctypes.byref(draft(**kw))
+        assert L.lsq_verify_tree(b, None, size, None) == 1
+        assert L.lsq_verify_tree(b, FAKE + 8, size, None) == 1
+        assert L.lsq_verify_tree(b, FAKE, size - 1, None) == 3
 
 
 def test_launches_of_too_many_threads_are_refused():
@@ -146,7 +163,8 @@ def test_python_checks_of_verify():
     good = dict(target=torch.zeros(n, V), tokens=torch.zeros(n, dtype=torch.int32),
                 parents=torch.zeros(n, dtype=torch.int32), cu_nodes=torch.zeros(m + 1, dtype=torch.int32),
                 uniform=torch.zeros(n), uniform_next=torch.zeros(m), draft=torch.zeros(n, V), replacement=True, depth=7)
-    b, path, lengths, token = drafts.draft_batch(**good)
+    b, ws, nb, path, lengths, token = drafts.draft_batch(**good)
+    assert nb == 0                                       # a small vocabulary
     assert (b.seqs, b.vocab, b.depth, b.nodes, b.target_stride) == (m, V, 7, n, V)
     assert path.shape == (m, 7) and lengths.shape == (m,) and token.shape == (m,)
     wide = torch.zeros(n, V + 9)

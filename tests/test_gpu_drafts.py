@@ -659,3 +659,128 @@ def test_a_run_of_drafted_decoding():
         moved += int(lengths.sum()) - 3
         pending = token
     assert moved > 0
+
+
+# ---- streams, graphs, batches ------------------------------------------------------------------
+
+def _tree_case(seed=1, delta=1):
+    counts = [9, 17, 3]
+    cu = offsets(counts)
+    x = [t.to(DEV) for t in tokens(cu[-1], 4, 2, 128, 128, torch.bfloat16, seed)]
+    return x, i32(*cu), i32(*trees(counts, "random", seed)), counts
+
+
+def test_replayed_graphs_take_other_slots_trees_and_paths():
+    """One captured run of tree, verification and acceptance, replayed with other contents in the same
+    buffers and eager work between: every replay is what eager calls give."""
+    vocab, dk = 20000, 128
+    st, _ = state(6, 4, dk, 128, 1)
+    ref, _ = state(6, 4, dk, 128, 1)
+    x, cu, parents, counts = _tree_case()
+    slots, fresh = i32(4, 0, 2), torch.tensor([False, True, False], device=DEV)
+    d = drafts(counts, vocab, "random", 1, "with")
+    rows = {n: d[n].to(DEV) for n in ("target", "draft", "ids", "uniform", "uniform_next")}
+    tree = i32(*d["parents"])
+
+    def run(s):
+        o = s.step_tree(*x, cu, parents, slots=slots, fresh=fresh, max_nodes=32)
+        path, lengths, token = lsq.verify_tree(rows["target"], rows["ids"], tree, cu, rows["uniform"],
+                                               rows["uniform_next"], draft=rows["draft"], depth=8)
+        s.accept_path(*x[1:], cu, path, lengths, slots=slots, fresh=fresh)
+        return o, path, lengths, token
+
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        run(st)
+    torch.cuda.current_stream().wait_stream(stream)
+    st.f32.copy_(ref.f32)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = run(st)
+    st.f32.copy_(ref.f32)
+    for step in range(4):
+        y, _, p, _ = _tree_case(seed=10 + step)
+        for a, b in zip(x, y):
+            a.copy_(b)
+        parents.copy_(p)
+        e = drafts(counts, vocab, "random", 20 + step, "with")
+        for n in rows:
+            rows[n].copy_(e[n])
+        tree.copy_(i32(*e["parents"]))
+        slots.copy_(i32(*[(4, 0, 2), (5, 1, 3), (0, -1, 5), (2, 2, 1)][step]))
+        g.replay()
+        got = [t.clone() for t in out]
+        torch.cuda.synchronize()
+        want = run(ref)                                  # eager, on another handle
+        named = [i for i in range(3) if int(slots[i]) >= 0]
+        begin = offsets(counts)
+        for i in named:
+            assert torch.equal(got[0][begin[i]:begin[i + 1]], want[0][begin[i]:begin[i + 1]])
+        for a, b in zip(got[1:], want[1:]):
+            assert torch.equal(a, b)
+        assert torch.equal(st.f32, ref.f32)
+
+
+def test_calls_on_other_streams():
+    """Two streams at once, each with a handle and a batch of its own."""
+    runs = []
+    for seed in (1, 2):
+        st, _ = state(4, 4, 128, 128, 1, seed=seed)
+        x, cu, parents, counts = _tree_case(seed)
+        d = drafts(counts, 40000, "random", seed, "without")
+        rows = [d[n].to(DEV) for n in ("target", "ids", "uniform", "uniform_next", "draft")]
+        runs.append((st, x, cu, parents, rows, i32(*d["parents"]), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+
+    def run(st, x, cu, parents, rows, tree, stream, given):
+        kw = dict(stream=stream if given else None)
+        o = st.step_tree(*x, cu, parents, slots=i3, max_nodes=17, **kw)
+        v = lsq.verify_tree(rows[0], rows[1], tree, cu, rows[2], rows[3], draft=rows[4], replacement=False, depth=9, **kw)
+        st.accept_path(*x[1:], cu, v[0], v[1], slots=i3, **kw)
+        return o, *v, st.f32.clone() if not given else None
+
+    i3 = i32(3, 0, 2)
+    before = [r[0].f32.clone() for r in runs]
+    torch.cuda.synchronize()
+    got = [run(*r, True) for _ in range(1) for r in runs]
+    torch.cuda.synchronize()
+    states = [r[0].f32.clone() for r in runs]
+    for r, b, g, s in zip(runs, before, got, states):
+        r[0].f32.copy_(b)
+        want = run(*r, False)
+        for a, w in zip(g[:4], want[:4]):
+            assert torch.equal(a, w)
+        assert torch.equal(s, want[4])
+
+
+def test_the_same_call_gives_the_same_bits():
+    st, _ = state(4, 4, 128, 128, 1)
+    x, cu, parents, counts = _tree_case()
+    first = st.step_tree(*x, cu, parents)
+    for _ in range(5):
+        assert torch.equal(st.step_tree(*x, cu, parents), first)
+
+
+def test_fewer_nodes_than_max_nodes_allows():
+    # the bound chooses the kernel's size, not its results beyond rounding
+    st, S = state(4, 4, 128, 128, 1)
+    x, cu, parents, counts = _tree_case()
+    want, mag = tree_ref(S, [0, 1, 2], None, cu.tolist(), parents.tolist(), *(t.cpu() for t in x), delta=1)
+    for bound in (17, 32, 33, 48, 64):
+        o = st.step_tree(*x, cu, parents, max_nodes=bound)
+        check_tree(o, want, mag, 17, 128, torch.bfloat16, 1)
+
+
+def test_verify_many_entries():
+    counts = [(5 * i) % 7 + 1 for i in range(300)]
+    d = drafts(counts, 700, "random", 2, "without")
+    for a in d["cu"][:-1]:
+        d["parents"][a] = -1
+    check_verify(d, "without", depth=5)
+    d = drafts([4] * 40, 33000, "star", 2, "with")       # several sums in the entries' own workgroups
+    check_verify(d, "with", depth=5)
+    d = drafts([12] * 5, 33000, "star", 3, "with", error=2.5)    # and by launches
+    check_verify(d, "with", depth=5)
+    d = drafts([14] * 5, 40001, "star", 3, "without", error=2.5)
+    check_verify(d, "without", depth=5)
