@@ -340,7 +340,7 @@ lsq_status check_drafts(const lsq_draft_batch* b) {
 size_t drafts_workspace(const lsq_draft_batch* b) {
   const size_t runs = ((size_t)b->vocab + lsq::kRun - 1) / lsq::kRun;
   const size_t rounds = lsq::verify_rounds(b->seqs, b->nodes, b->vocab, b->draft != nullptr);
-  return rounds ? (8 * runs * rounds + lsq::kEnded) * b->seqs : 0;
+  return (8 * runs * rounds * b->seqs + 15) / 16 * 16 + lsq::kSaved * rounds * b->seqs;
 }
 
 // Store (fp32 -> quantised) and load (quantised -> fp32) of slots.

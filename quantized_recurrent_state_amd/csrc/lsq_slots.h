@@ -99,9 +99,9 @@ struct VerifyArgs {
   int64_t target_stride, draft_stride, nodes;
   int32_t seqs, vocab, depth, replacement;
   int32_t rounds;          // sums made by launches of their own
-  double* ws;              // [seqs][rounds][runs], then where each entry's walk ended (kEnded bytes)
+  double* ws;              // rounds times seqs of the runs' sums, then of a walk's kSaved bytes
 };
-constexpr int kEnded = 16 + 4 * kMaxNodes;
+constexpr int kSaved = 1840;
 
 // Sums of rows that are split over the chip, by a launch each, before the walk's own.
 int verify_rounds(int32_t seqs, int64_t nodes, int32_t vocab, bool draft);

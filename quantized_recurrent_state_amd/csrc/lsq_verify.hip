@@ -78,9 +78,9 @@ struct Residual {
     const uint64_t any = any_in(e0, e1);
     double sum = 0.0;
 #pragma unroll 4
-    for (int e = e0 + 4 * lane; e < e1; e += 256) {
+    for (int y = 0; y < kRun; y += 256) {        // nothing behind the row
       double x[4];
-      four(e, any, x);
+      four(e0 + y + 4 * lane, any, x);
       sum += (x[0] + x[1]) + (x[2] + x[3]);
     }
 #pragma unroll
@@ -158,73 +158,113 @@ __device__ __forceinline__ int draw(const Residual& left, const double* sums, in
   return y < 0 ? -1 : e0 + E * l + y;
 }
 
-// The walk of one entry, the same in every wave.  It asks for the sum of what is
-// left of a row, in order, where a decision needs it: sum(k, left) of the k-th
-// time returns it, or ends the walk with a negative number.
+// An entry's walk between two launches.
+struct Saved {
+  int done;                                      // the launch it ended in, counted from 1; 0: not yet, -1: a refused entry
+  int node, len, parent[kMaxNodes], id[kMaxNodes], took[kMaxNodes], gone[kMaxNodes];
+  float u[kMaxNodes], px[kMaxNodes], qx[kMaxNodes];
+  double cut, rest;
+  uint64_t kids;
+};
+static_assert(sizeof(Saved) <= kSaved && kSaved % 16 == 0, "what the workspace holds");
+
+// The walk of one entry, the same in every wave that makes it.
 struct Walk {
   const VerifyArgs& a;
-  int i, lane;
+  int lane;
   int64_t t0;
-  int n, parent, id;
+  int parent, id;                                // of the lane's node
+  float u, px, qx;                               // its uniform number, its token's chances in the rows of its parent
   bool sound, testable;
-  double px, qx, u;
+  int node, len, took;                           // where it is; lane d holds the path's node d
+  uint64_t kids;                                 // children still to be tested
+  double total, rest;
+  bool stale;                                    // total is of an earlier cut
   Residual left;
-  int node, len, took;                           // the node it is at; lane d holds the path's node d
 
-  __device__ __forceinline__ Walk(const VerifyArgs& args, int entry, int l) : a(args), i(entry), lane(l) {
+  __device__ __forceinline__ Walk(const VerifyArgs& args, int i, int l) : a(args), lane(l) {
     t0 = min(max((int64_t)a.cu[i], (int64_t)0), a.nodes);
+  }
+
+  __device__ __forceinline__ void at_row(int j) {
+    node = j;
+    left.p = a.target + (t0 + j) * a.target_stride;
+    left.q = a.draft ? a.draft + (t0 + j) * a.draft_stride : nullptr;
+    left.vocab = a.vocab;
+  }
+
+  __device__ __forceinline__ void at_node(int j) {
+    at_row(j);
+    left.cut = 0.0;
+    left.gone = -1;
+    total = rest = 1.0;
+    stale = false;
+    kids = __ballot(testable && parent == j);
+  }
+
+  __device__ __forceinline__ void begin(int i) {
     const int64_t t1 = min(max((int64_t)a.cu[i + 1], (int64_t)0), a.nodes);
-    n = (int)min(t1 - t0, (int64_t)kMaxNodes + 1);
+    const int n = (int)min(t1 - t0, (int64_t)kMaxNodes + 1);
     parent = lane < n ? a.parents[t0 + lane] : -1;
     sound = n > 0 && n <= kMaxNodes && !__any(parent < -1 || parent >= lane);
     id = lane < n ? a.ids[t0 + lane] : -1;
     u = lane < n ? a.uniform[t0 + lane] : 0.f;
-    at_node(0);
-    len = 0, took = -1;
-    // every test's numbers at once: a token's probabilities in the rows of its parent
+    // every test's numbers at once
     testable = sound && lane < n && parent >= 0 && id >= 0 && id < a.vocab;
-    px = 0.0, qx = 1.0;
+    px = 0.f, qx = 1.f;
     if (testable) {
       px = a.target[(t0 + parent) * a.target_stride + id];
       if (a.draft) qx = a.draft[(t0 + parent) * a.draft_stride + id];
     }
+    len = 1, took = lane == 0 ? 0 : -1;
+    at_node(0);
   }
 
-  __device__ __forceinline__ void at_node(int j) {
-    node = j;
-    left.p = a.target + (t0 + j) * a.target_stride;
-    left.q = a.draft ? a.draft + (t0 + j) * a.draft_stride : nullptr;
-    left.cut = 0.0;
-    left.gone = -1;
-    left.vocab = a.vocab;
+  // Goes on from where another launch stopped for want of the sum `known`.
+  __device__ __forceinline__ void resume(const Saved& s, double known) {
+    sound = true;
+    parent = s.parent[lane], id = s.id[lane];
+    u = s.u[lane], px = s.px[lane], qx = s.qx[lane];
+    testable = parent >= 0 && id >= 0;
+    len = s.len, took = s.took[lane];
+    at_row(s.node);
+    left.cut = s.cut, left.gone = s.gone[lane];
+    total = known, rest = s.rest, stale = false;
+    kids = s.kids;
   }
 
-  // False where a sum was not to be had.  Ends with `left` at the last node.
+  __device__ __forceinline__ void save(Saved& s, int done) const {
+    s.parent[lane] = testable ? parent : -1, s.id[lane] = id, s.took[lane] = took, s.gone[lane] = left.gone;
+    s.u[lane] = u, s.px[lane] = px, s.qx[lane] = qx;
+    if (lane == 0) {
+      s.node = node, s.len = len;
+      s.cut = left.cut, s.rest = rest;
+      s.kids = kids;
+      s.done = done;
+    }
+  }
+
+  // Tests children until none is left or the path is full; sum() gives the sum of
+  // what is left where a test needs it, or a negative number: then it stops there
+  // and returns false.  In the end `left` is what the next token is drawn from.
   template <typename Sum>
   __device__ __forceinline__ bool run(Sum sum) {
-    len = 1, took = lane == 0 ? 0 : -1;
-    int sums = 0;                                // asked for so far
-    double total = 1.0, rest = 1.0;
-    bool stale = false;                          // total is of an earlier cut
-    at_node(0);
-    uint64_t kids = __ballot(testable && parent == 0);
     while (kids && len < a.depth) {
-      const int j = __builtin_ctzll(kids);
-      kids &= kids - 1;
-      const int x = __builtin_amdgcn_readlane(id, j);
-      const double pj = __shfl(px, j), qj = __shfl(qx, j), uj = __shfl(u, j);
       if (stale) {
-        total = sum(sums++);
+        total = sum();
         if (total < 0.0) return false;
         stale = false;
       }
-      const double pl = __any(left.gone == x) ? 0.0 : left.of((float)pj, (float)qj);
+      const int j = __builtin_ctzll(kids);
+      kids &= kids - 1;
+      const int x = __builtin_amdgcn_readlane(id, j);
+      const float pj = __shfl(px, j);
+      const double qj = __shfl(qx, j), uj = __shfl(u, j);
+      const double pl = __any(left.gone == x) ? 0.0 : left.of(pj, (float)qj);
       if (uj * total * qj < pl * rest) {
         took = lane == len ? j : took;
         ++len;
         at_node(j);
-        total = rest = 1.0;
-        kids = __ballot(testable && parent == j);
       } else if (a.draft) {
         if (rest > 0.0) left.cut += total / rest;
         if (!a.replacement) rest = fmax(rest - qj, 0.0);
@@ -236,116 +276,106 @@ struct Walk {
     }
     return true;
   }
+
+  __device__ __forceinline__ void put_path(int i) const {
+    for (int d = lane; d < a.depth; d += 64) a.path[(int64_t)i * a.depth + d] = sound && d < len ? took : -1;
+    if (lane == 0) a.lengths[i] = sound ? len : 0;
+  }
 };
 
-// Where an entry's walk ended, behind the sums in the workspace.
-struct Ended {
-  int done;                                      // the number of sums then made; 0: not yet, -1: a refused entry
-  int node;
-  double cut;
-  int gone[kMaxNodes];
-};
-static_assert(sizeof(Ended) == kEnded, "what the workspace holds");
-
-__device__ __forceinline__ Ended* ended_of(const VerifyArgs& a, int runs) {
-  return reinterpret_cast<Ended*>(a.ws + (int64_t)a.seqs * a.rounds * runs);
+// The workspace: the runs' sums [rounds][seqs][runs], then the walks [rounds][seqs].
+__device__ __forceinline__ double* sums_of(const VerifyArgs& a, int k, int i, int runs) {
+  return a.ws + ((int64_t)k * a.seqs + i) * runs;
 }
 
-// Outputs of an entry whose walk has ended, by one wave; of a refused one with len 0.
-__device__ __forceinline__ void put_path(const VerifyArgs& a, int i, int len, int took, int lane) {
-  for (int d = lane; d < a.depth; d += 64) a.path[(int64_t)i * a.depth + d] = d < len ? took : -1;
-  if (lane == 0) a.lengths[i] = len;
+__device__ __forceinline__ Saved* saved_of(const VerifyArgs& a, int k, int i, int runs) {
+  return reinterpret_cast<Saved*>(reinterpret_cast<char*>(a.ws + ((int64_t)a.rounds * a.seqs * runs + 1) / 2 * 2) +
+                                  ((int64_t)k * a.seqs + i) * kSaved);
 }
 
-// The k-th sum of every entry that needs one: a wave per run, the runs' sums to the
-// workspace [entries][rounds][runs].  Each wave makes the entry's walk by itself,
-// from the sums of the rounds before; the first tells where it ended.
+// The k-th sum of every entry that needs one: a wave per run.  Each wave makes the
+// entry's walk up to there by itself, from where the launch before left it; the
+// first one writes down where that is.
 __global__ __launch_bounds__(256) void sum_kernel(VerifyArgs a, int k) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int runs = (a.vocab + kRun - 1) / kRun, groups = (runs + 3) / 4;
   const int i = blockIdx.x / groups, r = blockIdx.x % groups * 4 + wave;
   if (r >= runs) return;
-  Ended* const end = ended_of(a, runs) + i;
-  if (k > 0) {                                   // ended before; k + 1 is this launch's own word
-    const int done = end->done;
-    if (done < 0 || (done > 0 && done <= k)) return;
-  }
+  Saved& now = *saved_of(a, k, i, runs);
   Walk w(a, i, lane);
-  double* const ws = a.ws + (int64_t)i * a.rounds * runs;
-  // the walk's last sum is the one that the next token is drawn from
-  const bool whole = w.sound && w.run([&](int m) { return m < k ? total_of(ws + (int64_t)m * runs, runs, lane) : -1.0; });
-  if (w.sound) {
+  if (k == 0) {
+    w.begin(i);
+  } else {
+    const Saved& before = *saved_of(a, k - 1, i, runs);
+    const int done = before.done;
+    if (done) {
+      if (r == 0 && lane == 0) now.done = done;
+      return;
+    }
+    w.resume(before, total_of(sums_of(a, k - 1, i, runs), runs, lane));
+  }
+  const bool whole = w.sound && w.run([] { return -1.0; });
+  if (w.sound) {                                 // the walk's last sum is the one that the next token is drawn from
     const double x = w.left.run(r, lane);
-    if (lane == 0) ws[(int64_t)k * runs + r] = x;
+    if (lane == 0) sums_of(a, k, i, runs)[r] = x;
   }
   if (r != 0) return;
-  if (whole || !w.sound) {
-    put_path(a, i, w.sound ? w.len : 0, w.took, lane);
-    end->gone[lane] = w.left.gone;
-  }
-  if (lane == 0) {
-    if (!w.sound) a.next[i] = -1;
-    end->node = w.node;
-    end->cut = w.left.cut;
-    end->done = !w.sound ? -1 : whole ? k + 1 : 0;
-  }
+  w.save(now, !w.sound ? -1 : whole ? k + 1 : 0);
+  if (whole || !w.sound) w.put_path(i);
+  if (!w.sound && lane == 0) a.next[i] = -1;
 }
 
-__global__ __launch_bounds__(1024) void verify_kernel(VerifyArgs a) {
+// What the launches above left to do: the token of each entry, by one wave, and
+// before it the walks that need more sums, with the whole workgroup.
+constexpr int kWaves = 16;                        // of verify_kernel: a run's elements are in flight at once
+
+__global__ __launch_bounds__(64 * kWaves) void verify_kernel(VerifyArgs a) {
   __shared__ double sums[kMaxRuns], buf[kRun / 64];
   const int lane = threadIdx.x & 63, i = blockIdx.x;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int runs = (a.vocab + kRun - 1) / kRun;
-  const double* const ws = a.ws + (int64_t)i * a.rounds * runs;
-  const double part = fmin(fmax(a.uniform_next ? (double)a.uniform_next[i] : 0.0, 0.0), 1.0);
-  const Ended* const end = ended_of(a, runs) + i;
-  const int done = a.rounds ? end->done : 0;
+  const int runs = (a.vocab + kRun - 1) / kRun, last = a.rounds - 1;
+  const int done = a.rounds ? saved_of(a, last, i, runs)->done : 0;
   if (done < 0 || (done && wave != 0)) return;
-  Residual left{nullptr, nullptr, 0.0, -1, a.vocab};
   const double* from = sums;
-  auto sum_runs = [&](int w0, int step) {        // waves w0, w0 + step, ...
-    for (int r = w0; r < runs; r += step) {
+  auto sum_runs = [&](const Residual& left, int first, int step) {
+    for (int r = first; r < runs; r += step) {
       const double x = left.run(r, lane);
       if (lane == 0) sums[r] = x;
     }
   };
-  if (done) {                                    // one wave draws
-    const int64_t row = min(max((int64_t)a.cu[i], (int64_t)0), a.nodes) + end->node;
-    left.p = a.target + row * a.target_stride;
-    left.q = a.draft ? a.draft + row * a.draft_stride : nullptr;
-    left.cut = end->cut;
-    left.gone = end->gone[lane];
-    from = ws + (int64_t)(done - 1) * runs;
+  Walk w(a, i, lane);
+  if (done) {
+    from = sums_of(a, done - 1, i, runs);
+    w.resume(*saved_of(a, done - 1, i, runs), 0.0);
   } else {
-    Walk w(a, i, lane);
+    if (a.rounds) w.resume(*saved_of(a, last, i, runs), total_of(sums_of(a, last, i, runs), runs, lane));
+    else w.begin(i);
     if (!w.sound) {
-      if (wave != 0) return;
-      put_path(a, i, 0, -1, lane);
-      if (lane == 0) a.next[i] = -1;
+      if (wave == 0) w.put_path(i);
+      if (threadIdx.x == 0) a.next[i] = -1;
       return;
     }
     auto sum_row = [&] {
-      left = w.left;
       __syncthreads();
-      sum_runs(wave, 16);
+      sum_runs(w.left, wave, kWaves);
       __syncthreads();
     };
-    w.run([&](int m) {
-      if (m < a.rounds) return total_of(ws + (int64_t)m * runs, runs, lane);
+    w.run([&] {
       sum_row();
       return total_of(sums, runs, lane);
     });
-    sum_row();                                   // of the last row: no launch made it
+    sum_row();
     if (wave != 0) return;
-    put_path(a, i, w.len, w.took, lane);
+    w.put_path(i);
   }
-  int token = draw(left, from, runs, part, buf, lane);
+  const double part = fmin(fmax((double)a.uniform_next[i], 0.0), 1.0);
+  int token = draw(w.left, from, runs, part, buf, lane);
   if (token < 0) {                               // nothing left: the token comes from p itself
-    left.q = nullptr;
-    left.gone = -1;
-    sum_runs(0, 1);
+    w.left.q = nullptr;
+    w.left.gone = -1;
+    sum_runs(w.left, 0, 1);
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    token = draw(left, sums, runs, part, buf, lane);
+    token = draw(w.left, sums, runs, part, buf, lane);
   }
   if (lane == 0) a.next[i] = token;
 }
@@ -367,13 +397,13 @@ int verify_rounds(int32_t seqs, int64_t nodes, int32_t vocab, bool draft) {
 
 hipError_t launch_verify(const VerifyArgs& a, hipStream_t s) {
   const int64_t blocks = (int64_t)a.seqs * ((a.vocab + 4 * kRun - 1) / (4 * kRun));
-  if (!fits_launch(a.seqs, 1024) || (a.rounds && !fits_launch(blocks, 256))) return hipErrorInvalidConfiguration;
+  if (!fits_launch(a.seqs, 64 * dev::kWaves) || (a.rounds && !fits_launch(blocks, 256))) return hipErrorInvalidConfiguration;
   for (int k = 0; k < a.rounds; ++k) {
     hipLaunchKernelGGL(dev::sum_kernel, dim3((unsigned)blocks), dim3(256), 0, s, a, k);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL(dev::verify_kernel, dim3((unsigned)a.seqs), dim3(1024), 0, s, a);
+  hipLaunchKernelGGL(dev::verify_kernel, dim3((unsigned)a.seqs), dim3(64 * dev::kWaves), 0, s, a);
   return hipGetLastError();
 }
 

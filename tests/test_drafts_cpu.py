@@ -111,7 +111,7 @@ def test_verify_workspace():
     assert need(vocab=8192) == 0 and need(seqs=0, vocab=100_000) == 0
     for kw in (dict(vocab=8193), dict(vocab=131_072), dict(vocab=131_072, draft=None), dict(vocab=1 << 22, nodes=99)):
         size = need(**kw)
-        assert 0 < size <= 3 * (4 * kw["vocab"] // 256 + 4096)
+        assert 0 < size <= 3 * 4 * (kw["vocab"] // 256 + 2048)
         b = ctypes.byref(draft(**kw))
         assert L.lsq_verify_tree(b, None, size, None) == 1
         assert L.lsq_verify_tree(b, FAKE + 8, size, None) == 1
