@@ -466,8 +466,23 @@ lsq_status lsq_state_load_slots(lsq_state* dst, const lsq_state* src, int32_t co
  * negative slots, are not written.  A slot >= batch, a tree of more than
  * max_nodes nodes and one with a parent outside [-1, j) are refused on the
  * device: their output rows are filled with NaN.  The step index does not
- * move.  Alignment and errors as lsq_attend (no workspace); INVALID_ARG also:
- * max_nodes < 1, null or misaligned parents; UNSUPPORTED also: max_nodes > 64. */
+ * move.  max_nodes also chooses the kernel's size (16, 32 or 64 nodes).
+ *
+ * The nodes are worked together on the matrix cores, the state read once.  fp32
+ * outputs keep fp32 accuracy; the operands of a 16-bit output are held to 16
+ * bits: before its one rounding it is off by at most 2^-16 of the sum of its
+ * terms' magnitudes (under the delta rule, where those of v and of S k both
+ * count at every node above, 2^-13: each of up to four tiles of 16 nodes adds
+ * 7 2^-18), beside fp32's own rounding.  |alpha| is at most 1; a
+ * negative one is taken as it stands; under a scalar decay one below 2^-126 in
+ * magnitude counts as 0.  An input that is not finite makes outputs NaN or
+ * infinite on its node and the nodes behind it, v its own value column alone,
+ * q its own node alone; nothing reaches a node off its paths or another head.
+ *
+ * Alignment and errors as lsq_attend (no workspace); INVALID_ARG also:
+ * max_nodes < 1, null or misaligned parents; UNSUPPORTED: a quantised handle,
+ * max_nodes > 64, a token stride of 2^31 elements or more, or a launch of 2^32
+ * threads or more. */
 lsq_status lsq_step_tree(const lsq_state* st, const lsq_token_batch* batch, const int32_t* parents,
                          int32_t max_nodes, void* stream);
 
@@ -479,7 +494,7 @@ lsq_status lsq_step_tree(const lsq_state* st, const lsq_token_batch* batch, cons
  * taken by an earlier entry, a length above depth, and a node outside the
  * entry's tree are refused on the device: the state stays as it was.  The
  * arithmetic is lsq_step_slots', token by token in fp32, whatever the io type.
- * depth = 0 does nothing.  Errors as lsq_step_tree; INVALID_ARG also: null or
+ * depth = 0 does nothing.  Errors as lsq_step_slots; INVALID_ARG also: null or
  * misaligned path or lengths, depth < 0; UNSUPPORTED also: depth > 64. */
 lsq_status lsq_accept_path(lsq_state* st, const lsq_token_batch* batch, const int32_t* path,
                            const int32_t* lengths, int32_t depth, void* stream);

@@ -406,14 +406,16 @@ class LsqState:
         ``attend`` with one token per entry and strides of any length.  Returns o [entries, heads, dv]."""
         return _slots().step_slots(self, q, k, v, alpha, beta, slots, fresh, o, stream)
 
-    def step_tree(self, q, k, v, alpha, beta, cu_nodes, parents, slots=None, fresh=None, max_nodes=64,
+    def step_tree(self, q, k, v, alpha, beta, cu_nodes, parents, slots=None, fresh=None, max_nodes=None,
                   o=None, stream=None):
         """The recurrence along every path of a tree of drafted tokens for each listed slot
         (``lsq_step_tree``), on an fp32 state, which is left as it is.
 
-        The tensors of ``attend`` with one row per node (strides of any length); cu_nodes int32
+        The tensors of ``attend`` with one row per node (strides below 2^31 elements); cu_nodes int32
         [seqs + 1] the trees' offsets; parents int32 [nodes], within the tree: -1 or an earlier node;
-        max_nodes (at most 64) bounds a tree's nodes.  Returns o [nodes, heads, dv] in q's type."""
+        max_nodes (at most 64, the default unless there are fewer rows) bounds a tree's nodes: it
+        chooses the kernel's size, so a program that knows a smaller bound gives it.  Returns o
+        [nodes, heads, dv] in q's type."""
         return _drafts().step_tree(self, q, k, v, alpha, beta, cu_nodes, parents, slots, fresh, max_nodes,
                                    o, stream)
 

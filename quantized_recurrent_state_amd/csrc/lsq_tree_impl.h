@@ -56,7 +56,9 @@ __device__ __forceinline__ uint64_t path_mask(int parent, int lane, double& x) {
 //
 // Precision: every operand is a sum of bf16 parts and the products of parts
 // i + j < N are added; N = 3 (fp32) for fp32 inputs, N = 2 for 16-bit ones, whose
-// outputs are rounded to 8 or 11 bits and whose states are not written.
+// outputs are rounded to 8 or 11 bits and whose states are not written.  With N = 2
+// a part's rounding and the product left out are 2^-18 each: S q lacks 2 2^-18 of its
+// terms, P w 3 2^-18, and a tile's w under the delta rule 7 2^-18 (S k and M w before T).
 //
 // What is not finite would reach other paths through the zeros of P, M and T.  A
 // w that is not counts as 0, and the outputs behind its node in its column become

@@ -17,7 +17,8 @@ def step_tree(state, q, k, v, alpha, beta, cu_nodes, parents, slots, fresh, max_
     def call(s):
         b, out = token_batch(state, q, k, v, alpha, beta, cu_nodes, slots, fresh, o)
         pp = _plain("parents", parents, (b.tokens,), torch.int32, out.get_device())
-        status = _lib.load().lsq_step_tree(state.handle, ctypes.byref(b), pp, int(max_nodes), s)
+        most = min(64, b.tokens or 1) if max_nodes is None else int(max_nodes)
+        status = _lib.load().lsq_step_tree(state.handle, ctypes.byref(b), pp, most, s)
         if status:
             _lib.check(status, "lsq_step_tree")
         return out

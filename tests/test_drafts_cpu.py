@@ -213,3 +213,16 @@ def test_the_rule_keeps_the_targets_distribution(drawn):
             left, _ = residual(p, rows, (x, y), drawn == "with")
             total += reach * left / left.sum() if float(left.sum()) else 0.0
         assert float((total - p).abs().max()) < 1e-12
+
+
+@pytest.mark.skipif(torch.cuda.device_count() > 0, reason="its made-up addresses must not reach a GPU")
+@pytest.mark.parametrize("name", ["q_stride", "k_stride", "v_stride", "o_stride"])
+def test_a_tree_of_far_rows_is_refused(name):
+    """Strides below 2^31 elements pass every check and end with the launch's own error (HIP) on a host
+    without a GPU; an accepted path takes any."""
+    h = handle()
+    for stride, status in (((1 << 31) - 8, 5), (1 << 31, 2), (1 << 40, 2), ((1 << 63) - 256, 2)):
+        b = batch(**{name: stride})
+        assert tree(h, b) == status, stride
+        assert accept(h, b) == 5
+    lsq.lsq_state_free(h)
