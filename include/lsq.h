@@ -527,7 +527,7 @@ typedef struct {
 } lsq_draft_batch;
 
 /* Bytes of workspace lsq_verify_tree needs for this batch (0 for vocabularies of
- * up to 8192 tokens).  Host only; depends on seqs, nodes, vocab and whether draft
+ * up to 65536 tokens).  Host only; depends on seqs, nodes, vocab and whether draft
  * is NULL alone. */
 lsq_status lsq_verify_workspace(const lsq_draft_batch* batch, size_t* bytes);
 

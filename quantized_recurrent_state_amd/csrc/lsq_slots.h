@@ -83,7 +83,7 @@ struct PathArgs {
 };
 
 constexpr int kMaxVocab = 1 << 22;
-constexpr int kRun = 2048;   // elements of a row that are summed together
+constexpr int kRun = 1024;   // elements of a row that are summed together
 
 struct VerifyArgs {
   const float* target;     // [nodes] rows target_stride elements apart

@@ -77,8 +77,8 @@ struct Residual {
     const int e0 = r * kRun, e1 = min(vocab, e0 + kRun);
     const uint64_t any = any_in(e0, e1);
     double sum = 0.0;
-#pragma unroll 4
-    for (int y = 0; y < kRun; y += 256) {        // nothing behind the row
+#pragma unroll
+    for (int y = 0; y < kRun; y += 256) {        // all in flight; nothing behind the row
       double x[4];
       four(e0 + y + 4 * lane, any, x);
       sum += (x[0] + x[1]) + (x[2] + x[3]);
@@ -327,7 +327,7 @@ __global__ __launch_bounds__(256) void sum_kernel(VerifyArgs a, int k) {
 
 // What the launches above left to do: the token of each entry, by one wave, and
 // before it the walks that need more sums, with the whole workgroup.
-constexpr int kWaves = 16;                        // of verify_kernel: a run's elements are in flight at once
+constexpr int kWaves = 16;                       // of verify_kernel
 
 __global__ __launch_bounds__(64 * kWaves) void verify_kernel(VerifyArgs a) {
   __shared__ double sums[kMaxRuns], buf[kRun / 64];
@@ -382,16 +382,16 @@ __global__ __launch_bounds__(64 * kWaves) void verify_kernel(VerifyArgs a) {
 
 }  // namespace dev
 
-// A sum made by a launch of its own takes about 5 us and 2.6 of the host, an idle
-// launch 1.2; the entry's own workgroup takes 10 us for rows of 131072 tokens, and
-// 2 for 16384.  The host does not see the trees: a chain asks for one sum, trees of 11
-// nodes for four to five where they ask most (64 of them, 131072 tokens: 72 us
-// without such launches, 69, 65, 53, 50 and 52 with one to five; one chain of five
-// nodes, 65536 tokens: 16.1, 16.1, 18.7, 21.3).
+// An entry's own workgroup reads 60-110 GB/s: rows of 512 KiB and less are best left
+// to it (one chain of five nodes, 65536 tokens: 14.3 us per call without launches
+// for sums, 17.2, 19.9 and 22.9 with one to three, of which the host takes 2.6 each).
+// Larger ones are split over the chip, by a launch for each sum; one that no entry
+// needs takes 2-4 us.  The host does not see the trees: a chain asks for one sum,
+// trees of 11 nodes for up to four (64 of them, 131072 tokens: 73 us without, 69, 60,
+// 45, 43 and 46 with one to five).  Without a draft's row there is one sum.
 int verify_rounds(int32_t seqs, int64_t nodes, int32_t vocab, bool draft) {
-  if (vocab <= 4 * kRun || seqs == 0) return 0;
-  if (!draft || vocab < (1 << 15)) return 1;     // without a draft's row there is one sum
-  const int64_t rounds = (nodes / seqs - 3) / 2;
+  if ((draft ? 2 : 1) * (int64_t)vocab <= 1 << 17 || seqs == 0) return 0;
+  const int64_t rounds = draft ? (nodes / seqs - 3) / 2 : 1;
   return rounds < 1 ? 1 : rounds > 4 ? 4 : (int)rounds;
 }
 

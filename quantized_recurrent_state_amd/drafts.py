@@ -75,7 +75,7 @@ def draft_batch(target, tokens, parents, cu_nodes, uniform, uniform_next, draft,
     b = _lib.lsq_draft_batch(m, vocab, depth, 1 if replacement else 0, n, ts, ds, tp, dp, ip, pp, cp, up, np,
                              None, None, None)
     nb = 0
-    if vocab > 8192:                         # smaller rows need no workspace
+    if vocab > 65536:                        # smaller rows need no workspace
         need = ctypes.c_size_t()
         status = _lib.load().lsq_verify_workspace(ctypes.byref(b), ctypes.byref(need))
         if status:

@@ -108,10 +108,10 @@ def test_verify_workspace():
     """Small vocabularies need none; larger ones a bounded one, which is checked."""
     L, n = _lib.load(), ctypes.c_size_t(1)
     need = lambda **kw: (L.lsq_verify_workspace(ctypes.byref(draft(**kw)), ctypes.byref(n)), n.value)[1]
-    assert need(vocab=8192) == 0 and need(seqs=0, vocab=100_000) == 0
-    for kw in (dict(vocab=8193), dict(vocab=131_072), dict(vocab=131_072, draft=None), dict(vocab=1 << 22, nodes=99)):
+    assert need(vocab=65536) == 0 and need(seqs=0, vocab=100_000) == 0
+    for kw in (dict(vocab=65537), dict(vocab=131_072), dict(vocab=131_073, draft=None), dict(vocab=1 << 22, nodes=99)):
         size = need(**kw)
-        assert 0 < size <= 3 * 4 * (kw["vocab"] // 256 + 2048)
+        assert 0 < size <= 3 * 4 * (kw["vocab"] // 128 + 2048)
         b = ctypes.byref(draft(**kw))
         assert L.lsq_verify_tree(b, None, size, None) == 1
         assert L.lsq_verify_tree(b, FAKE + 8, size, None) == 1

@@ -673,7 +673,7 @@ def _tree_case(seed=1, delta=1):
 def test_replayed_graphs_take_other_slots_trees_and_paths():
     """One captured run of tree, verification and acceptance, replayed with other contents in the same
     buffers and eager work between: every replay is what eager calls give."""
-    vocab, dk = 20000, 128
+    vocab, dk = 70001, 128
     st, _ = state(6, 4, dk, 128, 1)
     ref, _ = state(6, 4, dk, 128, 1)
     x, cu, parents, counts = _tree_case()
@@ -728,7 +728,7 @@ def test_calls_on_other_streams():
     for seed in (1, 2):
         st, _ = state(4, 4, 128, 128, 1, seed=seed)
         x, cu, parents, counts = _tree_case(seed)
-        d = drafts(counts, 40000, "random", seed, "without")
+        d = drafts(counts, 70001, "random", seed, "without")
         rows = [d[n].to(DEV) for n in ("target", "ids", "uniform", "uniform_next", "draft")]
         runs.append((st, x, cu, parents, rows, i32(*d["parents"]), torch.cuda.Stream()))
     torch.cuda.synchronize()
@@ -778,9 +778,20 @@ def test_verify_many_entries():
     for a in d["cu"][:-1]:
         d["parents"][a] = -1
     check_verify(d, "without", depth=5)
-    d = drafts([4] * 40, 33000, "star", 2, "with")       # several sums in the entries' own workgroups
-    check_verify(d, "with", depth=5)
-    d = drafts([12] * 5, 33000, "star", 3, "with", error=2.5)    # and by launches
-    check_verify(d, "with", depth=5)
-    d = drafts([14] * 5, 40001, "star", 3, "without", error=2.5)
-    check_verify(d, "without", depth=5)
+
+
+@pytest.mark.parametrize("drawn", DRAWN)
+@pytest.mark.parametrize("counts", [[1, 2, 0], [7, 8], [9, 10, 1, 17], [16, 17, 20]], ids=str)
+def test_verify_several_sums(drawn, counts):
+    """Large rows of trees of several sizes, where most children are rejected: sums by launches of their
+    own, fewer and more than the entries need."""
+    most = 0
+    for seed, vocab in ((1, 70001), (2, 140000)):
+        d = drafts(counts, vocab, "star" if seed == 1 else "random", seed, drawn, error=2.5)
+        for a, c in zip(d["cu"], counts):
+            if c:
+                d["parents"][a] = -1
+                d["parents"][a + 1:a + c] = [max(0, p) for p in d["parents"][a + 1:a + c]]
+        lengths = check_verify(d, drawn, depth=5)[1]
+        most = max(most, max(c - n for c, n in zip(counts, lengths)))
+    assert most >= max(counts) // 3                      # nodes that were not accepted
