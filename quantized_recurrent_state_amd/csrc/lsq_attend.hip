@@ -85,21 +85,6 @@ __device__ __forceinline__ f32x4 widen_bf16x4(bf16x4 p) {
                __uint_as_float(hi & 0xFFFF0000u)};
 }
 
-// Two values rounded once to a 16-bit type.
-template <int IO>
-__device__ __forceinline__ uint32_t pair16(float x, float y) {
-  if constexpr (IO == IO_BF16) return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{x, y}, bf16x2));
-  else return to16<IO_F16>(x) | (uint32_t)to16<IO_F16>(y) << 16;
-}
-
-// Four values of a column from four consecutive rows of a row-major LDS tile:
-// lane 16 g + i points at row 4 g + i / 4, column 4 (i % 4) of a 16 x 16 block
-// and receives rows 4 g .. 4 g + 3 of column i.
-__device__ __forceinline__ bf16x4 read_column4(const __bf16* p) {
-  return __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                                        (__attribute__((address_space(3))) s16x4*)p));
-}
-
 // Decays of N tokens, by token; chunk borders are every 32 tokens.
 template <int N>
 struct Decays {

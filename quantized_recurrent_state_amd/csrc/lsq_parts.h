@@ -5,6 +5,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "lsq_slots_dev.h"
+
 namespace lsq {
 namespace dev {
 
@@ -43,6 +45,21 @@ __device__ __forceinline__ bf16x8 join(bf16x4 a, bf16x4 b) {
 
 __device__ __forceinline__ f32x4 mfma(bf16x8 a, bf16x8 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+
+// Two values rounded once to a 16-bit type.
+template <int IO>
+__device__ __forceinline__ uint32_t pair16(float x, float y) {
+  if constexpr (IO == IO_BF16) return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{x, y}, bf16x2));
+  else return to16<IO_F16>(x) | (uint32_t)to16<IO_F16>(y) << 16;
+}
+
+// Four values of a column from four consecutive rows of a row-major LDS tile:
+// lane 16 g + i points at row 4 g + i / 4, column 4 (i % 4) of a 16 x 16 block
+// and receives rows 4 g .. 4 g + 3 of column i.
+__device__ __forceinline__ bf16x4 read_column4(const __bf16* p) {
+  return __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                        (__attribute__((address_space(3))) s16x4*)p));
 }
 
 // 2^x of a double, to fp32.

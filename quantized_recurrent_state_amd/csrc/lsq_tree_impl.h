@@ -167,7 +167,7 @@ __device__ __forceinline__ void tree_head(const TreeArgs& a, char* lds, TreeNode
   const auto* const vb = behind(b.v, t0 * b.v_stride + hv);
   const float* const ab = b.alpha + (t0 * b.heads + h) * (DIAG ? DK : 1);
 
-  // ---- loads: node rows first, as they are used first
+  // ---- loads, in the order of their use: node rows, v, the state
   int parent = lane < n ? a.parents[t0 + lane] : -1;
   constexpr int EU = T::EU, ROWU = DK / EU;      // units of a row
   auto unit_in = [&](int x) { return (x + 1) * 64 * NW <= N * ROWU || x * 64 * NW + tid < N * ROWU; };
@@ -199,18 +199,6 @@ __device__ __forceinline__ void tree_head(const TreeArgs& a, char* lds, TreeNode
     if constexpr (!DIAG) ra = ab[(lane < n ? lane : n - 1) * b.heads];
     rbeta = b.beta[(t0 + (lane < n ? lane : n - 1)) * b.heads + h];
   }
-  f32x4 s[KS][2];
-  if (b.fresh && b.fresh[i]) {
-#pragma unroll
-    for (int kk = 0; kk < KS; ++kk) s[kk][0] = s[kk][1] = f32x4{0.f, 0.f, 0.f, 0.f};
-  } else {
-    const float* S = b.S + (((int64_t)slot * b.heads + h) * b.dv + rowc) * DK + 4 * g;
-#pragma unroll
-    for (int kk = 0; kk < KS; ++kk)
-#pragma unroll
-      for (int y = 0; y < 2; ++y)
-        s[kk][y] = a.nt ? load_state<true>(S + 32 * kk + 16 * y) : load_state<false>(S + 32 * kk + 16 * y);
-  }
   typename Raw<IO>::One rv[T::STAGED ? 1 : NT][4];           // this lane's, or units of all columns
   u32x4 rvu[T::STAGED ? T::VUNITS : 1];
   const int col0 = rb * T::C;                    // the workgroup's first value column
@@ -235,6 +223,18 @@ __device__ __forceinline__ void tree_head(const TreeArgs& a, char* lds, TreeNode
 #pragma unroll
       for (int r = 0; r < 4; ++r) rv[t][r] = vb[at_node(16 * t + 4 * g + r, b.v_stride) + rowc];
   }
+  f32x4 s[KS][2];
+  if (b.fresh && b.fresh[i]) {
+#pragma unroll
+    for (int kk = 0; kk < KS; ++kk) s[kk][0] = s[kk][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+  } else {
+    const float* S = b.S + (((int64_t)slot * b.heads + h) * b.dv + rowc) * DK + 4 * g;
+#pragma unroll
+    for (int kk = 0; kk < KS; ++kk)
+#pragma unroll
+      for (int y = 0; y < 2; ++y)
+        s[kk][y] = a.nt ? load_state<true>(S + 32 * kk + 16 * y) : load_state<false>(S + 32 * kk + 16 * y);
+  }
 
   // ---- paths and decays.  A tree with a parent that is no earlier node is worked
   // as if it had none, so that no load waits for this one, and its outputs are NaN.
@@ -258,30 +258,31 @@ __device__ __forceinline__ void tree_head(const TreeArgs& a, char* lds, TreeNode
     if (lane == 0) nl.spoilt = 0;
   }
 
-  // A tile of S's products' decayed cousins: rows tj of P (or M) at columns ti.
+  // Tile (tj, ti) of P or M, from the rows of q or k: a lane has row 16 tj + lc at
+  // columns 16 ti + 4 g .. + 3.
   auto gram = [&](const __bf16* rows, int tj, int ti) {
     f32x4 d = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int kk = 0; kk < KS; ++kk) {
       bf16x8 x[NR], y[NR];
-      get8<NR>(rows + (16 * tj + lc) * PK + 32 * kk + 8 * g, kRow, x);
-      get8<NR>(kl + (16 * ti + lc) * PK + 32 * kk + 8 * g, kRow, y);
+      get8<NR>(kl + (16 * ti + lc) * PK + 32 * kk + 8 * g, kRow, x);
+      get8<NR>(rows + (16 * tj + lc) * PK + 32 * kk + 8 * g, kRow, y);
       d = mfma_parts<NO>(x, y, d);
     }
-    const int col = 16 * ti + lc, j0 = 16 * tj + 4 * g;
-    const float hc = nl.hi[col], lo = nl.lo[col];
-    const f32x4 hj = *reinterpret_cast<const f32x4*>(&nl.hi[j0]), lj = *reinterpret_cast<const f32x4*>(&nl.lo[j0]);
-    const u32x4 on = *reinterpret_cast<const u32x4*>(&nl.on[ti >> 1][j0]);
+    const int j = 16 * tj + lc, i0 = 16 * ti + 4 * g;
+    const float hj = nl.hi[j], lj = nl.lo[j];
+    const f32x4 hi = *reinterpret_cast<const f32x4*>(&nl.hi[i0]), lo = *reinterpret_cast<const f32x4*>(&nl.lo[i0]);
+    const uint32_t on = nl.on[ti >> 1][j] >> (i0 & 31);
     const uint64_t neg = nl.neg;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      float x = __builtin_amdgcn_exp2f((hj[r] - hc) + (lj[r] - lo)) * d[r];
+      float x = __builtin_amdgcn_exp2f((hj - hi[r]) + (lj - lo[r])) * d[r];
       if (neg) {
-        const uint32_t n0 = (uint32_t)neg & (nl.on[0][j0 + r] ^ nl.on[0][col]);
-        const uint32_t n1 = (uint32_t)(neg >> 32) & (nl.on[1][j0 + r] ^ nl.on[1][col]);
+        const uint32_t n0 = (uint32_t)neg & (nl.on[0][j] ^ nl.on[0][i0 + r]);
+        const uint32_t n1 = (uint32_t)(neg >> 32) & (nl.on[1][j] ^ nl.on[1][i0 + r]);
         x = (__popc(n0) + __popc(n1)) & 1 ? -x : x;
       }
-      d[r] = on[r] >> (col & 31) & 1 ? x : 0.f;
+      d[r] = on >> r & 1 ? x : 0.f;
     }
     return d;
   };
@@ -378,19 +379,8 @@ __device__ __forceinline__ void tree_head(const TreeArgs& a, char* lds, TreeNode
       for (int x = 0; x < T::TASKS; ++x) {
         int tj, ti;
         bool m;
-        if (task(x * NW + NW - 1 - wave, tj, ti, m)) {
-          __bf16* to = (m ? mp : pp) + (16 * tj + 4 * g) * PW + slot_order(16 * ti + lc);
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            float y = done[x][r];
-#pragma unroll
-            for (int p = 0; p < NO; ++p) {
-              const __bf16 part = (__bf16)y;
-              to[p * kPart + r * PW] = part;
-              y -= (float)part;
-            }
-          }
-        }
+        if (task(x * NW + NW - 1 - wave, tj, ti, m))
+          put4<NO>((m ? mp : pp) + (16 * tj + lc) * PW + slot_order(16 * ti + 4 * g), kPart, done[x]);
       }
     }
   };
@@ -415,8 +405,7 @@ __device__ __forceinline__ void tree_head(const TreeArgs& a, char* lds, TreeNode
       if (wave < NT) {
         const f32x4 d = gram(kl, wave, wave);
         float* m = ml + wave * 16 * PT;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) m[(4 * g + r) * PT + lc] = d[r];
+        *reinterpret_cast<f32x4*>(m + lc * PT + 4 * g) = d;
         invert(wave, m, PT);
       }
     }
@@ -525,7 +514,8 @@ __device__ __forceinline__ void tree_head(const TreeArgs& a, char* lds, TreeNode
       if (wave < NT) invert(wave, ml + 16 * wave * PP + 16 * wave, PP);
   }
 
-  // ---- S q and S k
+  // ---- S q and S k: q's with the lane's node 16 t + lc and value columns 4 g .. + 3,
+  // as the outputs are stored, k's with column lc and nodes 4 g .. + 3, as w is an operand
   f32x4 xq[NT], xk[DELTA ? NT : 1];
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
@@ -545,7 +535,7 @@ __device__ __forceinline__ void tree_head(const TreeArgs& a, char* lds, TreeNode
       const int at = (16 * t + lc) * PK + 32 * kk + 8 * g;
       bf16x8 x[NR];
       get8<NR>(ql + at, kRow, x);
-      xq[t] = mfma_parts<NO>(x, sp8, xq[t]);
+      xq[t] = mfma_parts<NO>(sp8, x, xq[t]);
       if constexpr (DELTA) {
         get8<NR>(kl + at, kRow, x);
         xk[t] = mfma_parts<NO>(x, sp8, xk[t]);
@@ -586,10 +576,13 @@ __device__ __forceinline__ void tree_head(const TreeArgs& a, char* lds, TreeNode
   for (int t = 0; t < NT; ++t) {
     const f32x4 beta = *reinterpret_cast<const f32x4*>(&nl.beta[16 * t + 4 * g]);
     f32x4 x;
+    if constexpr (T::STAGED) {
+      const bf16x4 v = read_column4(reinterpret_cast<const __bf16*>(vl) + (16 * t + 4 * g + lc / 4) * T::PC + 16 * wave + 4 * (lc & 3));
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      if constexpr (T::STAGED) x[r] = widen<IO>(vl[(16 * t + 4 * g + r) * T::PC + 16 * wave + lc]);
-      else x[r] = widen<IO>(rv[t][r]);
+      for (int r = 0; r < 4; ++r) x[r] = widen<IO>((uint16_t)(__builtin_bit_cast(uint64_t, v) >> 16 * r));
+    } else {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) x[r] = widen<IO>(rv[t][r]);
     }
     if constexpr (DELTA) {
       f32x4 y = xk[t];
@@ -630,14 +623,14 @@ __device__ __forceinline__ void tree_head(const TreeArgs& a, char* lds, TreeNode
   // ---- o
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
-    if constexpr (!DIAG) xq[t] *= *reinterpret_cast<const f32x4*>(&nl.g[16 * t + 4 * g]);
+    if constexpr (!DIAG) xq[t] *= nl.g[16 * t + lc];
 #pragma unroll
     for (int u = 0; u <= t; u += 2) {
       bf16x8 p[NO], x[NO];
       operand(pl, pp, t, u, u + 1 <= t, p);
 #pragma unroll
       for (int y = 0; y < NO; ++y) x[y] = join(w[u][y], u + 1 <= t ? w[u + 1 < NT ? u + 1 : u][y] : bf16x4{});
-      xq[t] = mfma_parts<NO>(p, x, xq[t]);
+      xq[t] = mfma_parts<NO>(x, p, xq[t]);
     }
   }
   const unsigned long long rows = DELTA ? nl.spoilt : 0;
@@ -651,22 +644,31 @@ __device__ __forceinline__ void tree_head(const TreeArgs& a, char* lds, TreeNode
     lo |= (uint32_t)rows;
     hi |= (uint32_t)(rows >> 32);
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
+    for (int r = 0; r < 4; ++r) {
+      const uint32_t l = __shfl((int)lo, 4 * g + r), h2 = __shfl((int)hi, 4 * g + r);
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int j = 16 * t + 4 * g + r;
-        if (refused || (lo & nl.on[0][j]) != 0 || (hi & nl.on[1][j]) != 0) xq[t][r] = __uint_as_float(0x7FC00000u);
-      }
+      for (int t = 0; t < NT; ++t)
+        if (refused || (l & nl.on[0][16 * t + lc]) != 0 || (h2 & nl.on[1][16 * t + lc]) != 0)
+          xq[t][r] = __uint_as_float(0x7FC00000u);
+    }
   }
   auto* const ob = static_cast<typename Raw<IO>::One*>(b.o) + t0 * b.o_stride + hv;
 #pragma unroll
-  for (int t = 0; t < NT; ++t)
+  for (int t = 0; t < NT; ++t) {
+    const int j = 16 * t + lc, c = row0 + 4 * g;
+    if constexpr (T::STAGED) {                   // in v's place: no other wave reads these columns
+      *reinterpret_cast<u32x2*>(&vl[j * T::PC + 16 * wave + 4 * g]) = u32x2{pair16<IO>(xq[t][0], xq[t][1]), pair16<IO>(xq[t][2], xq[t][3])};
+    } else if (j < n) {
+      float* to = ob + (uint64_t)(uint32_t)j * (uint32_t)b.o_stride + c;
+      if (a.wide) {
+        if (c < b.dv) *reinterpret_cast<f32x4*>(to) = xq[t];
+      } else {
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int j = 16 * t + 4 * g + r;
-      if constexpr (T::STAGED) vl[j * T::PC + 16 * wave + lc] = to16<IO>(xq[t][r]);   // v's: no other wave reads them
-      else if (j < n && row < b.dv) store1<IO>(ob, (uint64_t)(uint32_t)j * (uint32_t)b.o_stride + row, xq[t][r]);
+        for (int r = 0; r < 4; ++r)
+          if (c + r < b.dv) to[r] = xq[t][r];
+      }
     }
+  }
   if constexpr (T::STAGED) {
     __syncthreads();
 #pragma unroll
