@@ -31,7 +31,33 @@ __device__ __forceinline__ Four load4(const float* p) {
   return f;
 }
 
-__device__ __forceinline__ double shfl_up(double x, int n) { return __shfl_up(x, n); }
+// x of the lane that a DPP control names, 0 where it names none or the row is
+// masked out.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp(double x) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = __builtin_amdgcn_update_dpp(0u, (uint32_t)b, CTRL, ROWS, 0xF, false);
+  const uint32_t hi = __builtin_amdgcn_update_dpp(0u, (uint32_t)(b >> 32), CTRL, ROWS, 0xF, false);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+
+// Inclusive sums over the lanes.
+__device__ __forceinline__ double scan(double x) {
+  x += dpp<0x111, 0xF>(x);                       // row_shr 1, 2, 4, 8: within 16 lanes
+  x += dpp<0x112, 0xF>(x);
+  x += dpp<0x114, 0xF>(x);
+  x += dpp<0x118, 0xF>(x);
+  x += dpp<0x142, 0xA>(x);                       // row_bcast 15 into rows 1 and 3: within 32
+  x += dpp<0x143, 0xC>(x);                       // row_bcast 31 into rows 2 and 3
+  return x;
+}
+
+__device__ __forceinline__ double lane_of(double x, int lane) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)b, lane);
+  const uint32_t hi = __builtin_amdgcn_readlane((uint32_t)(b >> 32), lane);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
 
 // What is left of a node's target row: max(p - c q, 0), or p without the tokens
 // that the lanes hold in gone (-1: none) where the drafts have no probabilities.
@@ -72,40 +98,40 @@ struct Residual {
 
   __device__ __forceinline__ uint64_t any_in(int e0, int e1) const { return __ballot(gone >= e0 && gone < e1); }
 
-  // The sum of run r, in every lane.
-  __device__ __forceinline__ double run(int r, int lane) const {
+  // This lane's share of run r: four elements of every 256.
+  __device__ __forceinline__ double share(int r, int lane) const {
     const int e0 = r * kRun, e1 = min(vocab, e0 + kRun);
     const uint64_t any = any_in(e0, e1);
     double sum = 0.0;
+    if (e0 + kRun <= vocab && !any) {            // no branch between the loads: all in flight
+      Four a[kRun / 256], b[kRun / 256] = {};
 #pragma unroll
-    for (int y = 0; y < kRun; y += 256) {        // all in flight; nothing behind the row
+      for (int y = 0; y < kRun / 256; ++y) {
+        a[y] = load4(p + e0 + 256 * y + 4 * lane);
+        if (q) b[y] = load4(q + e0 + 256 * y + 4 * lane);
+      }
+#pragma unroll
+      for (int y = 0; y < kRun / 256; ++y)
+        sum += (of(a[y].x[0], b[y].x[0]) + of(a[y].x[1], b[y].x[1])) + (of(a[y].x[2], b[y].x[2]) + of(a[y].x[3], b[y].x[3]));
+      return sum;
+    }
+#pragma unroll
+    for (int y = 0; y < kRun; y += 256) {        // nothing behind the row
       double x[4];
       four(e0 + y + 4 * lane, any, x);
       sum += (x[0] + x[1]) + (x[2] + x[3]);
     }
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o);
     return sum;
   }
 };
 
-// Inclusive sums over the lanes.
-__device__ __forceinline__ double scan(double x, int lane) {
-#pragma unroll
-  for (int o = 1; o < 64; o *= 2) {
-    const double up = shfl_up(x, o);
-    if (lane >= o) x += up;
-  }
-  return x;
-}
-
 // The first lane whose inclusive sum (from base on) passes the threshold; where
 // rounding leaves none, the last with something in it.  before: the sum up to it.
 __device__ __forceinline__ int first_past(double own, double base, double threshold, int lane, double* before) {
-  const double up = base + scan(own, lane);
+  const double up = base + scan(own);
   const uint64_t past = __ballot(up > threshold && own > 0.0), some = __ballot(own > 0.0);
   const int at = past ? __builtin_ctzll(past) : some ? 63 - __builtin_clzll(some) : -1;
-  if (at >= 0) *before = __shfl(up - own, at);
+  if (at >= 0) *before = lane_of(up - own, at);
   return at;
 }
 
@@ -113,8 +139,8 @@ __device__ __forceinline__ int first_past(double own, double base, double thresh
 __device__ __forceinline__ double total_of(const double* sums, int runs, int lane) {
   double total = 0.0;
   for (int r0 = 0; r0 < runs; r0 += 64) {
-    const double up = total + scan(r0 + lane < runs ? sums[r0 + lane] : 0.0, lane);
-    total = __shfl(up, 63);
+    const double up = total + scan(r0 + lane < runs ? sums[r0 + lane] : 0.0);
+    total = lane_of(up, 63);
   }
   return total;
 }
@@ -128,15 +154,15 @@ __device__ __forceinline__ int draw(const Residual& left, const double* sums, in
   double before = 0.0, sum = 0.0;
   for (int r0 = 0; r0 < runs; r0 += 64) {
     const double own = r0 + lane < runs ? sums[r0 + lane] : 0.0;
-    const double up = sum + scan(own, lane);
+    const double up = sum + scan(own);
     const uint64_t over = __ballot(up > threshold && own > 0.0), some = __ballot(own > 0.0);
     if (over || some) {                          // the last run with something, until one passes
       const int at = over ? __builtin_ctzll(over) : 63 - __builtin_clzll(some);
       run = r0 + at;
-      before = __shfl(up - own, at);
+      before = lane_of(up - own, at);
     }
     if (over) break;
-    sum = __shfl(up, 63);
+    sum = lane_of(up, 63);
   }
   if (run < 0) return -1;
   constexpr int E = kRun / 64;                   // elements in a row per lane
@@ -316,8 +342,8 @@ __global__ __launch_bounds__(256) void sum_kernel(VerifyArgs a, int k) {
   }
   const bool whole = w.sound && w.run([] { return -1.0; });
   if (w.sound) {                                 // the walk's last sum is the one that the next token is drawn from
-    const double x = w.left.run(r, lane);
-    if (lane == 0) sums_of(a, k, i, runs)[r] = x;
+    const double x = scan(w.left.share(r, lane));
+    if (lane == 63) sums_of(a, k, i, runs)[r] = x;
   }
   if (r != 0) return;
   w.save(now, !w.sound ? -1 : whole ? k + 1 : 0);
@@ -337,10 +363,14 @@ __global__ __launch_bounds__(64 * kWaves) void verify_kernel(VerifyArgs a) {
   const int done = a.rounds ? saved_of(a, last, i, runs)->done : 0;
   if (done < 0 || (done && wave != 0)) return;
   const double* from = sums;
-  auto sum_runs = [&](const Residual& left, int first, int step) {
-    for (int r = first; r < runs; r += step) {
-      const double x = left.run(r, lane);
-      if (lane == 0) sums[r] = x;
+  auto sum_runs = [&](const Residual& left, int first, int step) __attribute__((always_inline)) {
+    for (int r = first; r < runs; r += 2 * step) {
+      const double x = left.share(r, lane), y = r + step < runs ? left.share(r + step, lane) : 0.0;
+      const double sx = scan(x), sy = scan(y);
+      if (lane == 63) {
+        sums[r] = sx;
+        if (r + step < runs) sums[r + step] = sy;
+      }
     }
   };
   Walk w(a, i, lane);
@@ -355,12 +385,12 @@ __global__ __launch_bounds__(64 * kWaves) void verify_kernel(VerifyArgs a) {
       if (threadIdx.x == 0) a.next[i] = -1;
       return;
     }
-    auto sum_row = [&] {
+    auto sum_row = [&]() __attribute__((always_inline)) {
       __syncthreads();
       sum_runs(w.left, wave, kWaves);
       __syncthreads();
     };
-    w.run([&] {
+    w.run([&]() __attribute__((always_inline)) {
       sum_row();
       return total_of(sums, runs, lane);
     });
