@@ -469,7 +469,8 @@ lsq_status lsq_state_load_slots(lsq_state* dst, const lsq_state* src, int32_t co
  * move.  max_nodes also chooses the kernel's size (16, 32 or 64 nodes).
  *
  * The nodes are worked together on the matrix cores, the state read once.  fp32
- * outputs keep fp32 accuracy; the operands of a 16-bit output are held to 16
+ * outputs keep fp32 accuracy (magnitudes from 2^-100 to 2^127, as lsq_attend's);
+ * the operands of a 16-bit output are held to 16
  * bits: before its one rounding it is off by at most 2^-16 of the sum of its
  * terms' magnitudes (under the delta rule, where those of v and of S k both
  * count at every node above, 2^-13: each of up to four tiles of 16 nodes adds
@@ -502,7 +503,7 @@ lsq_status lsq_accept_path(lsq_state* st, const lsq_token_batch* batch, const in
 /* Trees of drafted tokens and the probabilities they are tested against.  Row j
  * of target (and draft) is the target (draft) model's distribution behind node
  * j, that of its children; consecutive rows are target_stride (draft_stride)
- * elements apart.  ids[j] is node j's token (node 0's is not read), uniform[j]
+ * elements apart.  ids[j] is node j's token (node 0's is not used), uniform[j]
  * the number in [0, 1) that decides on node j, uniform_next[i] the one that
  * draws entry i's next token.  draft NULL: the drafts have no probabilities
  * (each is certain to its model: a one-hot row).  replacement: siblings were
@@ -532,8 +533,9 @@ typedef struct {
 lsq_status lsq_verify_workspace(const lsq_draft_batch* batch, size_t* bytes);
 
 /* Verification: entry i's walk starts at node 0, which is accepted as it
- * stands, and tests the children x_1, x_2, ... of the node it is at, in order,
- * with p and q the node's target and draft row.  P_1 = p, T_1 = Q_1 = 1, c_1 = 0:
+ * stands, and tests the children x_1, x_2, ... of the node it is at, in order (a
+ * second node with parent -1 is nobody's child), with p and q the node's target
+ * and draft row.  P_1 = p, T_1 = Q_1 = 1, c_1 = 0:
  *   x_i is accepted if uniform T_i q(x_i) < P_i(x_i) Q_i, and the walk goes on
  *   there; otherwise c_i+1 = c_i + T_i / Q_i, P_i+1 = max(p - c_i+1 q, 0), T_i+1 is
  *   its sum, and Q_i+1 is 1, or without replacement 1 - q(x_1) - ... - q(x_i).

@@ -795,3 +795,59 @@ def test_verify_several_sums(drawn, counts):
         lengths = check_verify(d, drawn, depth=5)[1]
         most = max(most, max(c - n for c, n in zip(counts, lengths)))
     assert most >= max(counts) // 3                      # nodes that were not accepted
+
+
+@pytest.mark.parametrize("io", TYPES)
+@pytest.mark.parametrize("delta,diag", RULES)
+def test_tree_fast_and_slow_decays(io, delta, diag):
+    # products of decays that leave the range of fp32, and decays so near one that their logarithms matter
+    for power in (40.0, 1e-4):
+        def edit(x):
+            x["alpha"].pow_(power)
+        for kind in ("chain", "random"):
+            o, want, mag, T = run_tree([40], kind, 2, 1, 64, 64, TYPES[io], delta, diag, edit=edit)
+            check_tree(o, want, mag, T, 64, TYPES[io], delta)
+
+
+@pytest.mark.parametrize("io", TYPES)
+def test_tree_and_path_broadcast_rows(io):
+    # one row of q, k, v for all nodes (stride 0)
+    dtype, n = TYPES[io], 21
+    st, S = state(2, 4, 128, 72, 1)
+    x = list(tokens(n, 4, 2, 128, 72, dtype, 8))
+    x[:3] = [t[:1].expand_as(t) for t in x[:3]]
+    dx = [t.to(DEV) for t in x]
+    dx[:3] = [t[:1].to(DEV).expand(t.shape) for t in x[:3]]
+    parents = trees([n], "random", 6)
+    o = st.step_tree(*dx, i32(0, n), i32(*parents), slots=i32(1), max_nodes=21)
+    want, mag = tree_ref(S, [1], None, [0, n], parents, *x, delta=1)
+    check_tree(o, want, mag, n, 128, dtype, 1)
+    path = [0, 4, 20]
+    st.accept_path(*dx[1:], i32(0, n), torch.tensor([path], dtype=torch.int32, device=DEV), i32(3), slots=i32(1))
+    pool, mag = path_ref(S, [1], None, [0, n], [path], *x[1:], delta=1)
+    check_state(st, pool, mag, 3, 128, 1)
+
+
+def test_tree_without_a_bound_or_slots():
+    # max_nodes left to its default, slots to the entries' order; many value heads to a key head, an odd count
+    counts = [3, 30, 64, 1]
+    for heads, hk in ((5, 1), (16, 2), (7, 7)):
+        cu = offsets(counts)
+        st, S = state(4, heads, 64, 48, 1)
+        x = tokens(cu[-1], heads, hk, 64, 48, torch.bfloat16, 8)
+        parents = trees(counts, "random", 6)
+        o = st.step_tree(*(t.to(DEV) for t in x), i32(*cu), i32(*parents))
+        want, mag = tree_ref(S, [0, 1, 2, 3], None, cu, parents, *x, delta=1)
+        check_tree(o, want, mag, 64, 64, torch.bfloat16, 1)
+
+
+def test_states_of_large_and_small_magnitudes():
+    for scale in (2.0 ** 100, 2.0 ** -80):
+        for io in ("bf16", "f32"):
+            st, S = state(1, 2, 64, 64, 0, scale=scale)
+            x = list(tokens(20, 2, 2, 64, 64, TYPES[io], 8))
+            x[2] = (x[2].float() * scale).to(TYPES[io])
+            parents = trees([20], "random", 6)
+            o = st.step_tree(*(t.to(DEV) for t in x), i32(0, 20), i32(*parents))
+            want, mag = tree_ref(S, [0], None, [0, 20], parents, *x)
+            check_tree(o, want, mag, 20, 64, TYPES[io], 0)
