@@ -14,8 +14,8 @@
 //
 // Bound by dependent reads: the offsets, the trees, the tokens' probabilities, then a
 // row for each sum, each behind the one before (a chain of five nodes, 65536 tokens: 12
-// us; 64 trees of 6-16, 131072 tokens: 17 us for the first sums, 6-10 for each later
-// launch, 6 for the draw).
+// us; 64 trees of 6-16, 131072 tokens: 15-17 us for the first sums, 5-9 for each later
+// launch, 5 for the draw).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -25,6 +25,7 @@ namespace lsq {
 namespace dev {
 
 constexpr int kMaxRuns = kMaxVocab / kRun;       // of a row; a wave sums a run
+constexpr int kSumWaves = 4;                     // of sum_kernel (8: 39 us as below instead of 38, 16: 40)
 
 // Four floats at any 4-byte address.
 struct Four {
@@ -324,36 +325,50 @@ __device__ __forceinline__ Saved* saved_of(const VerifyArgs& a, int k, int i, in
                                   ((int64_t)k * a.seqs + i) * kSaved);
 }
 
-// The k-th sum of every entry that needs one: a wave per run.  Each wave makes the
-// entry's walk up to there by itself, from where the launch before left it; the
-// first one writes down where that is.
-__global__ __launch_bounds__(256) void sum_kernel(VerifyArgs a, int k) {
+// The k-th sum of every entry that needs one: a wave per run.  The first wave of
+// each workgroup makes the entry's walk up to there, from where the launch before
+// left it; the entry's first workgroup writes down where that is.
+__global__ __launch_bounds__(64 * kSumWaves) void sum_kernel(VerifyArgs a, int k) {
+  __shared__ double cut;
+  __shared__ int node, gone[kMaxNodes];          // node -1: nothing to sum
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int runs = (a.vocab + kRun - 1) / kRun, groups = (runs + 3) / 4;
-  const int i = blockIdx.x / groups, r = blockIdx.x % groups * 4 + wave;
-  if (r >= runs) return;
-  Saved& now = *saved_of(a, k, i, runs);
+  const int runs = (a.vocab + kRun - 1) / kRun, groups = (runs + kSumWaves - 1) / kSumWaves;
+  const int i = blockIdx.x / groups, group = blockIdx.x % groups, r = group * kSumWaves + wave;
   Walk w(a, i, lane);
-  if (k == 0) {
-    w.begin(i);
-  } else {
-    const Saved& before = *saved_of(a, k - 1, i, runs);
-    const int done = before.done;
-    if (done) {
-      if (r == 0 && lane == 0) now.done = done;
-      return;
+  if (wave == 0) {
+    Saved& now = *saved_of(a, k, i, runs);
+    int done = 0;
+    if (k == 0) {
+      w.begin(i);
+    } else {
+      const Saved& before = *saved_of(a, k - 1, i, runs);
+      done = before.done;
+      w.resume(before, total_of(sums_of(a, k - 1, i, runs), runs, lane));
     }
-    w.resume(before, total_of(sums_of(a, k - 1, i, runs), runs, lane));
+    if (done) {
+      if (group == 0 && lane == 0) now.done = done;
+    } else {
+      // the walk's last sum is the one that the next token is drawn from
+      const bool whole = w.sound && w.run([] { return -1.0; });
+      if (group == 0) {
+        w.save(now, !w.sound ? -1 : whole ? k + 1 : 0);
+        if (whole || !w.sound) w.put_path(i);
+        if (!w.sound && lane == 0) a.next[i] = -1;
+      }
+    }
+    gone[lane] = w.left.gone;
+    if (lane == 0) {
+      node = done || !w.sound ? -1 : w.node;
+      cut = w.left.cut;
+    }
   }
-  const bool whole = w.sound && w.run([] { return -1.0; });
-  if (w.sound) {                                 // the walk's last sum is the one that the next token is drawn from
-    const double x = scan(w.left.share(r, lane));
-    if (lane == 63) sums_of(a, k, i, runs)[r] = x;
-  }
-  if (r != 0) return;
-  w.save(now, !w.sound ? -1 : whole ? k + 1 : 0);
-  if (whole || !w.sound) w.put_path(i);
-  if (!w.sound && lane == 0) a.next[i] = -1;
+  __syncthreads();
+  if (node < 0 || r >= runs) return;
+  w.at_row(node);
+  w.left.cut = cut;
+  w.left.gone = gone[lane];
+  const double x = scan(w.left.share(r, lane));
+  if (lane == 63) sums_of(a, k, i, runs)[r] = x;
 }
 
 // What the launches above left to do: the token of each entry, by one wave, and
@@ -422,8 +437,8 @@ __global__ __launch_bounds__(64 * kWaves) void verify_kernel(VerifyArgs a) {
 // for sums, 17.2, 19.9 and 22.9 with one to three, of which the host takes 2.6 each).
 // Larger ones are split over the chip, by a launch for each sum; one that no entry
 // needs takes 2-4 us.  The host does not see the trees: a chain asks for one sum,
-// trees of 11 nodes for up to four (64 of them, 131072 tokens: 73 us without, 69, 60,
-// 45, 43 and 46 with one to five).  Without a draft's row there is one sum.
+// trees of 11 nodes for up to four (64 of them, 131072 tokens: 66 us without, 63, 55,
+// 40, 38 and 42 with one to five).  Without a draft's row there is one sum.
 int verify_rounds(int32_t seqs, int64_t nodes, int32_t vocab, bool draft) {
   if ((draft ? 2 : 1) * (int64_t)vocab <= 1 << 17 || seqs == 0) return 0;
   const int64_t rounds = draft ? (nodes / seqs - 3) / 2 : 1;
@@ -431,10 +446,12 @@ int verify_rounds(int32_t seqs, int64_t nodes, int32_t vocab, bool draft) {
 }
 
 hipError_t launch_verify(const VerifyArgs& a, hipStream_t s) {
-  const int64_t blocks = (int64_t)a.seqs * ((a.vocab + 4 * kRun - 1) / (4 * kRun));
-  if (!fits_launch(a.seqs, 64 * dev::kWaves) || (a.rounds && !fits_launch(blocks, 256))) return hipErrorInvalidConfiguration;
+  constexpr int per = dev::kSumWaves * kRun;
+  const int64_t blocks = (int64_t)a.seqs * ((a.vocab + per - 1) / per);
+  if (!fits_launch(a.seqs, 64 * dev::kWaves) || (a.rounds && !fits_launch(blocks, 64 * dev::kSumWaves)))
+    return hipErrorInvalidConfiguration;
   for (int k = 0; k < a.rounds; ++k) {
-    hipLaunchKernelGGL(dev::sum_kernel, dim3((unsigned)blocks), dim3(256), 0, s, a, k);
+    hipLaunchKernelGGL(dev::sum_kernel, dim3((unsigned)blocks), dim3(64 * dev::kSumWaves), 0, s, a, k);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
