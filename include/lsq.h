@@ -468,13 +468,10 @@ lsq_status lsq_state_load_slots(lsq_state* dst, const lsq_state* src, int32_t co
  * device: their output rows are filled with NaN.  The step index does not
  * move.  max_nodes also chooses the kernel's size (16, 32 or 64 nodes).
  *
- * The nodes are worked together on the matrix cores, the state read once.  fp32
- * outputs keep fp32 accuracy (magnitudes from 2^-100 to 2^127, as lsq_attend's);
- * the operands of a 16-bit output are held to 16
- * bits: before its one rounding it is off by at most 2^-16 of the sum of its
- * terms' magnitudes (under the delta rule, where those of v and of S k both
- * count at every node above, 2^-13: each of up to four tiles of 16 nodes adds
- * 7 2^-18), beside fp32's own rounding.  |alpha| is at most 1; a
+ * The nodes are worked together on the matrix cores, the state read once.
+ * Operands and sums keep fp32 accuracy for every io type (magnitudes from 2^-100
+ * to 2^127, as lsq_attend's fp32 outputs), and an output is rounded once.
+ * |alpha| is at most 1; a
  * negative one is taken as it stands; under a scalar decay one below 2^-126 in
  * magnitude counts as 0.  An input that is not finite makes outputs NaN or
  * infinite on its node and the nodes behind it, v its own value column alone,

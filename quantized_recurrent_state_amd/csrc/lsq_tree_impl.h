@@ -54,29 +54,30 @@ __device__ __forceinline__ uint64_t path_mask(int parent, int lane, double& x) {
 // the negative ones between; under a diagonal one P and M are summed on the way up
 // from each node, which leaves g_j k_j and g_j q_j for the products with S.
 //
-// Precision: every operand is a sum of bf16 parts and the products of parts
-// i + j < N are added; N = 3 (fp32) for fp32 inputs, N = 2 for 16-bit ones, whose
-// outputs are rounded to 8 or 11 bits and whose states are not written.  With N = 2
-// a part's rounding and the product left out are 2^-18 each: S q lacks 2 2^-18 of its
-// terms, P w 3 2^-18, and a tile's w under the delta rule 7 2^-18 (S k and M w before T).
+// Precision: every operand that is not an input is a sum of three bf16 parts (24 bits)
+// and the products of parts i + j < 3 are added, so that outputs of every type have
+// fp32's accuracy before their one rounding.  (Two parts for the 16-bit types missed up
+// to 2^-16 of the terms where these cancel, and took 35 us instead of 36 for the 64 trees
+// below, 26 instead of 28 for the 32 and 105 instead of 108 for the 256.)
 //
 // What is not finite would reach other paths through the zeros of P, M and T.  A
 // w that is not counts as 0, and the outputs behind its node in its column become
 // NaN; a row of T that is not counts as 0 and spoils all columns so.
 //
 // Bound by the state's bytes where there are many trees (256 of 8 nodes, 32 heads of
-// 128x128 in bf16 with the delta rule: 104 us, 5.6 TB/s of state and rows), by rounds of
+// 128x128 in bf16 with the delta rule: 108 us, 5.4 TB/s of state and rows), by rounds of
 // workgroups whose loads and products take turns where there are few (64 of 6-16
-// nodes: 34-35 us, 4.4 TB/s; 32 of 40-64, 64 heads 128x64, linear write: 25 us).  The loads
+// nodes: 36 us, 4.3 TB/s; 32 of 40-64, 64 heads 128x64, linear write: 28 us).  The loads
 // alone take 107, 31 and 29 us in these workgroups.
 template <int IO, int DK, int DELTA, int DIAG, int NT, int NW>
 struct TreeTile {
   static constexpr int IN = IO == IO_BF16 ? 1 : IO == IO_F16 ? 2 : 3;   // parts of an input
-  static constexpr int NO = IO == IO_F32 ? 3 : 2;                       // parts of what is computed
-  static constexpr int NR = DIAG ? NO : IN;                             // parts of the node rows
+  static constexpr int NO = 3, NR = DIAG ? NO : IN;                     // of what is computed, of the node rows
   static constexpr int N = 16 * NT, W = (N + 31) / 32 * 32;             // nodes; columns of P and M as parts
   // Pitches in elements: node rows, P and M as parts and as fp32, T, rows of the walk.
-  static constexpr int PK = DK + 16, PW = W + 16, PP = N + 4, PT = 20, PR = DK + 4;
+  // (Those of P and M decide how many workgroups a CU holds: with W + 16 the 32 trees
+  // above take 31 us.)
+  static constexpr int PK = DK + 16, PW = W + 8, PP = N + 4, PT = 20, PR = DK + 4;
   static constexpr int EU = IO == IO_F32 ? 4 : 8;                       // elements of a 16-byte unit
   static constexpr int UNITS = (N * DK / EU + 64 * NW - 1) / (64 * NW); // units of q (k) per thread
   static constexpr int ROUNDS = (4 * NT + NW - 1) / NW;                 // nodes a lane group walks up from
@@ -90,17 +91,20 @@ struct TreeTile {
   static constexpr bool STAGED = IO != IO_F32;
   static constexpr int C = 16 * NW, PC = C + 8, VUNITS = (N * C / 8 + 64 * NW - 1) / (64 * NW);
   // LDS, in bytes.  P and M as parts, and the rows of v, take the place of the node
-  // rows once the products with S are done; one tile's have room beside them.
-  static constexpr bool OVERLAY = NT > 1 && !DIAG;
+  // rows once the products with S are done; one tile's have room beside them, and a
+  // diagonal decay's rows of v of two.
+  static constexpr bool OVERLAY = NT > 1 && !DIAG, LATE = OVERLAY || (DIAG && DELTA && NT > 2);
   static constexpr int max2(int x, int y) { return x > y ? x : y; }
   static constexpr int ROWS = 2 * NR * N * PK * (DIAG && !DELTA ? 1 : 2);
-  static constexpr int PARTS = DIAG ? 0 : 2 * NO * N * PW * (MTILES ? 2 : 1);
+  static constexpr int PARTS = DIAG ? 0 : 2 * PW * NO * N * (MTILES ? 2 : 1) - (MTILES ? 32 * PW : 0);
   static constexpr int VROWS = STAGED ? 2 * N * PC : 0;
   static constexpr int RAW = DIAG ? 8 * N * PR : 0;
-  static constexpr int PARTS_AT = OVERLAY ? 0 : ROWS, VROWS_AT = PARTS_AT + (DIAG ? max2(0, RAW - ROWS) : PARTS);
+  static constexpr int PARTS_AT = OVERLAY ? 0 : ROWS, VROWS_AT = LATE && DIAG ? 0 : PARTS_AT + (DIAG ? max2(0, RAW - ROWS) : PARTS);
   static constexpr int P_AT = max2(max2(ROWS, RAW), VROWS_AT + VROWS);  // P in fp32
-  static constexpr int M_AT = P_AT + (DIAG ? 4 * N * PP : 0);           // M in fp32, or its diagonal blocks
-  static constexpr int T_AT = M_AT + (!DELTA ? 0 : DIAG ? 4 * N * PP : 64 * NT * PT);
+  // M in fp32, or its diagonal blocks: behind the node rows, in the place of its parts.
+  static constexpr int M_AT = OVERLAY ? ROWS : P_AT + (DIAG ? 4 * N * PP : 0);
+  static constexpr int M = !DELTA ? 0 : DIAG ? 4 * N * PP : 64 * NT * PT;
+  static constexpr int T_AT = max2(P_AT, M_AT + M);
   static constexpr int BYTES = T_AT + (DELTA ? 2 * NO * N * PT : 0);
 };
 
@@ -152,7 +156,7 @@ __device__ __forceinline__ void tree_head(const TreeArgs& a, char* lds, TreeNode
   __bf16* const ql = reinterpret_cast<__bf16*>(lds);
   __bf16* const kl = ql + NR * kRow;
   __bf16* const pp = reinterpret_cast<__bf16*>(lds + T::PARTS_AT);     // P, then M, as parts
-  __bf16* const mp = pp + NO * kPart;
+  __bf16* const mp = pp + NO * kPart - 16 * PW;                        // M has no first row of tiles
   uint16_t* const vl = reinterpret_cast<uint16_t*>(lds + T::VROWS_AT);
   float* const pl = reinterpret_cast<float*>(lds + T::P_AT);
   float* const ml = reinterpret_cast<float*>(lds + T::M_AT);
@@ -441,7 +445,7 @@ __device__ __forceinline__ void tree_head(const TreeArgs& a, char* lds, TreeNode
         }
       }
     }
-    put_v();
+    if constexpr (!T::LATE) put_v();
     float q[R][EPT], k[DELTA ? R : 1][EPT];
     int at[R];
 #pragma unroll
@@ -557,6 +561,10 @@ __device__ __forceinline__ void tree_head(const TreeArgs& a, char* lds, TreeNode
     __syncthreads();
   } else if constexpr (DELTA) {
     __syncthreads();
+    if constexpr (T::LATE) {
+      put_v();
+      __syncthreads();
+    }
   }
   if (!T::STAGED && row0 >= b.dv) return;
 
