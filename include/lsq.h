@@ -542,7 +542,9 @@ lsq_status lsq_verify_workspace(const lsq_draft_batch* batch, size_t* bytes);
  * is P_i without x_i and T_i+1 = T_i - P_i(x_i).  Where no child is accepted,
  * or the path has depth nodes, the next token is the first y whose cumulative
  * sum of P (of p where the path is full) exceeds uniform_next times its sum;
- * where P is empty, of p; -1 where that is empty too.  All of it is fp64.
+ * where P is empty, of p; -1 where that is empty too.  All of it is fp64.  Of a
+ * node's draft row only its children's tokens count where no child is rejected:
+ * the rows of nodes without children may hold anything.
  * A NaN counts as no probability, and a node whose token lies outside
  * [0, vocab) is passed over.  Out: path, node 0 first, -1 behind its end; its
  * length; next.  An empty tree, one of more than 64 nodes, and one with a

@@ -65,8 +65,9 @@ __device__ __forceinline__ double lane_of(double x, int lane) {
   return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
 
-// What is left of a node's target row: max(p - c q, 0), or p without the tokens
-// that the lanes hold in gone (-1: none) where the drafts have no probabilities.
+// What is left of a node's target row: max(p - c q, 0), p itself where q is null (no
+// child was rejected: c = 0, and q may be anything), or p without the tokens that the
+// lanes hold in gone (-1: none) where the drafts have no probabilities.
 struct Residual {
   const float* p;
   const float* q;
@@ -218,16 +219,18 @@ struct Walk {
     t0 = min(max((int64_t)a.cu[i], (int64_t)0), a.nodes);
   }
 
-  __device__ __forceinline__ void at_row(int j) {
+  __device__ __forceinline__ const float* draft_row() const { return a.draft + (t0 + node) * a.draft_stride; }
+
+  __device__ __forceinline__ void at_row(int j, double cut) {
     node = j;
     left.p = a.target + (t0 + j) * a.target_stride;
-    left.q = a.draft ? a.draft + (t0 + j) * a.draft_stride : nullptr;
+    left.cut = cut;
+    left.q = cut > 0.0 ? draft_row() : nullptr;
     left.vocab = a.vocab;
   }
 
   __device__ __forceinline__ void at_node(int j) {
-    at_row(j);
-    left.cut = 0.0;
+    at_row(j, 0.0);
     left.gone = -1;
     total = rest = 1.0;
     stale = false;
@@ -259,8 +262,8 @@ struct Walk {
     u = s.u[lane], px = s.px[lane], qx = s.qx[lane];
     testable = parent >= 0 && id >= 0;
     len = s.len, took = s.took[lane];
-    at_row(s.node);
-    left.cut = s.cut, left.gone = s.gone[lane];
+    at_row(s.node, s.cut);
+    left.gone = s.gone[lane];
     total = known, rest = s.rest, stale = false;
     kids = s.kids;
   }
@@ -299,6 +302,7 @@ struct Walk {
         at_node(j);
       } else if (a.draft) {
         if (rest > 0.0) left.cut += total / rest;
+        left.q = draft_row();
         if (!a.replacement) rest = fmax(rest - qj, 0.0);
         stale = true;
       } else {
@@ -364,8 +368,7 @@ __global__ __launch_bounds__(64 * kSumWaves) void sum_kernel(VerifyArgs a, int k
   }
   __syncthreads();
   if (node < 0 || r >= runs) return;
-  w.at_row(node);
-  w.left.cut = cut;
+  w.at_row(node, cut);
   w.left.gone = gone[lane];
   const double x = scan(w.left.share(r, lane));
   if (lane == 63) sums_of(a, k, i, runs)[r] = x;
