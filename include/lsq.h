@@ -545,8 +545,8 @@ lsq_status lsq_verify_workspace(const lsq_draft_batch* batch, size_t* bytes);
  * where P is empty, of p; -1 where that is empty too.  All of it is fp64.  Of a
  * node's draft row only its children's tokens count where no child is rejected:
  * the rows of nodes without children may hold anything.
- * A NaN counts as no probability, and a node whose token lies outside
- * [0, vocab) is passed over.  Out: path, node 0 first, -1 behind its end; its
+ * A NaN or a negative number counts as 0 in either row, and a node whose token
+ * lies outside [0, vocab) is passed over.  Out: path, node 0 first, -1 behind its end; its
  * length; next.  An empty tree, one of more than 64 nodes, and one with a
  * parent outside [-1, j) get the length 0, next -1 and a path of -1; offsets
  * are clamped to [0, nodes].  The workspace is device memory, 16-byte aligned,

@@ -76,7 +76,7 @@ struct Residual {
   int vocab;
 
   __device__ __forceinline__ double of(float px, float qx) const {
-    return fmax(q ? (double)px - cut * (double)qx : (double)px, 0.0);   // a NaN counts as nothing
+    return fmax(q ? (double)px - cut * (double)fmaxf(qx, 0.f) : (double)px, 0.0);   // a NaN counts as nothing
   }
 
   // Four elements from e on, nothing behind the row; any: some token in gone
@@ -249,7 +249,7 @@ struct Walk {
     px = 0.f, qx = 1.f;
     if (testable) {
       px = a.target[(t0 + parent) * a.target_stride + id];
-      if (a.draft) qx = a.draft[(t0 + parent) * a.draft_stride + id];
+      if (a.draft) qx = fmaxf(a.draft[(t0 + parent) * a.draft_stride + id], 0.f);
     }
     len = 1, took = lane == 0 ? 0 : -1;
     at_node(0);

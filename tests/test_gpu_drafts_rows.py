@@ -25,3 +25,29 @@ def test_draft_rows_behind_the_walk_do_not_count(drawn, vocab, bad):
             row[token[i]] = bad                          # where it would show, and in half of the row
             row[::2] = bad
         assert run_verify(d, drawn, depth) == (path, lengths, token)
+
+
+@pytest.mark.parametrize("drawn", ["with", "without"])
+@pytest.mark.parametrize("vocab", [300, 5000, 70001, 140000])
+@pytest.mark.parametrize("bad", [NAN, -0.25])
+def test_what_is_no_probability_in_a_draft_row_counts_as_zero(drawn, vocab, bad):
+    """At a child's token and elsewhere: as if it were 0 there.  A child without a probability in either row
+    is rejected and does not disturb its later siblings."""
+    gone = set()
+    for seed, target in ((1, 0.0), (2, 0.0), (3, None), (4, None)):
+        d = drafts([6, 9, 4], vocab, "star", seed, drawn, error=2.5)
+        d["uniform"] = 0.75 + d["uniform"] / 4           # most children are rejected
+        clean = {**d, "draft": d["draft"].clone()}
+        d["draft"] = d["draft"].clone()
+        for i, a in enumerate(d["cu"][:-1]):
+            x = int(d["ids"][a + 1])                     # the first child's token
+            at = torch.cat((torch.arange(2, vocab, 7), torch.tensor([x])))
+            at = at[~torch.isin(at, d["ids"][a + 2:d["cu"][i + 1]])]
+            clean["draft"][a, at] = 0.0
+            d["draft"][a, at] = bad
+            if target is not None:
+                d["target"][a, x] = target
+        got = check_verify(clean, drawn)
+        assert run_verify(d, drawn) == got
+        gone |= {n for n, c in zip(got[1], (6, 9, 4)) if n < c}
+    assert gone
