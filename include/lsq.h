@@ -535,7 +535,9 @@ lsq_status lsq_verify_workspace(const lsq_draft_batch* batch, size_t* bytes);
  * and draft row.  P_1 = p, T_1 = Q_1 = 1, c_1 = 0:
  *   x_i is accepted if uniform T_i q(x_i) < P_i(x_i) Q_i, and the walk goes on
  *   there; otherwise c_i+1 = c_i + T_i / Q_i, P_i+1 = max(p - c_i+1 q, 0), T_i+1 is
- *   its sum, and Q_i+1 is 1, or without replacement 1 - q(x_1) - ... - q(x_i).
+ *   its sum, and Q_i+1 is 1, or without replacement 1 - q(x_1) - ... - q(x_i) and,
+ *   where that is below 1/16, the sum of q over the tokens not tried (in a small
+ *   difference a row's own rounding would count).
  * (P / T is what the residual rule of rejection sampling leaves for the next
  * sibling, so that every accepted or drawn token has the target's distribution.)
  * Without draft probabilities x_i is accepted if uniform T_i < P_i(x_i), else P_i+1

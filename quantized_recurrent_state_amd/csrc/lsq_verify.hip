@@ -9,6 +9,9 @@
 // (a rejected token has nothing left, P_i+1(x_i) = 0, so the q of a draw without
 // replacement may keep the tokens drawn before), and T_i+1 is its sum.  One number c
 // stands for all the rejections at a node, and a residual is never stored.
+// Without replacement Q_i+1 is 1 - q(x_1) - ... - q(x_i).  How far a row's sum is from one
+// (1e-7 for an fp32 softmax) counts there Q's inverse times, so below 1/16 it is the sum of
+// q over the tokens not tried: one more pass over the row, by the entry's own workgroup.
 // Sums and products are fp64: tokens are whole numbers, and a cumulative sum or
 // a ratio next to its border decides which.
 //
@@ -25,6 +28,7 @@ namespace lsq {
 namespace dev {
 
 constexpr int kMaxRuns = kMaxVocab / kRun;       // of a row; a wave sums a run
+constexpr double kLittle = 1.0 / 16;             // a smaller Q is summed
 constexpr int kSumWaves = 4;                     // of sum_kernel (8: 39 us as below instead of 38, 16: 40)
 
 // Four floats at any 4-byte address.
@@ -193,7 +197,8 @@ __device__ __forceinline__ int draw(const Residual& left, const double* sums, in
 
 // An entry's walk between two launches.
 struct Saved {
-  int done;                                      // the launch it ended in, counted from 1; 0: not yet, -1: a refused entry
+  int done;                                      // the launch it ended in, counted from 1; 0: not yet, -1: a refused
+                                                 // entry, -2 - k: it stopped in launch k and is left to verify_kernel
   int node, len, parent[kMaxNodes], id[kMaxNodes], took[kMaxNodes], gone[kMaxNodes];
   float u[kMaxNodes], px[kMaxNodes], qx[kMaxNodes];
   double cut, rest;
@@ -279,16 +284,26 @@ struct Walk {
     }
   }
 
-  // Tests children until none is left or the path is full; sum() gives the sum of
-  // what is left where a test needs it, or a negative number: then it stops there
-  // and returns false.  In the end `left` is what the next token is drawn from.
+  // Whether the next test needs Q as a sum.
+  __device__ __forceinline__ bool wants_rest() const { return stale && a.draft && !a.replacement && rest < kLittle; }
+
+  // The node's draft row without the children tested so far.
+  __device__ __forceinline__ Residual untried() const {
+    const bool tested = testable && parent == node && !(kids >> lane & 1);
+    return Residual{draft_row(), nullptr, 0.0, tested ? id : -1, a.vocab};
+  }
+
+  // Tests children until none is left or the path is full; sum(x) gives the sum of
+  // x where a test needs it, or a negative number: then it stops there and returns
+  // false.  In the end `left` is what the next token is drawn from.
   template <typename Sum>
   __device__ __forceinline__ bool run(Sum sum) {
     while (kids && len < a.depth) {
-      if (stale) {
-        total = sum();
-        if (total < 0.0) return false;
-        stale = false;
+      for (bool q = wants_rest(); stale; q = false) {   // Q before T
+        const double x = sum(q ? untried() : left);
+        if (x < 0.0) return false;
+        (q ? rest : total) = x;
+        stale = q;
       }
       const int j = __builtin_ctzll(kids);
       kids &= kids - 1;
@@ -353,9 +368,10 @@ __global__ __launch_bounds__(64 * kSumWaves) void sum_kernel(VerifyArgs a, int k
       if (group == 0 && lane == 0) now.done = done;
     } else {
       // the walk's last sum is the one that the next token is drawn from
-      const bool whole = w.sound && w.run([] { return -1.0; });
+      const bool whole = w.sound && w.run([](const Residual&) { return -1.0; });
+      if (w.sound && !whole && w.wants_rest()) done = -2 - k;
       if (group == 0) {
-        w.save(now, !w.sound ? -1 : whole ? k + 1 : 0);
+        w.save(now, !w.sound ? -1 : whole ? k + 1 : done);
         if (whole || !w.sound) w.put_path(i);
         if (!w.sound && lane == 0) a.next[i] = -1;
       }
@@ -384,7 +400,7 @@ __global__ __launch_bounds__(64 * kWaves) void verify_kernel(VerifyArgs a) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int runs = (a.vocab + kRun - 1) / kRun, last = a.rounds - 1;
   const int done = a.rounds ? saved_of(a, last, i, runs)->done : 0;
-  if (done < 0 || (done && wave != 0)) return;
+  if (done == -1 || (done > 0 && wave != 0)) return;
   const double* from = sums;
   auto sum_runs = [&](const Residual& left, int first, int step) __attribute__((always_inline)) {
     for (int r = first; r < runs; r += 2 * step) {
@@ -397,27 +413,33 @@ __global__ __launch_bounds__(64 * kWaves) void verify_kernel(VerifyArgs a) {
     }
   };
   Walk w(a, i, lane);
-  if (done) {
+  if (done > 0) {
     from = sums_of(a, done - 1, i, runs);
     w.resume(*saved_of(a, done - 1, i, runs), 0.0);
   } else {
-    if (a.rounds) w.resume(*saved_of(a, last, i, runs), total_of(sums_of(a, last, i, runs), runs, lane));
-    else w.begin(i);
+    if (done < 0) {
+      w.resume(*saved_of(a, -2 - done, i, runs), 0.0);
+      w.stale = true;
+    } else if (a.rounds) {
+      w.resume(*saved_of(a, last, i, runs), total_of(sums_of(a, last, i, runs), runs, lane));
+    } else {
+      w.begin(i);
+    }
     if (!w.sound) {
       if (wave == 0) w.put_path(i);
       if (threadIdx.x == 0) a.next[i] = -1;
       return;
     }
-    auto sum_row = [&]() __attribute__((always_inline)) {
+    auto sum_row = [&](const Residual& x) __attribute__((always_inline)) {
       __syncthreads();
-      sum_runs(w.left, wave, kWaves);
+      sum_runs(x, wave, kWaves);
       __syncthreads();
     };
-    w.run([&]() __attribute__((always_inline)) {
-      sum_row();
+    w.run([&](const Residual& x) __attribute__((always_inline)) {
+      sum_row(x);
       return total_of(sums, runs, lane);
     });
-    sum_row();
+    sum_row(w.left);
     if (wave != 0) return;
     w.put_path(i);
   }

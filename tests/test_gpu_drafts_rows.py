@@ -51,3 +51,69 @@ def test_what_is_no_probability_in_a_draft_row_counts_as_zero(drawn, vocab, bad)
         assert run_verify(d, drawn) == got
         gone |= {n for n, c in zip(got[1], (6, 9, 4)) if n < c}
     assert gone
+
+
+def rest_ref(d, depth):
+    """verify_tree of siblings drawn without replacement, in 64 bits, with Q the draft's mass that is not tried
+    yet wherever 1 - q(x_1) - ... is below 1/16."""
+    paths, lengths, tokens = [], [], []
+    for i, a in enumerate(d["cu"][:-1]):
+        n, path = d["cu"][i + 1] - a, [0]
+        while True:
+            row, tried, c, T, Q, taken = a + path[-1], [], 0.0, 1.0, 1.0, None
+            p, q = d["target"][row].double(), d["draft"][row].double()
+            for j in range(path[-1] + 1, n) if len(path) < depth else ():
+                if d["parents"][a + j] != path[-1]:
+                    continue
+                x = int(d["ids"][a + j])
+                if float(d["uniform"][a + j]) * T * float(q[x]) < max(float(p[x]) - c * float(q[x]), 0.0) * Q:
+                    taken = j
+                    break
+                tried.append(x)
+                c += T / Q
+                T = float((p - c * q).clamp(min=0).sum())
+                Q = Q - float(q[x])
+                if Q < 1.0 / 16:
+                    left = q.clone()
+                    left[tried] = 0.0
+                    Q = float(left.sum())
+            if taken is None:
+                break
+            path.append(taken)
+        cum = (p - c * q).clamp(min=0).cumsum(0)
+        tokens.append(int((cum <= float(d["uniform_next"][i]) * float(cum[-1])).sum()))
+        paths.append(path + [-1] * (depth - len(path)))
+        lengths.append(len(path))
+    return paths, lengths, tokens
+
+
+@pytest.mark.parametrize("vocab", [4099, 32000, 70001, 131073])
+@pytest.mark.parametrize("counts", [[3] * 12, [6] * 8, [9, 12, 3, 17]], ids=str)
+@pytest.mark.parametrize("little", [0.05, 7e-4, 2e-6, 2e-7])
+@pytest.mark.parametrize("scale", [1.0, 1.0 + 3e-5, 1.0 - 3e-5])
+def test_little_left_of_a_draft_without_replacement(vocab, counts, little, scale):
+    """A draft that is nearly certain of its first token, which fails; its later siblings are drawn from the
+    little that is left, of rows that sum to one but for `scale` and their rounding."""
+    for seed in (1, 2):
+        d = drafts(counts, vocab, "star" if seed == 1 else "random", seed, "without", error=2.0)
+        for a, c in zip(d["cu"], counts):
+            d["parents"][a] = -1
+            d["parents"][a + 1:a + c] = [max(0, p) for p in d["parents"][a + 1:a + c]]
+        rest = d["draft"].double()
+        first = torch.zeros(len(rest), dtype=torch.long)
+        used = {}
+        for i, a in enumerate(d["cu"][:-1]):
+            for j in range(1, counts[i]):
+                if a + d["parents"][a + j] not in used:
+                    used[a + d["parents"][a + j]] = True
+                    first[a + d["parents"][a + j]] = int(d["ids"][a + j])
+        at = torch.arange(len(rest))
+        rest[at, first] = 0.0
+        rest *= little / rest.sum(-1, keepdim=True)
+        rest[at, first] = 1.0 - little
+        d["draft"] = (rest * scale).float()
+        d["target"][at, first] = 0.0
+        d["target"] = (d["target"].double() / d["target"].double().sum(-1, keepdim=True)).float()
+        d["uniform"] = 0.9 + d["uniform"] / 10
+        got = run_verify(d, "without", 5)
+        assert got == rest_ref(d, 5)
