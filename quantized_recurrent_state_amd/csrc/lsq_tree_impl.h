@@ -61,8 +61,8 @@ __device__ __forceinline__ uint64_t path_mask(int parent, int lane, double& x) {
 // below, 26 instead of 28 for the 32 and 105 instead of 108 for the 256.)
 //
 // What is not finite would reach other paths through the zeros of P, M and T.  A
-// w that is not counts as 0, and the outputs behind its node in its column become
-// NaN; a row of T that is not counts as 0 and spoils all columns so.
+// w that is not, before or behind T, counts as 0, and the outputs behind its node in its
+// column become NaN; a row of T that is not counts as 0 and spoils all columns so.
 //
 // Bound by the state's bytes where there are many trees (256 of 8 nodes, 32 heads of
 // 128x128 in bf16 with the delta rule: 108 us, 5.4 TB/s of state and rows), by rounds of
@@ -115,6 +115,9 @@ struct TreeNodes {
   uint64_t neg;                                  // nodes with a negative decay
   unsigned long long spoilt;                     // whose row of T is not finite
 };
+
+// What rounds to infinity as a bf16 part, from here on, counts as not finite.
+constexpr float kLargest = 0x1.ffp127f;
 
 template <int N, int NA, int NB>
 __device__ __forceinline__ f32x4 mfma_parts(const bf16x8 (&a)[NA], const bf16x8 (&b)[NB], f32x4 c) {
@@ -315,7 +318,7 @@ __device__ __forceinline__ void tree_head(const TreeArgs& a, char* lds, TreeNode
             if (c + e < r) d = fmaf(y[e], x[c + e], d);
         }
         if (r > 0) x[r] = fmaf(-nl.beta[16 * t + r], d, x[r]);
-        const bool fine = fabsf(x[r]) <= 0x1.fffffep127f;
+        const bool fine = fabsf(x[r]) < kLargest;
         odd |= fine ? 0u : 1u << r;
         x[r] = fine ? x[r] : 0.f;
       }
@@ -585,6 +588,17 @@ __device__ __forceinline__ void tree_head(const TreeArgs& a, char* lds, TreeNode
 
   // ---- w
   uint32_t bad[2] = {};                          // bit 16 (t % 2) + r of word t / 2: w of node 16 t + 4 g + r is not finite
+  auto finite = [&](f32x4 x, int t) {
+    uint32_t odd = 0;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const bool fine = fabsf(x[r]) < kLargest;
+      odd |= fine ? 0u : 1u << r;
+      x[r] = fine ? x[r] : 0.f;
+    }
+    bad[t / 2] |= odd << 16 * (t % 2);
+    return x;
+  };
   bf16x4 w[NT][NO];
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
@@ -612,15 +626,7 @@ __device__ __forceinline__ void tree_head(const TreeArgs& a, char* lds, TreeNode
       x -= y;
     }
     x *= beta;
-    uint32_t odd = 0;
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const bool fine = fabsf(x[r]) <= 0x1.fffffep127f;
-      odd |= fine ? 0u : 1u << r;
-      x[r] = fine ? x[r] : 0.f;
-    }
-    bad[t / 2] |= odd << 16 * (t % 2);
-    split4<NO>(x, w[t]);
+    split4<NO>(finite(x, t), w[t]);
     if constexpr (DELTA) {
       f32x4 y = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -630,7 +636,7 @@ __device__ __forceinline__ void tree_head(const TreeArgs& a, char* lds, TreeNode
         for (int o = NO - 1 - p; o >= 0; --o)
           y = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(__builtin_bit_cast(s16x4, m), __builtin_bit_cast(s16x4, w[t][o]), y, 0, 0, 0);
       }
-      split4<NO>(y, w[t]);
+      split4<NO>(finite(y, t), w[t]);            // T w may overflow where T and w do not
     }
   }
 
