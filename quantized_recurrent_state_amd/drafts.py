@@ -56,8 +56,8 @@ def _probabilities(name, t, shape, dev):
 
 
 def draft_batch(target, tokens, parents, cu_nodes, uniform, uniform_next, draft, replacement, depth):
-    """Checks the tensors of ``verify_tree``; returns (lsq_draft_batch, its workspace's address and
-    bytes, path, lengths, next)."""
+    """Checks the tensors of ``verify_tree``; returns (lsq_draft_batch, its workspace or None, the
+    workspace's bytes, path, lengths, next)."""
     if target.dim() != 2:
         raise ValueError(f"target has shape {tuple(target.shape)}, expected (nodes, vocab)")
     if cu_nodes.dim() != 1 or cu_nodes.shape[0] < 1:
@@ -74,19 +74,20 @@ def draft_batch(target, tokens, parents, cu_nodes, uniform, uniform_next, draft,
     np = _plain("uniform_next", uniform_next, (m,), torch.float32, dev)
     b = _lib.lsq_draft_batch(m, vocab, depth, 1 if replacement else 0, n, ts, ds, tp, dp, ip, pp, cp, up, np,
                              None, None, None)
-    nb = 0
+    nb, ws = 0, None
     if vocab > 65536:                        # smaller rows need no workspace
         need = ctypes.c_size_t()
         status = _lib.load().lsq_verify_workspace(ctypes.byref(b), ctypes.byref(need))
         if status:
             _lib.check(status, "lsq_verify_workspace")
-        nb = need.value // 4                 # whole 8-byte numbers
-    # the workspace, then the outputs
-    buf = torch.empty(nb + m * (depth + 2), dtype=torch.int32, device=target.device)
+        nb = need.value
+        ws = torch.empty(nb, dtype=torch.uint8, device=target.device) if nb else None
+    # the outputs in one piece, apart from the workspace, which does not outlive the call
+    buf = torch.empty(m * (depth + 2), dtype=torch.int32, device=target.device)
     at = buf.data_ptr()
-    b.path, b.lengths, b.next = at + 4 * nb, at + 4 * (nb + m * depth), at + 4 * (nb + m * (depth + 1))
-    _, path, lengths, token = buf.split_with_sizes((nb, m * depth, m, m))
-    return b, at, 4 * nb, path.view(m, depth), lengths, token
+    b.path, b.lengths, b.next = at, at + 4 * m * depth, at + 4 * m * (depth + 1)
+    path, lengths, token = buf.split_with_sizes((m * depth, m, m))
+    return b, ws, nb, path.view(m, depth), lengths, token
 
 
 def verify_tree(target, tokens, parents, cu_nodes, uniform, uniform_next, draft, replacement, depth, stream):
@@ -96,7 +97,7 @@ def verify_tree(target, tokens, parents, cu_nodes, uniform, uniform_next, draft,
     def call(s):
         b, ws, nb, path, lengths, token = draft_batch(target, tokens, parents, cu_nodes, uniform, uniform_next,
                                                       draft, replacement, depth)
-        status = _lib.load().lsq_verify_tree(ctypes.byref(b), ws if nb else None, nb, s)
+        status = _lib.load().lsq_verify_tree(ctypes.byref(b), ws.data_ptr() if nb else None, nb, s)
         if status:
             _lib.check(status, "lsq_verify_tree")
         return path, lengths, token

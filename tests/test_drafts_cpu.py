@@ -226,3 +226,16 @@ def test_a_tree_of_far_rows_is_refused(name):
         assert tree(h, b) == status, stride
         assert accept(h, b) == 5
     lsq.lsq_state_free(h)
+
+
+def test_results_of_verify_do_not_hold_its_workspace():
+    n, m, depth = 5, 3, 7
+    for V in (40, 70_000):
+        good = dict(target=torch.zeros(n, V), tokens=torch.zeros(n, dtype=torch.int32),
+                    parents=torch.zeros(n, dtype=torch.int32), cu_nodes=torch.zeros(m + 1, dtype=torch.int32),
+                    uniform=torch.zeros(n), uniform_next=torch.zeros(m), draft=torch.zeros(n, V), replacement=True, depth=depth)
+        b, ws, nb, *results = drafts.draft_batch(**good)
+        assert (nb > 0) == (V > 65536)
+        for t, address, shape in zip(results, (b.path, b.lengths, b.next), ((m, depth), (m,), (m,))):
+            assert t.dtype == torch.int32 and t.shape == shape and t.data_ptr() == address and t.is_contiguous()
+            assert t.untyped_storage().nbytes() == 4 * m * (depth + 2)
