@@ -10,6 +10,11 @@ from . import _lib
 from .slots import _buffer, _on_device, _plain, token_batch
 
 
+def _i32(x):
+    """x, or the nearest number that a 32-bit argument holds: the library refuses both alike."""
+    return max(-2 ** 31, min(int(x), 2 ** 31 - 1))
+
+
 def step_tree(state, q, k, v, alpha, beta, cu_nodes, parents, slots, fresh, max_nodes, o, stream):
     if cu_nodes is None or parents is None:
         raise ValueError("cu_nodes must hold seqs + 1 offsets, parents one entry per node")
@@ -17,7 +22,7 @@ def step_tree(state, q, k, v, alpha, beta, cu_nodes, parents, slots, fresh, max_
     def call(s):
         b, out = token_batch(state, q, k, v, alpha, beta, cu_nodes, slots, fresh, o)
         pp = _plain("parents", parents, (b.tokens,), torch.int32, out.get_device())
-        most = min(64, b.tokens or 1) if max_nodes is None else int(max_nodes)
+        most = min(64, b.tokens or 1) if max_nodes is None else _i32(max_nodes)
         status = _lib.load().lsq_step_tree(state.handle, ctypes.byref(b), pp, most, s)
         if status:
             _lib.check(status, "lsq_step_tree")
@@ -63,8 +68,8 @@ def draft_batch(target, tokens, parents, cu_nodes, uniform, uniform_next, draft,
     if cu_nodes.dim() != 1 or cu_nodes.shape[0] < 1:
         raise ValueError("cu_nodes must hold seqs + 1 offsets")
     (n, vocab), dev, m, depth = target.shape, target.get_device(), cu_nodes.shape[0] - 1, int(depth)
-    if depth < 1:
-        raise ValueError("depth must be at least 1")
+    if not 1 <= depth < 2 ** 31:
+        raise ValueError("depth must be at least 1, and below 2^31")
     tp, ts = _probabilities("target", target, (n, vocab), dev)
     dp, ds = (None, 0) if draft is None else _probabilities("draft", draft, (n, vocab), dev)
     ip = _plain("tokens", tokens, (n,), torch.int32, dev)
@@ -72,7 +77,7 @@ def draft_batch(target, tokens, parents, cu_nodes, uniform, uniform_next, draft,
     cp = _plain("cu_nodes", cu_nodes, (m + 1,), torch.int32, dev)
     up = _plain("uniform", uniform, (n,), torch.float32, dev)
     np = _plain("uniform_next", uniform_next, (m,), torch.float32, dev)
-    b = _lib.lsq_draft_batch(m, vocab, depth, 1 if replacement else 0, n, ts, ds, tp, dp, ip, pp, cp, up, np,
+    b = _lib.lsq_draft_batch(m, _i32(vocab), depth, 1 if replacement else 0, n, ts, ds, tp, dp, ip, pp, cp, up, np,
                              None, None, None)
     nb, ws = 0, None
     if vocab > 65536:                        # smaller rows need no workspace

@@ -239,3 +239,29 @@ def test_results_of_verify_do_not_hold_its_workspace():
         for t, address, shape in zip(results, (b.path, b.lengths, b.next), ((m, depth), (m,), (m,))):
             assert t.dtype == torch.int32 and t.shape == shape and t.data_ptr() == address and t.is_contiguous()
             assert t.untyped_storage().nbytes() == 4 * m * (depth + 2)
+
+
+def test_numbers_beyond_32_bits_do_not_wrap(monkeypatch):
+    """The binding passes 32-bit numbers: 2^32 + 16 is no 16."""
+    st, n, m, V = _state(), 5, 3, 40
+    st.handle = h = handle(batch=4, heads=4, dk=64, dv=32)
+    monkeypatch.setattr(drafts, "_on_device", lambda index, stream, call: call(0))
+    x = dict(q=torch.zeros(n, 2, 64), k=torch.zeros(n, 2, 64), v=torch.zeros(n, 4, 32), alpha=torch.zeros(n, 4),
+             beta=torch.zeros(n, 4), cu_nodes=torch.zeros(m + 1, dtype=torch.int32), parents=torch.zeros(n, dtype=torch.int32))
+    for most, status in ((65, 2), ((1 << 32) + 16, 2), ((1 << 31) + 16, 2), (0, 1), (-(1 << 32) + 16, 1)):
+        with pytest.raises(lsq.LsqError) as e:
+            st.step_tree(**x, max_nodes=most)
+        assert e.value.status == status
+    lsq.lsq_state_free(h)
+    good = dict(target=torch.zeros(n, V), tokens=torch.zeros(n, dtype=torch.int32),
+                parents=torch.zeros(n, dtype=torch.int32), cu_nodes=torch.zeros(1, dtype=torch.int32),
+                uniform=torch.zeros(n), uniform_next=torch.zeros(0), draft=None, replacement=True)
+    for depth in (1 << 31, (1 << 32) + 7):               # no entries: nothing large is made here
+        with pytest.raises(ValueError):
+            drafts.draft_batch(**good, depth=depth)
+    wide = torch.zeros(0, (1 << 32) + 5)                 # no rows
+    none = {**good, "target": wide, "tokens": torch.zeros(0, dtype=torch.int32), "parents": torch.zeros(0, dtype=torch.int32),
+            "uniform": torch.zeros(0)}
+    with pytest.raises(lsq.LsqError) as e:
+        drafts.draft_batch(**none, depth=7)
+    assert e.value.status == 2
