@@ -419,6 +419,7 @@ __device__ __forceinline__ void tree_head(const TreeArgs& a, char* lds, TreeNode
         const f32x4 d = gram(kl, wave, wave);
         float* m = ml + wave * 16 * PT;
         *reinterpret_cast<f32x4*>(m + lc * PT + 4 * g) = d;
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         invert(wave, m, PT);
       }
     }
