@@ -200,9 +200,11 @@ def verify_tree(target, tokens, parents, cu_nodes, uniform, uniform_next, draft=
     target (and draft) fp32 [nodes, vocab], rows contiguous, row j the distribution of node j's
     children; tokens and parents int32 [nodes]; cu_nodes int32 [seqs + 1]; uniform fp32 [nodes] and
     uniform_next fp32 [seqs], in [0, 1).  draft None: the drafts have no probabilities.
-    replacement False: siblings were drawn without replacement.  Returns (path [seqs, depth],
-    lengths [seqs], next [seqs]), int32: the accepted nodes, node 0 first and -1 behind the last,
-    their number, and the token drawn behind them; the first two are ``accept_path``'s arguments."""
+    replacement False: siblings were drawn without replacement.  Of a draft row only the children's
+    tokens count where none of them is rejected; rows of nodes without children may hold anything.
+    Returns (path [seqs, depth], lengths [seqs], next [seqs]), int32: the accepted nodes, node 0
+    first and -1 behind the last, their number, and the token drawn behind them; the first two are
+    ``accept_path``'s arguments (for a depth of at most 64, which no tree exceeds)."""
     return _drafts().verify_tree(target, tokens, parents, cu_nodes, uniform, uniform_next, draft,
                                  replacement, depth, stream)
 
@@ -414,7 +416,8 @@ class LsqState:
         The tensors of ``attend`` with one row per node (strides below 2^31 elements); cu_nodes int32
         [seqs + 1] the trees' offsets; parents int32 [nodes], within the tree: -1 or an earlier node;
         max_nodes (at most 64, the default unless there are fewer rows) bounds a tree's nodes: it
-        chooses the kernel's size, so a program that knows a smaller bound gives it.  Returns o
+        chooses the kernel's size, so a program that knows a smaller bound gives it (the default
+        takes up to a sixth longer).  Returns o
         [nodes, heads, dv] in q's type."""
         return _drafts().step_tree(self, q, k, v, alpha, beta, cu_nodes, parents, slots, fresh, max_nodes,
                                    o, stream)

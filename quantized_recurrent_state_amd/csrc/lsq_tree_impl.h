@@ -67,8 +67,8 @@ __device__ __forceinline__ uint64_t path_mask(int parent, int lane, double& x) {
 // Bound by the state's bytes where there are many trees (256 of 8 nodes, 32 heads of
 // 128x128 in bf16 with the delta rule: 108 us, 5.4 TB/s of state and rows), by rounds of
 // workgroups whose loads and products take turns where there are few (64 of 6-16
-// nodes: 36 us, 4.3 TB/s; 32 of 40-64, 64 heads 128x64, linear write: 28 us).  The loads
-// alone take 107, 31 and 29 us in these workgroups.
+// nodes: 36 us, 4.3 TB/s; 32 of 40-64, 64 heads 128x64, linear write: 27-28 us).  The loads
+// and stores alone took 107, 31 and 29 us in these workgroups.
 template <int IO, int DK, int DELTA, int DIAG, int NT, int NW>
 struct TreeTile {
   static constexpr int IN = IO == IO_BF16 ? 1 : IO == IO_F16 ? 2 : 3;   // parts of an input
@@ -717,8 +717,9 @@ struct TreeLds {
   static constexpr int BYTES = T<1>::max2(T<1>::max2(T<1>::BYTES, T<MT >= 2 ? 2 : 1>::BYTES),
                                           T<1>::max2(T<MT >= 3 ? 3 : 1>::BYTES, T<MT >= 4 ? 4 : 1>::BYTES));
   // Waves of a SIMD: as many workgroups as LDS holds, and no more than leave the
-  // registers that a wave needs (256 trees of 8 nodes as above: six waves 104 us,
-  // five, which is two workgroups, 130; at six, the wave that makes T spills a few).
+  // registers that a wave needs (256 trees of 8 nodes as above: six waves 108 us,
+  // five, which is two workgroups, 124; at six, the wave that makes T spills three.
+  // The caps of the other instances follow this one and are not measured).
   static constexpr int HELD = 160 * 1024 / (BYTES + (int)sizeof(TreeNodes)) * NW / 4;
   static constexpr int FEWER = IO == IO_BF16 ? 0 : 1;    // parts take registers too
   static constexpr int MOST = DK == 128 ? (MT == 1 ? 6 : 5) - FEWER : (MT == 1 ? 7 : 6) - FEWER;
@@ -773,10 +774,10 @@ __global__ __launch_bounds__(64 * NW, (TreeLds<IO, DK, DELTA, DIAG, MT, NW>::WAV
 }  // namespace dev
 
 // Eight waves where there are more than 64 value columns, so that P, M and T are made
-// once for up to 128; four otherwise.  (Four waves with 32 columns each take the
-// same for large batches, 34 and 107 us as above, and longer for small ones: 9 trees
-// of 1-37 nodes, 16 heads 64x80 in binary16 14 us instead of 12, 24 of 9-25, 16 heads
-// 128x128 in fp32 with a diagonal decay 17 instead of 16.)
+// once for up to 128; four otherwise.  (Four waves with 32 columns each, tried with
+// operands of two parts, took the same for large batches and longer for small ones: 9
+// trees of 1-37 nodes, 16 heads 64x80 in binary16 14 us instead of 12, 24 of 9-25, 16
+// heads 128x128 in fp32 with a diagonal decay 17 instead of 16.)
 template <int IO, int DK, int DELTA, int DIAG>
 hipError_t launch_tree_instance(const TreeArgs& a, hipStream_t s) {
   auto launch = [&](auto kernel, int waves) {

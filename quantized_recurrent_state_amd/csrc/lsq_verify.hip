@@ -16,8 +16,8 @@
 // a ratio next to its border decides which.
 //
 // Bound by dependent reads: the offsets, the trees, the tokens' probabilities, then a
-// row for each sum, each behind the one before (a chain of five nodes, 65536 tokens: 12
-// us; 64 trees of 6-16, 131072 tokens: 15-17 us for the first sums, 5-9 for each later
+// row for each sum, each behind the one before (a chain of five nodes, 65536 tokens: 12-13
+// us; 64 trees of 6-16, 131072 tokens: 11-16 us for the first sums, 3-8 for each later
 // launch, 5 for the draw).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -29,7 +29,7 @@ namespace dev {
 
 constexpr int kMaxRuns = kMaxVocab / kRun;       // of a row; a wave sums a run
 constexpr double kLittle = 1.0 / 16;             // a smaller Q is summed
-constexpr int kSumWaves = 4;                     // of sum_kernel (8: 39 us as below instead of 38, 16: 40)
+constexpr int kSumWaves = 4;                     // of sum_kernel (8: 35 us as below instead of 34, 16: 36)
 
 // Four floats at any 4-byte address.
 struct Four {
@@ -458,12 +458,14 @@ __global__ __launch_bounds__(64 * kWaves) void verify_kernel(VerifyArgs a) {
 }  // namespace dev
 
 // An entry's own workgroup reads 60-110 GB/s: rows of 512 KiB and less are best left
-// to it (one chain of five nodes, 65536 tokens: 14.3 us per call without launches
-// for sums, 17.2, 19.9 and 22.9 with one to three, of which the host takes 2.6 each).
+// to it (one chain of five nodes, 65540 tokens: 13.6 us per call without launches
+// for sums, 17.2, 19.9 and 22.4 with one to three, of which the host takes 2.6 each).
 // Larger ones are split over the chip, by a launch for each sum; one that no entry
 // needs takes 2-4 us.  The host does not see the trees: a chain asks for one sum,
-// trees of 11 nodes for up to four (64 of them, 131072 tokens: 66 us without, 63, 55,
-// 40, 38 and 42 with one to five).  Without a draft's row there is one sum.
+// trees of 11 nodes for up to four (64 of them, 131072 tokens: 63 us without, 57, 47,
+// 33, 34 and 37 with one to five).  Without a draft's row there is one sum.  Many
+// rejected siblings of one node are slow either way, a sum behind the other (64 stars
+// of 64 nodes, 65540 tokens: 569 us without launches, 556 with five).
 int verify_rounds(int32_t seqs, int64_t nodes, int32_t vocab, bool draft) {
   if ((draft ? 2 : 1) * (int64_t)vocab <= 1 << 17 || seqs == 0) return 0;
   const int64_t rounds = draft ? (nodes / seqs - 3) / 2 : 1;
