@@ -2,7 +2,8 @@
 import pytest
 import torch
 
-from tests.test_gpu_drafts import check_verify, drafts, run_verify
+import quantized_recurrent_state_amd as lsq
+from tests.test_gpu_drafts import DEV, check_verify, drafts, i32, run_verify
 
 pytestmark = pytest.mark.gpu
 NAN, INF = float("nan"), float("inf")
@@ -87,6 +88,27 @@ def rest_ref(d, depth):
     return paths, lengths, tokens
 
 
+def nearly_certain(d, little, scale=1.0):
+    """Draft rows that leave `little` to all tokens but the first child's, which the target never has."""
+    rest = d["draft"].double()
+    first = torch.zeros(len(rest), dtype=torch.long)
+    used = set()
+    for a, b in zip(d["cu"], d["cu"][1:]):
+        for j in range(a + 1, b):
+            row = a + d["parents"][j]
+            if row not in used:
+                used.add(row)
+                first[row] = int(d["ids"][j])
+    at = torch.arange(len(rest))
+    rest[at, first] = 0.0
+    rest *= little / rest.sum(-1, keepdim=True)
+    rest[at, first] = 1.0 - little
+    d["draft"] = (rest * scale).float()
+    d["target"][at, first] = 0.0
+    d["target"] = (d["target"].double() / d["target"].double().sum(-1, keepdim=True)).float()
+    d["uniform"] = 0.9 + d["uniform"] / 10
+
+
 @pytest.mark.parametrize("vocab", [4099, 32000, 70001, 131073])
 @pytest.mark.parametrize("counts", [[3] * 12, [6] * 8, [9, 12, 3, 17]], ids=str)
 @pytest.mark.parametrize("little", [0.05, 7e-4, 2e-6, 2e-7])
@@ -99,21 +121,44 @@ def test_little_left_of_a_draft_without_replacement(vocab, counts, little, scale
         for a, c in zip(d["cu"], counts):
             d["parents"][a] = -1
             d["parents"][a + 1:a + c] = [max(0, p) for p in d["parents"][a + 1:a + c]]
-        rest = d["draft"].double()
-        first = torch.zeros(len(rest), dtype=torch.long)
-        used = {}
-        for i, a in enumerate(d["cu"][:-1]):
-            for j in range(1, counts[i]):
-                if a + d["parents"][a + j] not in used:
-                    used[a + d["parents"][a + j]] = True
-                    first[a + d["parents"][a + j]] = int(d["ids"][a + j])
-        at = torch.arange(len(rest))
-        rest[at, first] = 0.0
-        rest *= little / rest.sum(-1, keepdim=True)
-        rest[at, first] = 1.0 - little
-        d["draft"] = (rest * scale).float()
-        d["target"][at, first] = 0.0
-        d["target"] = (d["target"].double() / d["target"].double().sum(-1, keepdim=True)).float()
-        d["uniform"] = 0.9 + d["uniform"] / 10
+        nearly_certain(d, little, scale)
         got = run_verify(d, "without", 5)
         assert got == rest_ref(d, 5)
+
+
+@pytest.mark.parametrize("vocab", [32000, 70001])
+def test_a_replayed_graph_with_and_without_little_left(vocab):
+    counts = [9, 12, 3, 17]
+
+    def batch(seed, little):
+        d = drafts(counts, vocab, "star", seed, "without", error=2.0)
+        if little:
+            nearly_certain(d, little)
+        return d
+
+    d = batch(1, 0)
+    names = ("target", "draft", "ids", "uniform", "uniform_next")
+    rows = {n: d[n].to(DEV) for n in names}
+    tree, cu = i32(*d["parents"]), i32(*d["cu"])
+
+    def run():
+        return lsq.verify_tree(rows["target"], rows["ids"], tree, cu, rows["uniform"], rows["uniform_next"],
+                               draft=rows["draft"], replacement=False, depth=5)
+
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        run()
+    torch.cuda.current_stream().wait_stream(stream)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = run()
+    for seed, little in ((2, 2e-6), (3, 0), (4, 7e-4), (5, 0), (6, 0.05)):
+        d = batch(seed, little)
+        for n in names:
+            rows[n].copy_(d[n])
+        g.replay()
+        torch.cuda.synchronize()
+        got = tuple(t.tolist() for t in out)
+        assert got == rest_ref(d, 5)
+        assert got == tuple(t.tolist() for t in run())
